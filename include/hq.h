@@ -319,6 +319,111 @@ HQ_API hq_status_t hq_quantize_act(int32_t act_type, const void* x, int64_t M, i
                                    void* out_data, void* out_scale, float* out_global, void* workspace,
                                    size_t ws_bytes, hq_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Paged key-value cache: what a decoder layer does between the fused QKV projection and the output projection.
+ *
+ * The cache keeps the keys and values of `num_heads` key-value heads in pages of `page_size` tokens, one pool per
+ * side, laid out [num_pages, num_heads, page_size, head_dim].  A token's place is its slot, page id * page_size +
+ * offset; a sequence owns the pages its row of a page table names, in order.  Three operators share the layout:
+ * hq_kv_write (norm, rotation, quantised append), hq_kv_read and hq_paged_attention (one new token per sequence).
+ *
+ *   HQ_KV_BF16   values bf16
+ *   HQ_KV_E4M3   e4m3 codes, one fp32 scale per (token, head): value = code * scale; the scale is absmax / 448
+ *   HQ_KV_NVFP4  e2m1 codes, two per byte, low nibble = even dim; one ue4m3 scale per 16 dims; fp32 global scale g per
+ *                side: value = code * (scale * g), scale = e4m3(absmax_16 / (6 g)).  g is the caller's: a calibrated
+ *                largest magnitude / 2688; larger values saturate.
+ *
+ * Indices that only the device sees (page ids, slots, positions, lengths) are checked by the kernels.  One outside its
+ * range is never followed: what depends on it is left out as described at each call, and HQ_ERR_INVALID_ARG is
+ * recorded in the workspace status (hq_last_device_status). */
+enum { HQ_KV_BF16 = 1, HQ_KV_E4M3 = 2, HQ_KV_NVFP4 = 3 };
+
+typedef struct {
+  int32_t kind;      /* HQ_KV_* */
+  int32_t page_size; /* tokens per page, a multiple of 16, at most 1024 */
+  int32_t num_heads; /* key-value heads, 1 .. 1024 */
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int64_t num_pages; /* pages of each pool, 1 .. 2^31 - 1 */
+} hq_kv_format_t;
+
+/* The pools (device pointers, 16-byte aligned).  k, v: [num_pages][num_heads][page_size] rows of 2 * head_dim (BF16),
+ * head_dim (E4M3) or head_dim / 2 (NVFP4) bytes.  k_scale, v_scale: fp32 [num_pages][num_heads][page_size] (E4M3),
+ * ue4m3 [num_pages][num_heads][page_size][head_dim / 16] (NVFP4), else NULL.  k_global, v_global: fp32 [1] each
+ * (NVFP4), else NULL. */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  const float* k_global;
+  const float* v_global;
+} hq_kv_cache_t;
+
+/* Rows of one hq_kv_write call: the fused projection's output and what turns it into queries and cache rows. */
+typedef struct {
+  const void* qkv;         /* bf16 [T] rows of (num_q_heads + 2 num_heads) * head_dim: query, key, value heads */
+  int64_t row_stride;      /* elements from one row to the next, a multiple of 8, at least the row */
+  int64_t T;               /* rows (tokens), >= 0 */
+  int32_t num_q_heads;     /* a multiple of the format's num_heads */
+  int32_t rotary_dim;      /* leading dims of each head that are rotated: 0 (none) or a multiple of 16 up to head_dim */
+  int32_t interleaved;     /* 0: dim i pairs with i + rotary_dim / 2; 1: dim 2i pairs with 2i + 1 */
+  float eps;               /* of the norms, >= 0 */
+  const void* q_norm;      /* bf16 [head_dim] weight of the query heads' RMS norm, or NULL: no norm */
+  const void* k_norm;      /* the same for the key heads */
+  const float* cos_sin;    /* fp32 [num_positions][rotary_dim]: cosines of the rotary_dim / 2 angles, then sines */
+  int64_t num_positions;   /* rows of cos_sin */
+  const int32_t* positions; /* int32 [T], used when rotary_dim > 0 */
+  const int64_t* slots;    /* int64 [T]: where the token's key and value go; negative = not cached (padding) */
+  void* q_out;             /* bf16 [T][num_q_heads][head_dim] */
+} hq_kv_rows_t;
+
+/* Bytes of the workspace of the calls below: hq_kv_write and hq_kv_read need only the status header (pass batch = 0),
+ * hq_paged_attention the partial results of `batch` sequences with num_q_heads query heads on the current device.
+ * Zero it once with hq_workspace_init; calls leave it reusable.  One workspace serves one stream at a time, and none is
+ * shared with the GEMM calls above.  Returns 0 for an invalid format or size. */
+HQ_API size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, int32_t num_q_heads);
+
+/* Norm, rotation and quantised append.  Per query and key head x of a row, in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * w             (where a norm weight is given)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)       for the rotated pairs, angles of the row's position
+ * query heads are rounded once to bf16 into q_out; key heads, and value heads as they are, go to the row's slot,
+ * rounded once to the cache's format (nearest even, saturating; a scale of zero gives zero codes, and an e2m1 zero has
+ * no sign).  A row whose position is outside [0, num_positions) is skipped whole, a row whose slot is past the pools
+ * is not cached; both record HQ_ERR_INVALID_ARG.  Two rows of one call must not name one slot.  One kernel. */
+HQ_API hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* rows,
+                               void* workspace, size_t ws_bytes, hq_stream_t stream);
+
+/* Cached tokens back as contiguous bf16 rows (values as the cache holds them, rounded to nearest even).
+ *   page_table  int32 [B][table_stride]: sequence b's page ids; entries past its last page are not read
+ *   starts      int64 [B + 1], ascending: sequence b's tokens go to rows starts[b] .. starts[b + 1] - 1
+ *   first       int32 [B]: index in its sequence of the first token that is read, or NULL for 0
+ *   total       rows of k_out and v_out, bf16 [total][num_heads][head_dim]
+ * Rows that no sequence covers, and tokens whose page is past the table's row or the pools, are left unwritten; the
+ * latter, and a sequence that ends past `total`, record HQ_ERR_INVALID_ARG.  One kernel. */
+HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const int32_t* page_table,
+                              int64_t table_stride, const int64_t* starts, const int32_t* first, int64_t B,
+                              int64_t total, void* k_out, void* v_out, void* workspace, size_t ws_bytes,
+                              hq_stream_t stream);
+
+/* Attention of one new token per sequence over its cached tokens.  Query head h reads key-value head
+ * h / (num_q_heads / num_heads).  With n = lens[b], for the tokens j in [max(0, n - window), n):
+ *   s_j = scale * (q . k_j), or softcap * tanh(scale * (q . k_j) / softcap) when softcap > 0
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
+ * A sequence of length 0 gives out = 0 and lse = -inf.
+ *   q           bf16 [B][num_q_heads][head_dim]; the new token's own key and value are already in the cache
+ *   page_table  int32 [B][table_stride]; entries past the sequence's last page are not read
+ *   lens        int32 [B], 0 <= lens[b] <= table_stride * page_size
+ *   window      tokens that are seen, 0 = all of them
+ *   out         bf16 [B][num_q_heads][head_dim];  lse  fp32 [B][num_q_heads] (natural logarithm) or NULL
+ * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) are rounded to the
+ * values' 16-bit type before they multiply them.  A length outside its range is taken as the nearest end of it, and
+ * tokens on a page outside the pools are left out; both record HQ_ERR_INVALID_ARG.  Results do not depend on timing:
+ * the length is split by a fixed rule and the parts are joined in order.  One kernel. */
+HQ_API hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const void* q,
+                                      int32_t num_q_heads, const int32_t* page_table, int64_t table_stride,
+                                      const int32_t* lens, int64_t B, float scale, int64_t window, float softcap,
+                                      void* out, float* lse, void* workspace, size_t ws_bytes, hq_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 HQ_API const char* hq_status_string(hq_status_t status);
 

@@ -30,11 +30,13 @@ HQ_W_INT4_SYM, HQ_W_UINT4_ZP, HQ_W_NVFP4, HQ_W_MXFP4 = 1, 2, 3, 4
 HQ_W_INT8_SYM, HQ_W_UINT2_ZP, HQ_W_MXINT4, HQ_W_E4M3, HQ_W_UINT1_ZP, HQ_W_UINT3_ZP = 5, 6, 7, 8, 9, 10
 HQ_S_BF16, HQ_S_UE4M3, HQ_S_UE8M0 = 1, 2, 3
 HQ_A_BF16, HQ_A_E4M3_TOKEN, HQ_A_NVFP4, HQ_A_MXFP8, HQ_A_MXFP4 = 1, 2, 3, 4, 5
+HQ_KV_BF16, HQ_KV_E4M3, HQ_KV_NVFP4 = 1, 2, 3
 
 EXPORTS = ["hq_packed_bytes", "hq_pack_weights", "hq_unpack_weights", "hq_workspace_bytes", "hq_workspace_init",
            "hq_gemm", "hq_moe_gemm", "hq_last_device_status", "hq_status_string", "hq_gemm_static_scratch",
            "hq_kernels_per_call", "hq_launch_plan", "hq_quantize_act_workspace_bytes", "hq_quantize_act",
-           "hq_moe_combine_workspace_bytes", "hq_moe_gemm_combine", "hq_swiglu", "hq_set_wait_limit_ns"]
+           "hq_moe_combine_workspace_bytes", "hq_moe_gemm_combine", "hq_swiglu", "hq_set_wait_limit_ns",
+           "hq_kv_workspace_bytes", "hq_kv_write", "hq_kv_read", "hq_paged_attention"]
 
 
 class Format(ctypes.Structure):
@@ -47,9 +49,28 @@ class Act(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("global_scale", ctypes.c_void_p)]
 
 
+class KVFormat(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int64)]
+
+
+class KVPools(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_global", ctypes.c_void_p), ("v_global", ctypes.c_void_p)]
+
+
+class KVRows(ctypes.Structure):
+    _fields_ = [("qkv", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("T", ctypes.c_int64),
+                ("num_q_heads", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("q_out", ctypes.c_void_p)]
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _F = ctypes.POINTER(Format)
 _A = ctypes.POINTER(Act)
+_KF, _KP, _f32 = ctypes.POINTER(KVFormat), ctypes.POINTER(KVPools), ctypes.c_float
 _lib.hq_packed_bytes.argtypes = [_F]
 _lib.hq_packed_bytes.restype = _sz
 _lib.hq_pack_weights.argtypes = [_F, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -84,6 +105,15 @@ _lib.hq_swiglu.argtypes = [_vp, _i64, _i64, _vp, _vp]
 _lib.hq_swiglu.restype = ctypes.c_int
 _lib.hq_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.hq_set_wait_limit_ns.restype = None
+_lib.hq_kv_workspace_bytes.argtypes = [_KF, _i64, _i32]
+_lib.hq_kv_workspace_bytes.restype = _sz
+_lib.hq_kv_write.argtypes = [_KF, _KP, ctypes.POINTER(KVRows), _vp, _sz, _vp]
+_lib.hq_kv_write.restype = ctypes.c_int
+_lib.hq_kv_read.argtypes = [_KF, _KP, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.hq_kv_read.restype = ctypes.c_int
+_lib.hq_paged_attention.argtypes = [_KF, _KP, _vp, _i32, _vp, _i64, _vp, _i64, _f32, _i64, _f32, _vp, _vp, _vp, _sz,
+                                    _vp]
+_lib.hq_paged_attention.restype = ctypes.c_int
 _lib.hq_status_string.argtypes = [ctypes.c_int]
 _lib.hq_status_string.restype = ctypes.c_char_p
 
@@ -133,6 +163,8 @@ _SCALE_BYTES = {HQ_S_BF16: 2, HQ_S_UE4M3: 1, HQ_S_UE8M0: 1}
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_U8 = (torch.uint8,)
 
 
 class _Args:
@@ -460,3 +492,210 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     _check(_lib.hq_quantize_act(at, p[0], M, K, p[1], pd, ps, pg, pws, ws_bytes, _stream(stream)), w)
     return out
+
+
+# ----------------------------------------------------------------- paged key-value cache
+_KV = {"bf16": HQ_KV_BF16, "e4m3": HQ_KV_E4M3, "nvfp4": HQ_KV_NVFP4}
+
+
+class KVCache:
+    """A paged key-value cache: its format and its pools, device tensors of the caller.
+
+    k, v: [pages, heads, page_size, row], row = head_dim bf16 values ('bf16'), head_dim e4m3 codes as uint8 ('e4m3') or
+    head_dim / 2 bytes of two e2m1 codes ('nvfp4', low nibble = even dim).  k_scale, v_scale: fp32 [pages, heads,
+    page_size] ('e4m3') or ue4m3 bytes [pages, heads, page_size, head_dim / 16] ('nvfp4').  k_global, v_global: fp32
+    [1] ('nvfp4'), the calibrated largest magnitude of each side / 2688."""
+
+    def __init__(self, kind, k, v, k_scale=None, v_scale=None, k_global=None, v_global=None):
+        w = "KVCache"
+        if kind not in _KV:
+            raise HQArgError(w, f"kind must be one of {', '.join(_KV)}, not {kind!r}")
+        code = _KV[kind]
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise HQArgError(w, "k must be a 4-D [pages, heads, page_size, row] tensor")
+        pages, heads, page, row = (int(n) for n in k.shape)
+        dim = 2 * row if code == HQ_KV_NVFP4 else row
+        rows = pages * heads * page
+        dt, size = (_BF16, 2 * rows * dim) if code == HQ_KV_BF16 else (_U8, rows * row)
+        sdt, ssize = {HQ_KV_BF16: (None, 0), HQ_KV_E4M3: (_F32, 4 * rows), HQ_KV_NVFP4: (_U8, rows * (dim // 16))}[code]
+        args = _Args(w).add(k, "k", size, dt).add(v, "v", size, dt)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is None) != (ssize == 0):
+                raise HQArgError(w, f"{name} is {'required' if ssize else 'not used'} by a {kind} cache")
+            args.add(t, name, ssize, sdt)
+        for name, t in (("k_global", k_global), ("v_global", v_global)):
+            if (t is None) != (code != HQ_KV_NVFP4):
+                raise HQArgError(w, f"{name} is {'required' if code == HQ_KV_NVFP4 else 'not used'} by a {kind} cache")
+            args.add(t, name, 4, _F32)
+        args.ptrs()
+        self.kind, self.device = kind, k.device
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_global, self.v_global = k_global, v_global
+        self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.fmt = KVFormat(code, page, heads, dim, pages)
+
+    def _pools(self):
+        return KVPools(*(None if t is None else t.data_ptr() for t in
+                         (self.k, self.v, self.k_scale, self.v_scale, self.k_global, self.v_global)))
+
+
+def make_kv_cache(kind, num_pages, page_size, num_heads, head_dim, k_amax=None, v_amax=None, device="cuda"):
+    """A KVCache with pools of its own, zeroed.  'nvfp4': k_amax, v_amax are the calibrated largest magnitudes."""
+    if kind not in _KV:
+        raise HQArgError("make_kv_cache", f"kind must be one of {', '.join(_KV)}, not {kind!r}")
+    shape = (int(num_pages), int(num_heads), int(page_size))
+    row, dt = {"bf16": (head_dim, torch.bfloat16), "e4m3": (head_dim, torch.uint8),
+               "nvfp4": (head_dim // 2, torch.uint8)}[kind]
+    t = dict(k=torch.zeros(*shape, row, dtype=dt, device=device), v=torch.zeros(*shape, row, dtype=dt, device=device))
+    if kind == "e4m3":
+        t.update({s: torch.zeros(*shape, dtype=torch.float32, device=device) for s in ("k_scale", "v_scale")})
+    elif kind == "nvfp4":
+        if k_amax is None or v_amax is None:
+            raise HQArgError("make_kv_cache", "an nvfp4 cache needs k_amax and v_amax")
+        t.update({s: torch.zeros(*shape, head_dim // 16, dtype=torch.uint8, device=device)
+                  for s in ("k_scale", "v_scale")})
+        t.update({s: torch.full((1,), float(m) / 2688.0, dtype=torch.float32, device=device)
+                  for s, m in (("k_global", k_amax), ("v_global", v_amax))})
+    return KVCache(kind, **t)
+
+
+def kv_workspace_bytes(cache, batch=0, num_q_heads=0):
+    return int(_lib.hq_kv_workspace_bytes(ctypes.byref(cache.fmt), int(batch), int(num_q_heads)))
+
+
+def make_kv_workspace(cache, batch=0, num_q_heads=0, stream=None):
+    """Allocate (through torch) and zero a workspace for kv_write and kv_read, and for paged_attention of up to `batch`
+    sequences.  It serves one stream at a time and is not shared with the GEMM calls."""
+    nb = kv_workspace_bytes(cache, batch, num_q_heads)
+    if nb == 0:
+        raise HQError(HQ_ERR_INVALID_ARG, "hq_kv_workspace_bytes")
+    ws = _on(stream, torch.empty, nb, dtype=torch.uint8, device=cache.device)
+    _check(_lib.hq_workspace_init(_ptr(ws), nb, _stream(stream)), "hq_workspace_init")
+    return ws
+
+
+def _on(stream, make, *a, **k):
+    """A new tensor that belongs to the stream the call runs on, so that its memory is not handed out to another
+    stream's work before the call has finished."""
+    if stream is None:
+        return make(*a, **k)
+    with torch.cuda.stream(stream):
+        return make(*a, **k)
+
+
+def _kv_cache(w, cache):
+    if not isinstance(cache, KVCache):
+        raise HQArgError(w, f"cache must be a KVCache, not {type(cache).__name__}")
+    return cache
+
+
+def _kv_table(w, args, page_table, batch):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise HQArgError(w, f"page_table must be a 2-D [{batch}, pages] tensor")
+    args.add(page_table, "page_table", 0, _I32)
+
+
+def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6, positions=None, cos_sin=None,
+             interleaved=False, q_out=None, workspace=None, stream=None):
+    """Norm, rotation and quantised append of the fused projection's rows qkv, bf16 [T, (num_q_heads + 2 heads) *
+    head_dim] (rows may be strided): query and key heads get an RMS norm with weights q_norm / k_norm (bf16 [head_dim],
+    None = no norm) and are rotated by `positions` (int32 [T]) with cos_sin (fp32 [positions, rotary_dim]: cosines,
+    then sines; None = no rotation); keys and values go to `slots` (int64 [T], page id * page_size + offset, negative =
+    not cached).  Returns the queries, bf16 [T, num_q_heads, head_dim]."""
+    w = "hq_kv_write"
+    c = _kv_cache(w, cache)
+    D, Hq = c.head_dim, int(num_q_heads)
+    row = (Hq + 2 * c.num_heads) * D
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2 or qkv.shape[1] != row:
+        raise HQArgError(w, f"qkv must be a 2-D [T, {row}] tensor")
+    T, stride = int(qkv.shape[0]), row
+    args = _Args(w)
+    if T > 1 and qkv.stride(0) != row:  # rows of a wider tensor
+        stride = int(qkv.stride(0))
+        if stride < row or (row > 1 and qkv.stride(1) != 1):
+            raise HQArgError(w, "qkv's rows must be contiguous and must not overlap")
+        args.add(qkv[0], "qkv", 2 * row, _BF16)
+    else:
+        args.add(qkv, "qkv", 2 * T * row, _BF16)
+    args.add(slots, "slots", 8 * T, _I64).add(q_norm, "q_norm", 2 * D, _BF16).add(k_norm, "k_norm", 2 * D, _BF16)
+    R = P = 0
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise HQArgError(w, "cos_sin must be a 2-D [positions, rotary_dim] tensor")
+        P, R = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+        if R == 0:
+            raise HQArgError(w, "cos_sin has no angles; pass None for no rotation")
+        if positions is None:
+            raise HQArgError(w, "positions are required with cos_sin")
+    args.add(cos_sin, "cos_sin", 4 * P * R, _F32).add(positions if R else None, "positions", 4 * T, _I32)
+    args.add(q_out, "q_out", 2 * T * Hq * D, _BF16).add(workspace, "workspace").add(c.k, "cache.k")
+    px, psl, pqn, pkn, pcs, pps, pq, pws, _ = args.ptrs()
+    if q_out is None:
+        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=c.device)
+        pq = _ptr(q_out)
+    if workspace is None:
+        workspace = make_kv_workspace(c, stream=stream)
+        pws = _ptr(workspace)
+    r = KVRows(px, stride, T, Hq, R, 1 if interleaved else 0, float(eps), pqn, pkn, pcs, P, pps, psl, pq)
+    _check(_lib.hq_kv_write(ctypes.byref(c.fmt), ctypes.byref(c._pools()), ctypes.byref(r), pws, _nbytes(workspace),
+                            _stream(stream)), w)
+    return q_out
+
+
+def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=None, stream=None):
+    """Cached tokens as contiguous bf16 rows: sequence b's tokens first[b].. (None: from 0), as many as starts[b + 1] -
+    starts[b], go to rows starts[b].. of (k, v), each bf16 [total, heads, head_dim].  page_table int32 [B, pages],
+    starts int64 [B + 1].  `out` = (k, v) receives the result when given; rows no sequence covers keep their values."""
+    w = "hq_kv_read"
+    c = _kv_cache(w, cache)
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
+        raise HQArgError(w, "starts must be a 1-D [B + 1] tensor")
+    B, total = int(starts.shape[0]) - 1, int(total)
+    size = 2 * total * c.num_heads * c.head_dim
+    ko, vo = (None, None) if out is None else out
+    args = _Args(w)
+    _kv_table(w, args, page_table, B)
+    args.add(starts, "starts", 8 * (B + 1), _I64).add(first, "first", 4 * B, _I32)
+    args.add(ko, "out[0]", size, _BF16).add(vo, "out[1]", size, _BF16).add(workspace, "workspace").add(c.k, "cache.k")
+    pt, pst, pf, pk, pv, pws, _ = args.ptrs()
+    if out is None:
+        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=torch.bfloat16, device=c.device)
+                  for _ in range(2))
+        pk, pv = _ptr(ko), _ptr(vo)
+    if workspace is None:
+        workspace = make_kv_workspace(c, stream=stream)
+        pws = _ptr(workspace)
+    _check(_lib.hq_kv_read(ctypes.byref(c.fmt), ctypes.byref(c._pools()), pt, int(page_table.shape[1]), pst, pf, B,
+                           total, pk, pv, pws, _nbytes(workspace), _stream(stream)), w)
+    return ko, vo
+
+
+def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.0, out=None, lse=None, workspace=None,
+                    stream=None):
+    """Attention of one new token per sequence: q bf16 [B, q_heads, head_dim], page_table int32 [B, pages], lens int32
+    [B] (cached tokens, the new one among them).  scale defaults to head_dim ** -0.5; window > 0: only the last `window`
+    tokens are seen; softcap > 0: scores become softcap * tanh(score / softcap).  Returns (out bf16 [B, q_heads,
+    head_dim], lse fp32 [B, q_heads]); a sequence of length 0 gets out = 0, lse = -inf."""
+    w = "hq_paged_attention"
+    c = _kv_cache(w, cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != c.head_dim:
+        raise HQArgError(w, f"q must be a 3-D [B, q_heads, {c.head_dim}] tensor")
+    B, Hq, D = (int(n) for n in q.shape)
+    args = _Args(w).add(q, "q", 2 * B * Hq * D, _BF16)
+    _kv_table(w, args, page_table, B)
+    args.add(lens, "lens", 4 * B, _I32).add(out, "out", 2 * B * Hq * D, _BF16).add(lse, "lse", 4 * B * Hq, _F32)
+    pq, pt, pn, po, pl, pws, _ = args.add(workspace, "workspace").add(c.k, "cache.k").ptrs()
+    if out is None:
+        out = _on(stream, torch.empty, (B, Hq, D), dtype=torch.bfloat16, device=c.device)
+        po = _ptr(out)
+    if lse is None:
+        lse = _on(stream, torch.empty, (B, Hq), dtype=torch.float32, device=c.device)
+        pl = _ptr(lse)
+    if workspace is None:
+        workspace = make_kv_workspace(c, B, Hq, stream=stream)
+        pws = _ptr(workspace)
+    s = D ** -0.5 if scale is None else float(scale)
+    _check(_lib.hq_paged_attention(ctypes.byref(c.fmt), ctypes.byref(c._pools()), pq, Hq, pt,
+                                   int(page_table.shape[1]), pn, B, s, int(window), float(softcap), po, pl, pws,
+                                   _nbytes(workspace), _stream(stream)), w)
+    return out, lse
