@@ -412,7 +412,7 @@ HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* ca
  * A sequence of length 0 gives out = 0 and lse = -inf.
  *   q           bf16 [B][num_q_heads][head_dim]; the new token's own key and value are already in the cache
  *   page_table  int32 [B][table_stride]; entries past the sequence's last page are not read
- *   lens        int32 [B], 0 <= lens[b] <= table_stride * page_size
+ *   lens        int32 [B], 0 <= lens[b] <= table_stride * page_size and 2^30
  *   window      tokens that are seen, 0 = all of them
  *   out         bf16 [B][num_q_heads][head_dim];  lse  fp32 [B][num_q_heads] (natural logarithm) or NULL
  * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) are rounded to the

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libhq.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libhq_debug.so")
 SOURCES = ["hq_api.cu", "hq_pack.cu", "hq_route.cu", "hq_gemm_int4.cu", "hq_gemm_nvfp4.cu", "hq_gemm_mxfp4.cu", "hq_gemm_mxfp4a.cu", "hq_gemm_mxfp4x.cu", "hq_gemm_mxfp4x_comb.cu", "hq_gemm_small.cu", "hq_gemm_small_fmt.cu", "hq_gemm_small_bits.cu", "hq_splitk.cu", "hq_noalloc.cu", "hq_act_quant.cu", "hq_moe_combine.cu", "hq_gemm_int4_comb.cu", "hq_gemm_nvfp4_comb.cu", "hq_gemm_mxfp4_comb.cu",
-           "kv/hq_kv_api.cu", "kv/hq_kv_write.cu", "kv/hq_kv_read.cu", "kv/hq_kv_attention.cu"]
+           "kv/hq_kv_api.cu", "kv/hq_kv_write.cu", "kv/hq_kv_read.cu",
+           "kv/hq_kv_attention_bf16.cu", "kv/hq_kv_attention_e4m3.cu", "kv/hq_kv_attention_nvfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

@@ -75,6 +75,7 @@ struct KvAttnArgs {
   int64_t table_stride;
   const int32_t* lens;
   int64_t B;
+  int64_t most;  // largest length: the table's row, or 2^30
   float scale;
   int64_t window;  // 0: all tokens
   float softcap;   // 0: none
@@ -85,6 +86,11 @@ struct KvAttnArgs {
 
 cudaError_t launch_kv_write(int kind, int dim, const KvWriteArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_read(int kind, int dim, const KvReadArgs& a, cudaStream_t stream);
-cudaError_t launch_kv_attention(int kind, int dim, const KvAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_attention_bf16(int dim, const KvAttnArgs& a, int ctas, float* slots, int* counters,
+                                     cudaStream_t stream);
+cudaError_t launch_kv_attention_e4m3(int dim, const KvAttnArgs& a, int ctas, float* slots, int* counters,
+                                     cudaStream_t stream);
+cudaError_t launch_kv_attention_nvfp4(int dim, const KvAttnArgs& a, int ctas, float* slots, int* counters,
+                                      cudaStream_t stream);
 
 }  // namespace hq

@@ -5,6 +5,7 @@
 
 #include "../../../include/hq.h"
 #include "hq_kv.h"
+#include "hq_kv_attention.cuh"
 
 namespace hq {
 namespace {
@@ -38,6 +39,11 @@ hq_status_t check_cache(const hq_kv_format_t* f, const hq_kv_cache_t* c) {
   return HQ_OK;
 }
 
+// (sequence, head, row tile) triples of the attention
+int64_t pairs(const hq_kv_format_t* f, int64_t batch, int32_t num_q_heads) {
+  return batch * f->num_heads * ((num_q_heads / f->num_heads + KA_ROWS - 1) / KA_ROWS);
+}
+
 hq_status_t check_workspace(const hq_kv_format_t* f, int64_t batch, int32_t num_q_heads, const void* ws,
                             size_t ws_bytes) {
   if (!ws || ws_bytes < hq_kv_workspace_bytes(f, batch, num_q_heads)) return HQ_ERR_WORKSPACE;
@@ -58,6 +64,15 @@ KvView view(const hq_kv_format_t* f, const hq_kv_cache_t* c) {
   return v;
 }
 
+// CTAs of the attention: two per SM of the current device (without a device: of a GB300, for host-only queries)
+int attention_ctas() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 152;
+  return 2 * n;
+}
+
 hq_status_t launched(cudaError_t e) { return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA; }
 
 }  // namespace
@@ -70,8 +85,8 @@ extern "C" {
 size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, int32_t num_q_heads) {
   if (check_format(fmt) != HQ_OK || batch < 0 || batch > kMaxRows) return 0;
   if (batch == 0) return KV_HEADER_BYTES;
-  if (check_q_heads(fmt, num_q_heads) != HQ_OK) return 0;
-  return KV_HEADER_BYTES;
+  if (check_q_heads(fmt, num_q_heads) != HQ_OK || batch * num_q_heads > kMaxRows) return 0;
+  return ka_counters_at(attention_ctas()) + sizeof(int) * (size_t)pairs(fmt, batch, num_q_heads);
 }
 
 hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* r, void* workspace,
@@ -166,13 +181,24 @@ hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* c
   a.table_stride = table_stride;
   a.lens = lens;
   a.B = B;
+  const int64_t most = table_stride * fmt->page_size;
+  a.most = most < kMaxRows ? most : kMaxRows;
   a.scale = scale;
   a.window = window;
   a.softcap = softcap;
   a.out = (uint16_t*)out;
   a.lse = lse;
   a.status = (int*)workspace;
-  return launched(launch_kv_attention(fmt->kind, fmt->head_dim, a, (cudaStream_t)stream));
+  // no more CTAs than units of 64 tokens that the lengths can make
+  const int64_t seen = window > 0 && window < a.most ? window + KV_BLOCK : a.most;
+  const int64_t units = pairs(fmt, B, num_q_heads) * ((seen + 63) / 64 > 0 ? (seen + 63) / 64 : 1);
+  const int all = attention_ctas(), ctas = units < all ? (int)units : all;
+  float* slots = reinterpret_cast<float*>((uint8_t*)workspace + KV_HEADER_BYTES);
+  int* counters = reinterpret_cast<int*>((uint8_t*)workspace + ka_counters_at(all));
+  const auto launch = fmt->kind == HQ_KV_BF16 ? launch_kv_attention_bf16
+                                              : (fmt->kind == HQ_KV_E4M3 ? launch_kv_attention_e4m3
+                                                                         : launch_kv_attention_nvfp4);
+  return launched(launch(fmt->head_dim, a, ctas, slots, counters, (cudaStream_t)stream));
 }
 
 }  // extern "C"
