@@ -533,10 +533,10 @@ class KVCache:
         self.k_global, self.v_global = k_global, v_global
         self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, heads, page, dim
         self.fmt = KVFormat(code, page, heads, dim, pages)
-
-    def _pools(self):
-        return KVPools(*(None if t is None else t.data_ptr() for t in
-                         (self.k, self.v, self.k_scale, self.v_scale, self.k_global, self.v_global)))
+        # the handle keeps the pools alive and their addresses with them: they must not be resized
+        self._pools = KVPools(*(None if t is None else t.data_ptr() for t in
+                                (k, v, k_scale, v_scale, k_global, v_global)))
+        self._refs = ctypes.byref(self.fmt), ctypes.byref(self._pools)
 
 
 def make_kv_cache(kind, num_pages, page_size, num_heads, head_dim, k_amax=None, v_amax=None, device="cuda"):
@@ -589,10 +589,36 @@ def _kv_cache(w, cache):
     return cache
 
 
-def _kv_table(w, args, page_table, batch):
+def _kv_ptrs(w, c, items):
+    """Addresses of a call's tensors: items are (tensor or None, name, elements that the call reads or writes, dtype or
+    None).  One look at each right tensor, because a decoding step makes this call for every layer; at the first one
+    that is not, _Args judges them all and raises."""
+    dev, out = c.device.index, []
+    for t, _, n, dt in items:
+        if t is None:
+            out.append(None)
+        elif (isinstance(t, torch.Tensor) and (t.dtype is dt or dt is None) and t.get_device() == dev
+              and t.numel() >= n and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        if torch._C._cuda_getDevice() == dev:
+            return out
+    args = _Args(w)
+    for t, name, n, dt in items:
+        args.add(t, name, n * (dt.itemsize if dt else 1), (dt,) if dt else None)
+    return [None if p is None else p.value for p in args.add(c.k, "cache.k").ptrs()][:-1]
+
+
+def _kv_stream(c, stream):
+    return torch._C._cuda_getCurrentRawStream(c.device.index) if stream is None else stream.cuda_stream
+
+
+def _kv_table(w, page_table, batch):
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise HQArgError(w, f"page_table must be a 2-D [{batch}, pages] tensor")
-    args.add(page_table, "page_table", 0, _I32)
+    return page_table.shape[1]
 
 
 def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6, positions=None, cos_sin=None,
@@ -608,37 +634,34 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
     row = (Hq + 2 * c.num_heads) * D
     if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2 or qkv.shape[1] != row:
         raise HQArgError(w, f"qkv must be a 2-D [T, {row}] tensor")
-    T, stride = int(qkv.shape[0]), row
-    args = _Args(w)
+    T, stride, x = qkv.shape[0], row, qkv
     if T > 1 and qkv.stride(0) != row:  # rows of a wider tensor
-        stride = int(qkv.stride(0))
+        stride, x = qkv.stride(0), qkv[0]
         if stride < row or (row > 1 and qkv.stride(1) != 1):
             raise HQArgError(w, "qkv's rows must be contiguous and must not overlap")
-        args.add(qkv[0], "qkv", 2 * row, _BF16)
-    else:
-        args.add(qkv, "qkv", 2 * T * row, _BF16)
-    args.add(slots, "slots", 8 * T, _I64).add(q_norm, "q_norm", 2 * D, _BF16).add(k_norm, "k_norm", 2 * D, _BF16)
     R = P = 0
     if cos_sin is not None:
         if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
             raise HQArgError(w, "cos_sin must be a 2-D [positions, rotary_dim] tensor")
-        P, R = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+        P, R = cos_sin.shape
         if R == 0:
             raise HQArgError(w, "cos_sin has no angles; pass None for no rotation")
         if positions is None:
             raise HQArgError(w, "positions are required with cos_sin")
-    args.add(cos_sin, "cos_sin", 4 * P * R, _F32).add(positions if R else None, "positions", 4 * T, _I32)
-    args.add(q_out, "q_out", 2 * T * Hq * D, _BF16).add(workspace, "workspace").add(c.k, "cache.k")
-    px, psl, pqn, pkn, pcs, pps, pq, pws, _ = args.ptrs()
+    bf16 = torch.bfloat16
+    px, psl, pqn, pkn, pcs, pps, pq, pws = _kv_ptrs(w, c, (
+        (x, "qkv", row if x is not qkv else T * row, bf16), (slots, "slots", T, torch.int64),
+        (q_norm, "q_norm", D, bf16), (k_norm, "k_norm", D, bf16), (cos_sin, "cos_sin", P * R, torch.float32),
+        (positions if R else None, "positions", T, torch.int32), (q_out, "q_out", T * Hq * D, bf16),
+        (workspace, "workspace", 0, None)))
     if q_out is None:
-        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=torch.bfloat16, device=c.device)
-        pq = _ptr(q_out)
+        q_out = _on(stream, qkv.new_empty, (T, Hq, D))
+        pq = q_out.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-        pws = _ptr(workspace)
-    r = KVRows(px, stride, T, Hq, R, 1 if interleaved else 0, float(eps), pqn, pkn, pcs, P, pps, psl, pq)
-    _check(_lib.hq_kv_write(ctypes.byref(c.fmt), ctypes.byref(c._pools()), ctypes.byref(r), pws, _nbytes(workspace),
-                            _stream(stream)), w)
+        pws = workspace.data_ptr()
+    r = KVRows(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl, pq)
+    _check(_lib.hq_kv_write(*c._refs, ctypes.byref(r), pws, _nbytes(workspace), _kv_stream(c, stream)), w)
     return q_out
 
 
@@ -650,23 +673,23 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
     c = _kv_cache(w, cache)
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
         raise HQArgError(w, "starts must be a 1-D [B + 1] tensor")
-    B, total = int(starts.shape[0]) - 1, int(total)
-    size = 2 * total * c.num_heads * c.head_dim
+    B, total, bf16 = starts.shape[0] - 1, int(total), torch.bfloat16
+    size = total * c.num_heads * c.head_dim
     ko, vo = (None, None) if out is None else out
-    args = _Args(w)
-    _kv_table(w, args, page_table, B)
-    args.add(starts, "starts", 8 * (B + 1), _I64).add(first, "first", 4 * B, _I32)
-    args.add(ko, "out[0]", size, _BF16).add(vo, "out[1]", size, _BF16).add(workspace, "workspace").add(c.k, "cache.k")
-    pt, pst, pf, pk, pv, pws, _ = args.ptrs()
+    cols = _kv_table(w, page_table, B)
+    pt, pst, pf, pk, pv, pws = _kv_ptrs(w, c, (
+        (page_table, "page_table", B * cols, torch.int32), (starts, "starts", B + 1, torch.int64),
+        (first, "first", B, torch.int32), (ko, "out[0]", size, bf16), (vo, "out[1]", size, bf16),
+        (workspace, "workspace", 0, None)))
     if out is None:
-        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=torch.bfloat16, device=c.device)
+        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=bf16, device=c.device)
                   for _ in range(2))
-        pk, pv = _ptr(ko), _ptr(vo)
+        pk, pv = ko.data_ptr(), vo.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-        pws = _ptr(workspace)
-    _check(_lib.hq_kv_read(ctypes.byref(c.fmt), ctypes.byref(c._pools()), pt, int(page_table.shape[1]), pst, pf, B,
-                           total, pk, pv, pws, _nbytes(workspace), _stream(stream)), w)
+        pws = workspace.data_ptr()
+    _check(_lib.hq_kv_read(*c._refs, pt, cols, pst, pf, B, total, pk, pv, pws, _nbytes(workspace),
+                           _kv_stream(c, stream)), w)
     return ko, vo
 
 
@@ -680,22 +703,21 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
     c = _kv_cache(w, cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != c.head_dim:
         raise HQArgError(w, f"q must be a 3-D [B, q_heads, {c.head_dim}] tensor")
-    B, Hq, D = (int(n) for n in q.shape)
-    args = _Args(w).add(q, "q", 2 * B * Hq * D, _BF16)
-    _kv_table(w, args, page_table, B)
-    args.add(lens, "lens", 4 * B, _I32).add(out, "out", 2 * B * Hq * D, _BF16).add(lse, "lse", 4 * B * Hq, _F32)
-    pq, pt, pn, po, pl, pws, _ = args.add(workspace, "workspace").add(c.k, "cache.k").ptrs()
+    B, Hq, D = q.shape
+    size, cols = B * Hq * D, _kv_table(w, page_table, B)
+    pq, pt, pn, po, pl, pws = _kv_ptrs(w, c, (
+        (q, "q", size, torch.bfloat16), (page_table, "page_table", B * cols, torch.int32),
+        (lens, "lens", B, torch.int32), (out, "out", size, torch.bfloat16), (lse, "lse", B * Hq, torch.float32),
+        (workspace, "workspace", 0, None)))
     if out is None:
-        out = _on(stream, torch.empty, (B, Hq, D), dtype=torch.bfloat16, device=c.device)
-        po = _ptr(out)
+        out = _on(stream, q.new_empty, (B, Hq, D))
+        po = out.data_ptr()
     if lse is None:
-        lse = _on(stream, torch.empty, (B, Hq), dtype=torch.float32, device=c.device)
-        pl = _ptr(lse)
+        lse = _on(stream, q.new_empty, (B, Hq), dtype=torch.float32)
+        pl = lse.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, B, Hq, stream=stream)
-        pws = _ptr(workspace)
-    s = D ** -0.5 if scale is None else float(scale)
-    _check(_lib.hq_paged_attention(ctypes.byref(c.fmt), ctypes.byref(c._pools()), pq, Hq, pt,
-                                   int(page_table.shape[1]), pn, B, s, int(window), float(softcap), po, pl, pws,
-                                   _nbytes(workspace), _stream(stream)), w)
+        pws = workspace.data_ptr()
+    _check(_lib.hq_paged_attention(*c._refs, pq, Hq, pt, cols, pn, B, D ** -0.5 if scale is None else scale, window,
+                                   softcap, po, pl, pws, _nbytes(workspace), _kv_stream(c, stream)), w)
     return out, lse

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../../include/hq.h"
 #include "hq_kv.h"
 #include "hq_kv_attention.cuh"
@@ -64,13 +66,15 @@ KvView view(const hq_kv_format_t* f, const hq_kv_cache_t* c) {
   return v;
 }
 
-// CTAs of the attention: two per SM of the current device (without a device: of a GB300, for host-only queries)
-int attention_ctas() {
+// SMs of the current device, looked up once per device (without a device: a GB300's, for host-only queries)
+int num_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    n = 152;
-  return 2 * n;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 hq_status_t launched(cudaError_t e) { return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA; }
@@ -86,7 +90,7 @@ size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, int32_t n
   if (check_format(fmt) != HQ_OK || batch < 0 || batch > kMaxRows) return 0;
   if (batch == 0) return KV_HEADER_BYTES;
   if (check_q_heads(fmt, num_q_heads) != HQ_OK || batch * num_q_heads > kMaxRows) return 0;
-  return ka_counters_at(attention_ctas()) + sizeof(int) * (size_t)pairs(fmt, batch, num_q_heads);
+  return ka_counters_at(num_sms()) + sizeof(int) * (size_t)pairs(fmt, batch, num_q_heads);
 }
 
 hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* r, void* workspace,
@@ -189,16 +193,14 @@ hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* c
   a.out = (uint16_t*)out;
   a.lse = lse;
   a.status = (int*)workspace;
-  // no more CTAs than units of 64 tokens that the lengths can make
-  const int64_t seen = window > 0 && window < a.most ? window + KV_BLOCK : a.most;
-  const int64_t units = pairs(fmt, B, num_q_heads) * ((seen + 63) / 64 > 0 ? (seen + 63) / 64 : 1);
-  const int all = attention_ctas(), ctas = units < all ? (int)units : all;
+  const int sms = num_sms();
   float* slots = reinterpret_cast<float*>((uint8_t*)workspace + KV_HEADER_BYTES);
-  int* counters = reinterpret_cast<int*>((uint8_t*)workspace + ka_counters_at(all));
+  int* counters = reinterpret_cast<int*>((uint8_t*)workspace + ka_counters_at(sms));
+  const int64_t seen = window > 0 && window < a.most ? window + KV_BLOCK : a.most;
   const auto launch = fmt->kind == HQ_KV_BF16 ? launch_kv_attention_bf16
                                               : (fmt->kind == HQ_KV_E4M3 ? launch_kv_attention_e4m3
                                                                          : launch_kv_attention_nvfp4);
-  return launched(launch(fmt->head_dim, a, ctas, slots, counters, (cudaStream_t)stream));
+  return launched(launch(fmt->head_dim, a, sms, seen, slots, counters, (cudaStream_t)stream));
 }
 
 }  // extern "C"

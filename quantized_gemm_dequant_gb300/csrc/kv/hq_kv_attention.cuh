@@ -8,16 +8,17 @@
 //
 // What bounds it: the cache is read once and 4 G operations are done per key-value pair of elements for the G query
 // heads that share a head, so up to G = 16 the kernel is bound by memory.  The work is laid out for that:
-//  - The tokens of all (sequence, head) pairs form one list of 64-token units, cut into equal shares for a fixed number
-//    of CTAs (two per SM), whatever the lengths are.  A pair inside one share is finished there; one that crosses
-//    shares leaves fp32 partial results in the workspace, and the last CTA to arrive joins them in order.  The lengths
-//    are read on the device, so a captured call follows them.
-//  - The four warps of a CTA each stream every fourth 16-token block through a ring of their own in shared memory
-//    (cp.async, 16 bytes a lane, one slot per block and side); no barrier but the warp's own between them until a
-//    pair's parts are joined.  The ring runs ahead across pairs.
-//  - Products run on mma.sync m16n8k16 with the G heads as the 16 rows.  A tcgen05 tile has at least 64 rows, of which
-//    G would be used, and its operands would have to be decoded through shared memory; the legacy unit's rate is
-//    several times what memory feeds here (see the table of measurements at the launch).
+//  - The tokens of all (sequence, head) pairs form one list of small units, cut into equal shares for a fixed number of
+//    CTAs, whatever the lengths are.  A pair inside one share is finished there; one that crosses shares leaves fp32
+//    partial results in the workspace, and the last CTA to arrive joins them in order.  The lengths are read on the
+//    device, so a captured call follows them.
+//  - The four warps of a CTA each stream every fourth chunk of 16 or 32 tokens through a ring of their own in shared
+//    memory (cp.async, 16 bytes a lane, one slot per chunk and side); no barrier but the warp's own until a pair's
+//    parts are joined.  The ring runs ahead across pairs.
+//  - Products run on mma.sync m16n8k16 with 16 tokens as the rows and 8 query heads as the columns, s^T = K q^T and
+//    o^T = V^T p^T: the codes are the A operand of both, so their decoding is shared by up to 16 heads, and a group of
+//    8 heads wastes nothing.  Between the two, movmatrix turns p.  (A tcgen05 tile would need the decoded operands
+//    back in shared memory; the legacy unit is at a fifth of its rate here.)
 //  - 8- and 4-bit codes go from shared memory through ldmatrix to registers and become f16 there, exactly.  The
 //    fragments' dims are permuted so that a lane's bytes are its own: the dot product does not care about the order of
 //    dims if q follows it, and the output's order is undone when it is stored.
@@ -26,8 +27,8 @@
 //    whatever the scales' range, while l sums exp2(s_j - m) in fp32 beside it.
 //  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and o.
 //  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
-//  - The running maximum only moves when a score exceeds it by 8 (powers of two): o is seldom rescaled, and weights up
-//    to 2^8 fit the 16-bit types.
+//  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
+//    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.
 #pragma once
 #include <cuda_runtime.h>
 #include <math.h>
@@ -42,56 +43,84 @@ namespace hq {
 
 constexpr int KA_WARPS = 4;
 constexpr int KA_THREADS = 32 * KA_WARPS;
-constexpr int KA_ROWS = 16;        // query heads of one tile (the matrix instruction's rows)
-constexpr float KA_LAZY = 8.0f;    // the running maximum lags by at most this (log2)
+constexpr int KA_ROWS = 16;          // query heads of one row tile, at most
+constexpr float KA_LAZY = 8.0f;      // the running maximum lags by at most this (log2)
+constexpr float KA_NONE = -3.0e38f;  // the running maximum of no token
 
-template <int KIND, int D>
+// Units of 16 tokens per unit of the list, CTAs per SM.
+__host__ __device__ constexpr int ka_blocks(int kind, int dim) { return kind == HQ_KV_BF16 || dim == 256 ? 1 : 2; }
+__host__ __device__ constexpr int ka_ctas(int kind, int dim, int nt) {
+  return dim == 256 ? 2 : (nt == 2 ? 2 : 3);
+}
+
+template <int KIND, int D, int NT>
 struct KaCfg {
   static constexpr int RB = kv_row_bytes(KIND, D), SB = kv_scale_bytes(KIND, D);
-  static constexpr int TOK = 16;                     // tokens of one ring slot
-  static constexpr int SLOT = TOK * (RB + SB);       // bytes of one slot: codes, then scales, of one side
-  static constexpr int PAD = KIND == HQ_KV_BF16 ? 8 : (KIND == HQ_KV_E4M3 ? 16 : 4);  // floats: no bank conflicts
-  static constexpr int MERGE = KA_WARPS * 8 * (D + PAD) * 4;  // eight rows of every warp
-  static constexpr bool QS = D == 256;               // q's fragments in shared memory instead of registers
-  static constexpr int QBYTES = QS ? D / 16 * 512 : 0;
-  static constexpr int FIXED = MERGE + QBYTES + 512;
-  static constexpr int LIMIT = (228 * 1024) / 2 - 1024;  // shared memory of one of two CTAs on an SM
+  static constexpr int TB = ka_blocks(KIND, D);      // 16-token blocks of one ring slot
+  static constexpr int BLOCK = 16 * (RB + SB);       // a block's codes, then its scales
+  static constexpr int SLOT = TB * BLOCK;
+  static constexpr int CTAS = ka_ctas(KIND, D, NT);  // per SM
+  static constexpr int PAD = 4;                      // floats: the lanes' stores of a head's dims meet no bank twice
+  static constexpr int MERGE = KA_WARPS * 8 * (D + PAD) * 4;  // eight heads of every warp
+  static constexpr bool QS = D == 256 && NT == 2;    // q's fragments in shared memory instead of registers
+  static constexpr int QBYTES = QS ? D / 16 * NT * 256 : 0;
+  static constexpr int FIXED = MERGE + QBYTES + 384;
+  static constexpr int LIMIT = (228 * 1024) / CTAS / 128 * 128 - 1024;  // shared memory of a CTA
   static constexpr int FIT = (LIMIT - FIXED) / (KA_WARPS * (SLOT + 4));
   static constexpr int SLOTS = FIT < 2 ? 2 : (FIT > 12 ? 12 : FIT);
   static constexpr int SMEM = FIXED + KA_WARPS * SLOTS * (SLOT + 4);
-  // 16-byte units: unit u of row r sits at u ^ swz(r), so that eight rows' equal units lie in different banks
+  static_assert(SMEM <= LIMIT, "shared memory");
+  // unit u (16 bytes) of row r sits at u ^ ((r / RPL) & XM), so that eight rows' equal units lie in different banks
   static constexpr int UPR = RB / 16;
   static constexpr int RPL = UPR >= 8 ? 1 : 8 / UPR;  // rows of a 128-byte line
   static constexpr int XM = (UPR >= 8 ? 8 : UPR) - 1;
-  static __device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * RB + ((u ^ ((r / RPL) & XM)) << 4)); }
+  static __device__ __forceinline__ uint32_t at(int r, int u) {
+    return (uint32_t)(r * RB + ((u ^ ((r / RPL) & XM)) << 4));
+  }
 };
 
 // Workspace of a call, for the host (sizes) and the device: the status, then two slots per CTA for the parts of split
 // pairs, then a counter per (sequence, head, row tile).  A slot has room for any format's part, so that the counters,
 // which have to be zero between calls, are at one place whatever the calls' shapes are.
 constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 2);  // o, then (m, l) of each row
-constexpr size_t ka_counters_at(int ctas) {
-  return KV_HEADER_BYTES + 2 * (size_t)ctas * KA_SLOT_FLOATS * sizeof(float);
+constexpr int KA_MOST_CTAS = 4;                         // per SM
+constexpr size_t ka_counters_at(int sms) {
+  return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
 }
 
 #ifdef __CUDACC__
 
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// transpose of an 8 x 8 matrix of 16-bit values, a row's pair per lane
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 template <bool BF16>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
   if constexpr (BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -122,9 +151,10 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t x, int i) {
 
 // One sequence's share of the list of units.
 struct KaSeq {
-  int n, j0, t0;     // tokens, the first that is seen, and that one's block
-  int64_t units;     // per (head, row tile), at least one: an empty sequence's output is written too
+  int n, j0, t0;  // tokens, the first that is seen, and that one's block
+  int units;      // per (head, row tile), at least one: an empty sequence's output is written too
 };
+template <int TB>
 __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
   KaSeq s;
   int64_t n = a.lens[b];
@@ -132,13 +162,14 @@ __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
   const int64_t j0 = a.window > 0 && n > a.window ? n - a.window : 0;
   s.n = (int)n;
   s.j0 = (int)j0;
-  s.t0 = (int)(j0 & ~(int64_t)(KV_BLOCK - 1));
-  const int64_t u = (n - s.t0 + 63) >> 6;
+  s.t0 = s.j0 & ~(KV_BLOCK - 1);
+  const int u = (s.n - s.t0 + 16 * TB - 1) / (16 * TB);
   s.units = u > 0 ? u : 1;
   return s;
 }
 
 // A walk over a CTA's share, one (sequence, head, row tile) after another.
+template <int TB>
 struct KaWalk {
   int64_t u, hi;   // position in the list, end of the share
   int64_t seg0;    // the pair's first unit in the list
@@ -148,10 +179,10 @@ struct KaWalk {
   __device__ __forceinline__ bool done() const { return u >= hi; }
   __device__ __forceinline__ int64_t stop() const { return seg0 + s.units < hi ? seg0 + s.units : hi; }
   // tokens of the share's part of the pair
-  __device__ __forceinline__ int from() const { return s.t0 + (int)((u - seg0) << 6); }
+  __device__ __forceinline__ int from() const { return s.t0 + (int)(u - seg0) * (16 * TB); }
   __device__ __forceinline__ int to() const {
-    const int64_t t = s.t0 + ((stop() - seg0) << 6);
-    return t < s.n ? (int)t : s.n;
+    const int t = s.t0 + (int)(stop() - seg0) * (16 * TB);
+    return t < s.n ? t : s.n;
   }
   __device__ __forceinline__ void next(const KvAttnArgs& a, int hrs) {
     u = stop();
@@ -159,22 +190,33 @@ struct KaWalk {
     seg0 = u;
     if (++hr == hrs) {
       hr = 0;
-      s = ka_seq(a, ++b);
+      s = ka_seq<TB>(a, ++b);
     }
   }
 };
 
-template <int KIND, int D>
-__global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAttnArgs a, float* slots, int* counters) {
-  using C = KaCfg<KIND, D>;
-  constexpr bool BF = KIND == HQ_KV_BF16;
-  constexpr int KS = D / 16, NT = D / 8;
+// One row's result: 4 dims of o, and lse
+__device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, int d, float4 y, float top, float sum,
+                                         float gain) {
+  const float inv = sum > 0.0f ? gain / sum : 0.0f;
+  *reinterpret_cast<uint2*>(a.out + q * D + d) =
+      make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  if (d == 0 && a.lse) a.lse[q] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int KIND, int D, int NT>
+__global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
+    kv_attention_kernel(const KvAttnArgs a, float* slots, int* counters) {
+  using C = KaCfg<KIND, D, NT>;
+  constexpr bool BF = KIND == HQ_KV_BF16, F8 = KIND == HQ_KV_E4M3;
+  constexpr int KS = D / 16, TB = C::TB, STRIDE = 16 * TB * KA_WARPS;
+  constexpr uint32_t FULL = TB == 1 ? 0xFFFFu : 0xFFFFFFFFu;
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem);
   uint32_t* qsm = reinterpret_cast<uint32_t*>(smem + C::MERGE);
-  int64_t* found = reinterpret_cast<int64_t*>(smem + C::MERGE + C::QBYTES);  // 3 words; then the warps' m and l
-  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 64);   // [warp][8 rows][2]
-  uint32_t* scan = reinterpret_cast<uint32_t*>(smem + C::MERGE + C::QBYTES + 64);
+  int64_t* found = reinterpret_cast<int64_t*>(smem + C::MERGE + C::QBYTES);  // 3 words
+  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 64);   // [warp][8 heads][2]
+  int64_t* scan = reinterpret_cast<int64_t*>(mls);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + C::FIXED + warp * C::SLOTS * C::SLOT;
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::FIXED + KA_WARPS * C::SLOTS * C::SLOT) + warp * C::SLOTS;
@@ -189,7 +231,7 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
   const int64_t b0 = per * threadIdx.x < a.B ? per * threadIdx.x : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
   int64_t mine = 0;
   for (int64_t b = b0; b < b1; ++b) {
-    mine += ka_seq(a, b).units;
+    mine += ka_seq<TB>(a, b).units;
     if (blockIdx.x == 0 && (a.lens[b] < 0 || a.lens[b] > a.most)) kv_report(a.status);
   }
   int64_t before = mine;  // inclusive sum over the warp's lanes, then exclusive over the CTA
@@ -198,24 +240,25 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
     const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += y;
   }
-  if (lane == 31) reinterpret_cast<int64_t*>(scan)[warp] = before;
+  if (lane == 31) scan[warp] = before;
   before -= mine;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < KA_WARPS; ++w) {
-    const int64_t y = reinterpret_cast<int64_t*>(scan)[w];
+    const int64_t y = scan[w];
     if (w < warp) before += y;
     total += y;
   }
   total *= hrs;
-  const int64_t W = total < gridDim.x ? total : gridDim.x;  // every CTA that works has a unit at least
+  // every CTA that works has four units (one for each warp) or the whole list is shorter
+  const int64_t want = (total + 3) >> 2, W = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= W) return;
   const int64_t lo = total * blockIdx.x / W, hi = total * (blockIdx.x + 1) / W;
   if (lo >= before * hrs && lo < (before + mine) * hrs) {
     int64_t p = before;
     for (int64_t b = b0; b < b1; ++b) {
-      const int64_t n = ka_seq(a, b).units;
+      const int64_t n = ka_seq<TB>(a, b).units;
       if (lo < (p + n) * hrs) {
         found[0] = b;
         found[1] = p;
@@ -225,71 +268,79 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
     }
   }
   __syncthreads();
-  KaWalk at;
+  KaWalk<TB> at;
   at.u = lo;
   at.hi = hi;
   at.b = found[0];
-  at.s = ka_seq(a, at.b);
+  at.s = ka_seq<TB>(a, at.b);
   const int64_t in = lo - found[1] * hrs;
   at.hr = (int)(in / at.s.units);
   at.seg0 = lo - in % at.s.units;
 
-  // ---- the ring's front: this warp's 16-token blocks of the share, keys and values alternating
-  KaWalk ahead = at;
-  int next_tok = ahead.from() + KV_BLOCK * warp, next_end = ahead.to();
-  int page = 0, off = 0, have = 0, used = 0;  // lane i: the page and offset of the warp's i-th block from here
+  // ---- the ring's front: this warp's chunks of the share, keys and values alternating
+  KaWalk<TB> ahead = at;
+  int next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to();
+  int64_t row = -1;            // lane i: the first row of the warp's i-th block from the last look at the table
+  int used = 32;               // blocks of it that are used up
   bool more = true;
   int put = 0, side = 0;
-  uint32_t word = 0;
-  int64_t base = 0;
+  uint32_t word = 0;           // tokens of the chunk that are seen
+  int64_t base[TB];
   auto issue = [&]() {
     if (side == 0) {
       while (more && next_tok >= next_end) {  // the share's next pair
         ahead.next(a, hrs);
         more = !ahead.done();
-        if (more) next_tok = ahead.from() + KV_BLOCK * warp, next_end = ahead.to(), have = used = 0;
+        if (more) next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to(), used = 32;
       }
       if (more) {
-        if (used == have) {
-          const int64_t tok = (int64_t)next_tok + KV_BLOCK * KA_WARPS * lane;
-          page = -1;
-          off = 0;
+        if (used == 32) {
+          const int64_t tok = (int64_t)next_tok + STRIDE * (lane / TB) + 16 * (lane % TB);
+          row = -1;
           if (tok < next_end) {
             const int col = (int)((uint32_t)tok / (uint32_t)a.kv.page_size);
-            page = a.page_table[ahead.b * a.table_stride + col];
-            off = (int)tok - col * a.kv.page_size;
-            if (page < 0 || page >= a.kv.num_pages) {
+            const int64_t page = a.page_table[ahead.b * a.table_stride + col];
+            if (page >= 0 && page < a.kv.num_pages)
+              row = (page * H + ahead.hr / tiles) * a.kv.page_size + ((int)tok - col * a.kv.page_size);
+            else
               kv_report(a.status);
-              page = -1;
-            }
           }
-          have = 32;
           used = 0;
         }
-        const int p = __shfl_sync(0xffffffffu, page, used), o = __shfl_sync(0xffffffffu, off, used);
-        ++used;
-        const int first = ahead.s.j0 - next_tok, last = ahead.s.n - next_tok;  // tokens of the block that are seen
-        word = 0xFFFFu;
-        if (first > 0) word &= 0xFFFFu << first;
-        if (last < 16) word &= 0xFFFFu >> (16 - last);
-        if (p < 0) word = 0;
-        base = ((int64_t)(p < 0 ? 0 : p) * H + ahead.hr / tiles) * a.kv.page_size + o;
-        next_tok += KV_BLOCK * KA_WARPS;
-      } else {
-        word = 0;
+        const int first = ahead.s.j0 - next_tok, last = ahead.s.n - next_tok;
+        word = FULL;
+        if (first > 0) word &= FULL << first;
+        if (last < 16 * TB) word &= FULL >> (16 * TB - last);
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+          base[i] = __shfl_sync(0xffffffffu, row, used + i);
+          if (base[i] < 0) word &= ~(0xFFFFu << (16 * i)), base[i] = 0;
+        }
+        used += TB;
+        next_tok += STRIDE;
       }
     }
     if (more) {
-      const uint8_t* codes = (side ? a.kv.v : a.kv.k) + base * C::RB;
-      uint8_t* slot = ring + put * C::SLOT;
+      const uint32_t slot = ring_at + put * C::SLOT;
 #pragma unroll
-      for (int i = 0; i < C::RB / 32; ++i) {
-        const int e = lane + 32 * i, r = e / C::UPR, u = e % C::UPR;
-        cp_async_16(slot + C::at(r, u), codes + e * 16, (word >> r) & 1u ? 16u : 0u);
-      }
-      if constexpr (C::SB > 0) {
-        const uint8_t* scales = (side ? a.kv.v_scale : a.kv.k_scale) + base * C::SB;
-        if (lane < C::SB) cp_async_16(slot + 16 * C::RB + 16 * lane, scales + 16 * lane, word ? 16u : 0u);
+      for (int t = 0; t < TB; ++t) {
+        const uint8_t* codes = (side ? a.kv.v : a.kv.k) + base[t] * C::RB + lane * 16;
+        const uint8_t* scales = (side ? a.kv.v_scale : a.kv.k_scale) + base[t] * C::SB + lane * 16;
+        const uint32_t to = slot + t * C::BLOCK;
+        if (word == FULL) {
+#pragma unroll
+          for (int i = 0; i < C::RB / 32; ++i)
+            copy16(to + C::at((lane + 32 * i) / C::UPR, (lane + 32 * i) % C::UPR), codes + 512 * i);
+          if (C::SB > 0 && lane < C::SB) copy16(to + 16 * C::RB + 16 * lane, scales);
+        } else {  // rows that are not seen are zero: whatever they hold meets a weight of zero, and may be NaN
+          const uint32_t w = word >> (16 * t);
+#pragma unroll
+          for (int i = 0; i < C::RB / 32; ++i) {
+            const int r = (lane + 32 * i) / C::UPR;
+            copy16_or_zero(to + C::at(r, (lane + 32 * i) % C::UPR), codes + 512 * i, (w >> r) & 1u ? 16u : 0u);
+          }
+          if (C::SB > 0 && lane < C::SB) copy16_or_zero(to + 16 * C::RB + 16 * lane, scales, w & 0xFFFFu ? 16u : 0u);
+        }
       }
       if (lane == 0) masks[put] = word;
     }
@@ -306,177 +357,187 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
     kg = *a.kv.k_global;
     vg = *a.kv.v_global * 128.0f;  // the values' f16 are 2^-7 of them
   }
+  const float cap = a.softcap * 1.4426950408889634f;
 
   // ---- one pair after another
   for (; !at.done(); at.next(a, hrs)) {
     const int h = at.hr / tiles, r0 = (at.hr - h * tiles) * KA_ROWS, rows = G - r0 < KA_ROWS ? G - r0 : KA_ROWS;
-    const uint16_t* qrow = a.q + ((at.b * H + h) * G + r0) * (int64_t)D;
-    uint32_t qa[C::QS ? 1 : KS][4];
-    float qscale[2];
-    {
-      // the lane's dims of rows g and g + 8: two pairs of each 16-dim step
-      uint32_t raw[KS][4];
+    const int64_t q0 = (at.b * H + h) * G + r0;  // the tile's first query head
+    uint32_t qb[C::QS ? 1 : KS][NT][2];  // B fragments: head 8 x + g, two pairs of dims of each 16-dim step
+    float qscale[NT][2];                 // of heads 8 x + 2 c and the next
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      uint32_t raw[KS][2];
+      const bool live = 8 * x + g < rows;
+      const uint16_t* p = a.q + (q0 + 8 * x + g) * D;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const int d0 = BF ? 16 * s + 2 * c : (KIND == HQ_KV_E4M3 ? 16 * s + 4 * c : 32 * (s / 2) + 8 * c + 4 * (s & 1));
+        const int d0 = BF ? 16 * s + 2 * c : (F8 ? 16 * s + 4 * c : 32 * (s / 2) + 8 * c + 4 * (s & 1));
         const int d1 = BF ? d0 + 8 : d0 + 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool live = g + 8 * i < rows;
-          const uint16_t* p = qrow + (int64_t)(g + 8 * i) * D;
-          raw[s][i] = live ? *reinterpret_cast<const uint32_t*>(p + d0) : 0u;
-          raw[s][2 + i] = live ? *reinterpret_cast<const uint32_t*>(p + d1) : 0u;
-        }
+        raw[s][0] = live ? *reinterpret_cast<const uint32_t*>(p + d0) : 0u;
+        raw[s][1] = live ? *reinterpret_cast<const uint32_t*>(p + d1) : 0u;
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        qscale[i] = a.scale;
-        if constexpr (!BF) {
-          float top = 0.0f;
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[s][2 + i])), fabsf(bf16_hi(raw[s][2 + i]))));
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest magnitude goes to [1, 2)
-          e = top == 0.0f ? 0 : (e < -100 ? -100 : (e > 100 ? 100 : e));
-          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-          qscale[i] *= kg * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            raw[s][i] = pack_f16x2(bf16_lo(raw[s][i]) * f, bf16_hi(raw[s][i]) * f);
-            raw[s][2 + i] = pack_f16x2(bf16_lo(raw[s][2 + i]) * f, bf16_hi(raw[s][2 + i]) * f);
-          }
-        }
-        qscale[i] *= a.softcap > 0.0f ? 2.0f * 1.4426950408889634f / a.softcap : 1.4426950408889634f;
-      }
-      if constexpr (C::QS) {
-        if (warp == 0) {
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-            *reinterpret_cast<uint4*>(qsm + (s * 32 + lane) * 4) =
-                make_uint4(raw[s][0], raw[s][1], raw[s][2], raw[s][3]);
-        }
-        __syncthreads();
-      } else {
+      float back = 1.0f;
+      if constexpr (!BF) {
+        float top = 0.0f;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qa[s][i] = raw[s][i];
+          for (int i = 0; i < 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest magnitude goes to [1, 2)
+        e = top == 0.0f ? 0 : (e < -100 ? -100 : (e > 100 ? 100 : e));
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+        back = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) raw[s][i] = pack_f16x2(bf16_lo(raw[s][i]) * f, bf16_hi(raw[s][i]) * f);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        qscale[x][k] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + k)) * kg * a.scale;
+        qscale[x][k] *= a.softcap > 0.0f ? 2.0f * 1.4426950408889634f / a.softcap : 1.4426950408889634f;
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if constexpr (C::QS) {
+          if (warp == 0)
+            *reinterpret_cast<uint2*>(qsm + ((s * NT + x) * 32 + lane) * 2) = make_uint2(raw[s][0], raw[s][1]);
+        } else {
+          qb[s][x][0] = raw[s][0];
+          qb[s][x][1] = raw[s][1];
+        }
       }
     }
-    float o[NT][4];
+    if constexpr (C::QS) __syncthreads();
+    auto qfrag = [&](int s, int x, uint32_t (&f)[2]) {
+      if constexpr (C::QS) {
+        const uint2 v = *reinterpret_cast<const uint2*>(qsm + ((s * NT + x) * 32 + lane) * 2);
+        f[0] = v.x, f[1] = v.y;
+      } else {
+        f[0] = qb[s][x][0], f[1] = qb[s][x][1];
+      }
+    };
+    float o[KS][NT][4];  // o^T: 16 dims by 8 heads
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][x][i] = 0.0f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = KA_NONE, l[x][0] = l[x][1] = 0.0f;
 
     const int end = at.to();
 #pragma unroll 1
-    for (int tok = at.from() + KV_BLOCK * warp; tok < end; tok += KV_BLOCK * KA_WARPS) {
-      // ---- keys
+    for (int tok = at.from() + 16 * TB * warp; tok < end; tok += STRIDE) {
+      // ---- keys: s^T = K q^T, two sums of every other step (a shorter chain)
       cp_async_wait_group<C::SLOTS - 2>();
       __syncwarp();
       issue();
       const uint32_t kslot = ring_at + get * C::SLOT;
-      const uint8_t* kscale = ring + get * C::SLOT + 16 * C::RB;
+      const uint8_t* kslot_p = ring + get * C::SLOT;
       const uint32_t seen = masks[get];
       get = get + 1 == C::SLOTS ? 0 : get + 1;
-      float s[2][4];
+      const int lr = lane & 15, lu = lane >> 4;  // ldmatrix: 16 tokens by two units
+      float s[TB][NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TB; ++t) {
+        const uint32_t kb = kslot + t * C::BLOCK;
+        const uint8_t* kscale = kslot_p + t * C::BLOCK + 16 * C::RB;
+        float s2[2][NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
-      const int lr = (lane & 7) + ((lane >> 4) << 3), lu = (lane >> 3) & 1;  // ldmatrix: tokens by two units
-      auto qfrag = [&](int k, uint32_t (&f)[4]) {
-        if constexpr (C::QS) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qsm + (k * 32 + lane) * 4);
-          f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-        } else {
+        for (int i = 0; i < 2 * NT * 4; ++i) (&s2[0][0][0])[i] = 0.0f;
+        if constexpr (BF) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = qa[k][i];
-        }
-      };
-      if constexpr (BF) {
+          for (int k = 0; k < KS; ++k) {
+            uint32_t r[4], f[2];
+            ldsm_x4(kb + C::at(lr, 2 * k + lu), r[0], r[1], r[2], r[3]);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t b[4], f[4];
-          ldsm_x4(kslot + C::at(lr, 2 * k + lu), b[0], b[1], b[2], b[3]);
-          qfrag(k, f);
-          mma16<true>(s[0], f, b[0], b[1]);
-          mma16<true>(s[1], f, b[2], b[3]);
-        }
-      } else if constexpr (KIND == HQ_KV_E4M3) {
-#pragma unroll
-        for (int k = 0; k < KS; k += 2) {  // a unit is 16 dims: one step
-          uint32_t b[4], f[4];
-          ldsm_x4(kslot + C::at(lr, k + lu), b[0], b[1], b[2], b[3]);
-          qfrag(k, f);
-          mma16<false>(s[0], f, e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[0] >> 16));
-          mma16<false>(s[1], f, e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[2] >> 16));
-          qfrag(k + 1, f);
-          mma16<false>(s[0], f, e4m3x2_to_f16x2(b[1]), e4m3x2_to_f16x2(b[1] >> 16));
-          mma16<false>(s[1], f, e4m3x2_to_f16x2(b[3]), e4m3x2_to_f16x2(b[3] >> 16));
-        }
-      } else {
-        // a unit is 32 dims: two steps, two block scales; lanes c = 0, 1 hold the first block's dims
-        uint32_t f16s[2][D / 32];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(kscale + (g + 8 * t) * C::SB + 4 * w);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t y = c < 2 ? __byte_perm(x, 0, i ? 0x22 : 0x00) : __byte_perm(x, 0, i ? 0x33 : 0x11);
-              f16s[t][2 * w + i] = e4m3x2_to_f16x2(y);
+            for (int x = 0; x < NT; ++x) {
+              qfrag(k, x, f);
+              mma16<true>(s2[k & 1][x], r[0], r[1], r[2], r[3], f[0], f[1]);
             }
           }
+        } else if constexpr (F8) {
 #pragma unroll
-        for (int u = 0; u < D / 32; u += 2) {
-          uint32_t b[4], f[4];
-          ldsm_x4(kslot + C::at(lr, u + lu), b[0], b[1], b[2], b[3]);
+          for (int k = 0; k < KS; k += 2) {  // a unit is 16 dims: one step
+            uint32_t r[4], f[2];
+            ldsm_x4(kb + C::at(lr, k + lu), r[0], r[1], r[2], r[3]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a0 = e4m3x2_to_f16x2(r[2 * i]), a1 = e4m3x2_to_f16x2(r[2 * i + 1]),
+                             a2 = e4m3x2_to_f16x2(r[2 * i] >> 16), a3 = e4m3x2_to_f16x2(r[2 * i + 1] >> 16);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              qfrag(2 * (u + i) + p, f);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t x = b[2 * t + i] >> (16 * p);
-                mma16<false>(s[t], f, hmul2(e2m1x2_to_f16x2(x & 0xFFu), f16s[t][u + i]),
-                             hmul2(e2m1x2_to_f16x2((x >> 8) & 0xFFu), f16s[t][u + i]));
+              for (int x = 0; x < NT; ++x) {
+                qfrag(k + i, x, f);
+                mma16<false>(s2[i][x], a0, a1, a2, a3, f[0], f[1]);
               }
             }
           }
+        } else {
+          // a unit is 32 dims: two steps, two block scales; lanes c = 0, 1 hold the first block's dims
+          uint32_t sc[2][D / 32];  // of tokens g and g + 8
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              uint32_t x = *reinterpret_cast<const uint32_t*>(kscale + (g + 8 * i) * C::SB + 4 * w);
+              x = c < 2 ? x : x >> 8;
+              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x00));
+              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x22));
+            }
+#pragma unroll
+          for (int u = 0; u < D / 32; u += 2) {
+            uint32_t r[4], f[2];
+            ldsm_x4(kb + C::at(lr, u + lu), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t y = r[2 * i] >> (16 * p), z = r[2 * i + 1] >> (16 * p);
+                const uint32_t a0 = hmul2(e2m1x2_to_f16x2(y), sc[0][u + i]),
+                               a1 = hmul2(e2m1x2_to_f16x2(z), sc[1][u + i]),
+                               a2 = hmul2(e2m1x2_to_f16x2(y >> 8), sc[0][u + i]),
+                               a3 = hmul2(e2m1x2_to_f16x2(z >> 8), sc[1][u + i]);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                  qfrag(2 * (u + i) + p, x, f);
+                  mma16<false>(s2[p][x], a0, a1, a2, a3, f[0], f[1]);
+                }
+              }
+          }
         }
-      }
-
-      // ---- scores: rows g and g + 8 (i >> 1), tokens 8 t + 2 c + (i & 1)
-      float vl[2][2];  // e4m3: log2 of the value scales
+        // ---- scores: tokens g (+ 8: i >> 1), heads 2 c (+ 1: i & 1)
+        float ks[2] = {1.0f, 1.0f};
+        if constexpr (F8) {
+          ks[0] = *reinterpret_cast<const float*>(kscale + 4 * g);
+          ks[1] = *reinterpret_cast<const float*>(kscale + 4 * g + 32);
+        }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float2 ks = make_float2(1.0f, 1.0f);
-        if constexpr (KIND == HQ_KV_E4M3) ks = *reinterpret_cast<const float2*>(kscale + 4 * (8 * t + 2 * c));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] *= qscale[i >> 1] * ((i & 1) ? ks.y : ks.x);
-      }
-      if (a.softcap > 0.0f) {  // cap * tanh(x) = cap * (1 - 2 / (1 + e^2x)); the scores hold 2 x log2 e
-        const float cap = a.softcap * 1.4426950408889634f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[t][i] = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(fminf(s[t][i], 80.0f))));
-      }
-      if (seen != 0xFFFFu) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (!((seen >> (8 * t + 2 * c + (i & 1))) & 1u)) s[t][i] = -INFINITY;
+            s[t][x][i] = (s2[0][x][i] + s2[1][x][i]) * (F8 ? qscale[x][i & 1] * ks[i >> 1] : qscale[x][i & 1]);
+      }
+      if (a.softcap > 0.0f) {  // cap * tanh(y) = cap * (1 - 2 / (1 + e^2y)); the scores hold 2 y log2 e
+#pragma unroll
+        for (int i = 0; i < TB * NT * 4; ++i) {
+          float& y = (&s[0][0][0])[i];
+          y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(fminf(y, 80.0f))));
+        }
+      }
+      if (seen != FULL) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!((seen >> (16 * t + g + 8 * (i >> 1))) & 1u)) s[t][x][i] = -INFINITY;
       }
 
       // ---- values
@@ -484,178 +545,190 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
       __syncwarp();
       issue();
       const uint32_t vslot = ring_at + get * C::SLOT;
-      uint8_t* vscale = ring + get * C::SLOT + 16 * C::RB;
+      uint8_t* vslot_p = ring + get * C::SLOT;
       get = get + 1 == C::SLOTS ? 0 : get + 1;
-      if constexpr (KIND == HQ_KV_E4M3) {
+      float vl[TB][2];  // log2 of the value scales of tokens g and g + 8
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float2 v = *reinterpret_cast<const float2*>(vscale + 4 * (8 * t + 2 * c));
-          vl[t][0] = lg2(fmaxf(v.x, 7.8886091e-31f));  // 2^-100: a smaller scale's values are all but zero
-          vl[t][1] = lg2(fmaxf(v.y, 7.8886091e-31f));
+      for (int t = 0; t < TB; ++t) {
+        vl[t][0] = vl[t][1] = 0.0f;
+        if constexpr (F8) {  // a scale under 2^-100 counts as that: its values are as good as zero
+          const uint8_t* vscale = vslot_p + t * C::BLOCK + 16 * C::RB;
+          vl[t][0] = lg2(fmaxf(*reinterpret_cast<const float*>(vscale + 4 * g), 7.8886091e-31f));
+          vl[t][1] = lg2(fmaxf(*reinterpret_cast<const float*>(vscale + 4 * g + 32), 7.8886091e-31f));
         }
       }
       if constexpr (KIND == HQ_KV_NVFP4) {
-        if (seen != 0xFFFFu) {  // scales of tokens that are not seen: zero codes times them must be zero
-          if (lane < 16 && !((seen >> lane) & 1u)) {
+        if (seen != FULL) {  // scales of tokens that are not seen: zero codes times them must be zero
+          if (lane < 16 * TB && !((seen >> lane) & 1u)) {
+            uint8_t* z = vslot_p + (lane / 16) * C::BLOCK + 16 * C::RB + (lane % 16) * C::SB;
 #pragma unroll
-            for (int w = 0; w < C::SB / 4; ++w) *reinterpret_cast<uint32_t*>(vscale + lane * C::SB + 4 * w) = 0u;
+            for (int w = 0; w < C::SB / 4; ++w) *reinterpret_cast<uint32_t*>(z + 4 * w) = 0u;
           }
           __syncwarp();
         }
       }
-      // running maximum: of s, or of s + log2 of the value scale
-      float f[2] = {1.0f, 1.0f};
-      bool moved = false;
+      // ---- weights; the running maximum is of s, or of s + log2 of the value scale
+      bool over = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = -INFINITY;
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int k = 0; k < 2; ++k) {
+          float y = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < TB; ++t)
+            y = fmaxf(y, F8 ? fmaxf(s[t][x][k] + vl[t][0], s[t][x][k + 2] + vl[t][1])
+                            : fmaxf(s[t][x][k], s[t][x][k + 2]));
+          over |= y > m[x][k] + KA_LAZY;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float y = KIND == HQ_KV_E4M3 ? s[t][2 * i + k] + vl[t][k] : s[t][2 * i + k];
-            x = fmaxf(x, y);
+            float y = m[x][k];
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+              y = fmaxf(y, F8 ? fmaxf(s[t][x][k] + vl[t][0], s[t][x][k + 2] + vl[t][1])
+                              : fmaxf(s[t][x][k], s[t][x][k + 2]));
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, i));
+            const float f = ex2(m[x][k] - y);
+            m[x][k] = y;
+            l[x][k] *= f;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) o[j][x][k] *= f, o[j][x][k + 2] *= f;
           }
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        if (x > m[i] + KA_LAZY || (m[i] == -INFINITY && x > m[i])) {
-          f[i] = ex2(m[i] - x);
-          m[i] = x;
-          moved = true;
-        }
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      uint32_t pb[TB][NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int t = 0; t < TB; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= f[i >> 1];
-        l[0] *= f[0];
-        l[1] *= f[1];
-      }
-      uint32_t p[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mm = m[i] == -INFINITY ? 0.0f : m[i];
-          float w[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float e = ex2(s[t][2 * i + k] - mm);
-            l[i] += e;
-            w[k] = KIND == HQ_KV_E4M3 ? ex2(s[t][2 * i + k] + vl[t][k] - mm) : e;
-          }
-          p[2 * t + i] = BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]);
-        }
-      const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vu = lane >> 4;
-      if constexpr (BF) {
-#pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          uint32_t b[4];
-          ldsm4t(b, vslot + C::at(vr, j + vu));
-          mma16<true>(o[j], p, b[0], b[1]);
-          mma16<true>(o[j + 1], p, b[2], b[3]);
-        }
-      } else if constexpr (KIND == HQ_KV_E4M3) {
-        // a unit is 16 dims: a lane gets dims 2g, 2g + 1 of tokens 2c, 2c + 1; tiles of the even and of the odd dims
-#pragma unroll
-        for (int u = 0; u < D / 16; u += 2) {
-          uint32_t b[4];
-          ldsm4t(b, vslot + C::at(vr, u + vu));
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t x = __byte_perm(b[2 * i], 0, 0x3120), y = __byte_perm(b[2 * i + 1], 0, 0x3120);
-            mma16<false>(o[2 * (u + i)], p, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-            mma16<false>(o[2 * (u + i) + 1], p, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+            float w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float y = s[t][x][2 * i + k] - m[x][k], e = ex2(y);
+              l[x][k] += e;
+              w[k] = F8 ? ex2(y + vl[t][i]) : e;
+            }
+            pb[t][x][i] = turn8x8(BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]));
           }
-        }
-      } else {
-        // a unit is 32 dims: a lane gets dims 4g .. 4g + 3 of tokens 2c, 2c + 1; four tiles, dims 4n + i each
-        uint32_t vs[2][D / 32];  // f16x2 of the two tokens' scales * 2^7
-        const uint32_t sel = g < 4 ? 0x0040u : 0x0051u;  // the first or second block's byte of each token
+      // ---- o^T += V^T p^T
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TB; ++t) {
+        const uint32_t vb = vslot + t * C::BLOCK;
+        const uint8_t* vscale = vslot_p + t * C::BLOCK + 16 * C::RB;
+        if constexpr (BF) {
 #pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            const uint32_t x = *reinterpret_cast<const uint32_t*>(vscale + (8 * t + 2 * c) * C::SB + 4 * w);
-            const uint32_t y = *reinterpret_cast<const uint32_t*>(vscale + (8 * t + 2 * c + 1) * C::SB + 4 * w);
-            vs[t][2 * w] = hmul2(e4m3x2_to_f16x2(__byte_perm(x, y, sel)), 0x58005800u);
-            vs[t][2 * w + 1] = hmul2(e4m3x2_to_f16x2(__byte_perm(x, y, sel + 0x0022u)), 0x58005800u);
+          for (int j = 0; j < KS; ++j) {
+            uint32_t r[4];
+            ldsm_x4_t(vb + C::at(lr, 2 * j + lu), r);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) mma16<true>(o[j][x], r[0], r[2], r[1], r[3], pb[t][x][0], pb[t][x][1]);
           }
+        } else if constexpr (F8) {
+          // a unit is 16 dims: a lane gets dims 2 g, 2 g + 1 of two tokens; even dims are rows 0-7, odd ones 8-15
 #pragma unroll
-        for (int u = 0; u < D / 32; u += 2) {
-          uint32_t b[4];
-          ldsm4t(b, vslot + C::at(vr, u + vu));
+          for (int u = 0; u < KS; u += 2) {
+            uint32_t r[4];
+            ldsm_x4_t(vb + C::at(lr, u + lu), r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t y = __byte_perm(r[2 * i], 0, 0x3120), z = __byte_perm(r[2 * i + 1], 0, 0x3120);
+              const uint32_t a0 = e4m3x2_to_f16x2(y), a1 = e4m3x2_to_f16x2(y >> 16), a2 = e4m3x2_to_f16x2(z),
+                             a3 = e4m3x2_to_f16x2(z >> 16);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16<false>(o[u + i][x], a0, a1, a2, a3, pb[t][x][0], pb[t][x][1]);
+            }
+          }
+        } else {
+          // a unit is 32 dims: a lane gets dims 4 g .. 4 g + 3 of two tokens; two tiles of two of them each
+          uint32_t sc[2][D / 32];  // of tokens 2 c, 2 c + 1, and 8 on, times 2^7
+          const uint32_t sel = g < 4 ? 0x0040u : 0x0051u;  // the first or second block's byte of each token
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              mma16<false>(o[4 * (u + i) + n], p, hmul2(e2m1_pair(b[2 * i], n), vs[0][u + i]),
-                           hmul2(e2m1_pair(b[2 * i + 1], n), vs[1][u + i]));
+            for (int w = 0; w < D / 64; ++w) {
+              const uint32_t y = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c) * C::SB + 4 * w);
+              const uint32_t z = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c + 1) * C::SB + 4 * w);
+              sc[i][2 * w] = hmul2(e4m3x2_to_f16x2(__byte_perm(y, z, sel)), 0x58005800u);
+              sc[i][2 * w + 1] = hmul2(e4m3x2_to_f16x2(__byte_perm(y, z, sel + 0x0022u)), 0x58005800u);
+            }
+#pragma unroll
+          for (int u = 0; u < D / 32; u += 2) {
+            uint32_t r[4];
+            ldsm_x4_t(vb + C::at(lr, u + lu), r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const uint32_t a0 = hmul2(e2m1_pair(r[2 * i], 2 * n), sc[0][u + i]),
+                               a1 = hmul2(e2m1_pair(r[2 * i], 2 * n + 1), sc[0][u + i]),
+                               a2 = hmul2(e2m1_pair(r[2 * i + 1], 2 * n), sc[1][u + i]),
+                               a3 = hmul2(e2m1_pair(r[2 * i + 1], 2 * n + 1), sc[1][u + i]);
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                  mma16<false>(o[2 * (u + i) + n][x], a0, a1, a2, a3, pb[t][x][0], pb[t][x][1]);
+              }
+          }
         }
       }
     }
 
-    // ---- join the four warps, eight rows at a time, and write the pair's result or its part
+    // ---- join the four warps, eight heads at a time, and write the pair's result or its part
     const bool whole = at.u == at.seg0 && at.stop() == at.seg0 + at.s.units;
-    const int64_t pair = at.b * hrs + at.hr;
-    const int64_t my_slot = 2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1);
-    float* part = slots + my_slot * KA_SLOT_FLOATS;
+    float* part = slots + (2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1)) * KA_SLOT_FLOATS;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int x = 0; x < NT; ++x) {
+      if (8 * x >= rows) break;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (8 * i >= rows) break;
-      if (c == 0) {
-        mls[(warp * 8 + g) * 2] = m[i];
-        mls[(warp * 8 + g) * 2 + 1] = l[i];
-      }
-      float* to = merge + (warp * 8 + g) * (D + C::PAD);
-      if constexpr (BF) {
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          *reinterpret_cast<float2*>(to + 8 * j + 2 * c) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-      } else if constexpr (KIND == HQ_KV_E4M3) {
+        for (int i = 4; i < 32; i <<= 1) l[x][k] += __shfl_xor_sync(0xffffffffu, l[x][k], i);
+        if (g == 0) {
+          mls[(warp * 8 + 2 * c + k) * 2] = m[x][k];
+          mls[(warp * 8 + 2 * c + k) * 2 + 1] = l[x][k];
+        }
+        float* to = merge + (warp * 8 + 2 * c + k) * (D + C::PAD);
+        if constexpr (BF) {
 #pragma unroll
-        for (int j = 0; j < NT; j += 2)
-          *reinterpret_cast<float4*>(to + 8 * j + 4 * c) =
-              make_float4(o[j][2 * i], o[j + 1][2 * i], o[j][2 * i + 1], o[j + 1][2 * i + 1]);
-      } else {
+          for (int j = 0; j < KS; ++j) {
+            to[16 * j + g] = o[j][x][k];
+            to[16 * j + 8 + g] = o[j][x][k + 2];
+          }
+        } else if constexpr (F8) {
 #pragma unroll
-        for (int j = 0; j < NT; j += 4)
+          for (int j = 0; j < KS; ++j)
+            *reinterpret_cast<float2*>(to + 16 * j + 2 * g) = make_float2(o[j][x][k], o[j][x][k + 2]);
+        } else {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(to + 8 * j + 8 * c + 4 * k) =
-                make_float4(o[j][2 * i + k], o[j + 1][2 * i + k], o[j + 2][2 * i + k], o[j + 3][2 * i + k]);
+          for (int j = 0; j < KS; j += 2)
+            *reinterpret_cast<float4*>(to + 16 * j + 4 * g) =
+                make_float4(o[j][x][k], o[j][x][k + 2], o[j + 1][x][k], o[j + 1][x][k + 2]);
+        }
       }
       __syncthreads();
-      const int some = rows - 8 * i < 8 ? rows - 8 * i : 8;
+      const int some = rows - 8 * x < 8 ? rows - 8 * x : 8;
       for (int e = threadIdx.x; e < some * (D / 4); e += KA_THREADS) {
         const int r = e / (D / 4), d = 4 * (e % (D / 4));
-        float top = -INFINITY, sum = 0.0f;
+        float top = KA_NONE, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < KA_WARPS; ++w) top = fmaxf(top, mls[(w * 8 + r) * 2]);
         float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < KA_WARPS; ++w) {
-          const float mw = mls[(w * 8 + r) * 2], x = mw == -INFINITY ? 0.0f : ex2(mw - top);
+          const float f = ex2(mls[(w * 8 + r) * 2] - top);
           const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + r) * (D + C::PAD) + d);
-          sum = fmaf(x, mls[(w * 8 + r) * 2 + 1], sum);
-          y.x = fmaf(x, v.x, y.x), y.y = fmaf(x, v.y, y.y), y.z = fmaf(x, v.z, y.z), y.w = fmaf(x, v.w, y.w);
+          sum = fmaf(f, mls[(w * 8 + r) * 2 + 1], sum);
+          y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
         }
-        const int row = 8 * i + r;
         if (whole) {
-          const float inv = sum > 0.0f ? vg / sum : 0.0f;
-          const int64_t q = (at.b * H + h) * G + r0 + row;
-          *reinterpret_cast<uint2*>(a.out + q * D + d) =
-              make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-          if (d == 0 && a.lse) a.lse[q] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          ka_store(a, q0 + 8 * x + r, D, d, y, top, sum, vg);
         } else {
-          __stcg(reinterpret_cast<float4*>(part + row * D + d), y);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(part + part_rows * D + 2 * row), make_float2(top, sum));
+          __stcg(reinterpret_cast<float4*>(part + (8 * x + r) * D + d), y);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(part + part_rows * D + 2 * (8 * x + r)), make_float2(top, sum));
         }
       }
       __syncthreads();
@@ -664,6 +737,7 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
 
     // ---- split pair: the last CTA to arrive joins the parts, first to last
     const int64_t c0 = ((at.seg0 + 1) * W - 1) / total, c1 = ((at.seg0 + at.s.units) * W - 1) / total;
+    const int64_t pair = at.b * hrs + at.hr;
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) found[2] = atomicAdd(counters + pair, 1) == (int)(c1 - c0);
@@ -673,39 +747,52 @@ __global__ void __launch_bounds__(KA_THREADS, 2) kv_attention_kernel(const KvAtt
     const int parts = (int)(c1 - c0) + 1;
     const int64_t s0 = 2 * c0 + (total * c0 / W == at.seg0 ? 0 : 1);  // the others' first pair is this one
     for (int e = threadIdx.x; e < rows * (D / 4); e += KA_THREADS) {
-      const int row = e / (D / 4), d = 4 * (e % (D / 4));
-      float top = -INFINITY, sum = 0.0f;
-      for (int k = 0; k < parts; ++k) {
-        const float* x = slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS;
-        top = fmaxf(top, __ldcg(x + part_rows * D + 2 * row));
-      }
+      const int r = e / (D / 4), d = 4 * (e % (D / 4));
+      float top = KA_NONE, sum = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k)
+        top = fmaxf(top, __ldcg(slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS + part_rows * D + 2 * r));
       float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
       for (int k = 0; k < parts; ++k) {
-        const float* x = slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(x + part_rows * D + 2 * row));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(x + row * D + d));
-        const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-        sum = fmaf(w, ml.y, sum);
-        y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+        const float* p = slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + part_rows * D + 2 * r));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+        const float f = ex2(ml.x - top);
+        sum = fmaf(f, ml.y, sum);
+        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
       }
-      const float inv = sum > 0.0f ? vg / sum : 0.0f;
-      const int64_t q = (at.b * H + h) * G + r0 + row;
-      *reinterpret_cast<uint2*>(a.out + q * D + d) =
-          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-      if (d == 0 && a.lse) a.lse[q] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      ka_store(a, q0 + r, D, d, y, top, sum, vg);
     }
     if (threadIdx.x == 0) counters[pair] = 0;
   }
   cp_async_wait_all();
 }
 
-template <int KIND, int D>
-cudaError_t launch_ka(const KvAttnArgs& a, int ctas, float* slots, int* counters, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<KIND, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             KaCfg<KIND, D>::SMEM);
+template <int KIND, int D, int NT>
+cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, float* slots, int* counters, cudaStream_t stream) {
+  using C = KaCfg<KIND, D, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<KIND, D, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kv_attention_kernel<KIND, D>, dim3((unsigned)ctas), dim3(KA_THREADS), KaCfg<KIND, D>::SMEM,
-                       stream, a, slots, counters);
+  // no more CTAs than four units each of the longest lengths
+  const int64_t per = (tokens + 16 * C::TB - 1) / (16 * C::TB);
+  const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
+  const int64_t want = (pairs * (per > 0 ? per : 1) + 3) / 4, all = (int64_t)C::CTAS * sms;
+  return launch_kernel(kv_attention_kernel<KIND, D, NT>, dim3((unsigned)(want < all ? want : all)), dim3(KA_THREADS),
+                       C::SMEM, stream, a, slots, counters);
+}
+
+template <int KIND>
+cudaError_t launch_ka_dim(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots, int* counters,
+                          cudaStream_t stream) {
+  if (a.group <= 8)
+    return dim == 64 ? launch_ka<KIND, 64, 1>(a, sms, tokens, slots, counters, stream)
+                     : (dim == 128 ? launch_ka<KIND, 128, 1>(a, sms, tokens, slots, counters, stream)
+                                   : launch_ka<KIND, 256, 1>(a, sms, tokens, slots, counters, stream));
+  return dim == 64 ? launch_ka<KIND, 64, 2>(a, sms, tokens, slots, counters, stream)
+                   : (dim == 128 ? launch_ka<KIND, 128, 2>(a, sms, tokens, slots, counters, stream)
+                                 : launch_ka<KIND, 256, 2>(a, sms, tokens, slots, counters, stream));
 }
 
 #endif  // __CUDACC__

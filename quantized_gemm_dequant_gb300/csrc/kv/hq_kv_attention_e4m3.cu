@@ -3,11 +3,9 @@
 
 namespace hq {
 
-cudaError_t launch_kv_attention_e4m3(int dim, const KvAttnArgs& a, int ctas, float* slots, int* counters,
-                                     cudaStream_t stream) {
-  return dim == 64 ? launch_ka<HQ_KV_E4M3, 64>(a, ctas, slots, counters, stream)
-                   : (dim == 128 ? launch_ka<HQ_KV_E4M3, 128>(a, ctas, slots, counters, stream)
-                                 : launch_ka<HQ_KV_E4M3, 256>(a, ctas, slots, counters, stream));
+cudaError_t launch_kv_attention_e4m3(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots,
+                                    int* counters, cudaStream_t stream) {
+  return launch_ka_dim<HQ_KV_E4M3>(dim, a, sms, tokens, slots, counters, stream);
 }
 
 }  // namespace hq
