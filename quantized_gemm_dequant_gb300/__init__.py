@@ -10,6 +10,7 @@ index checks that report HQ_ERR_BOUNDS through the workspace status.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -67,6 +68,9 @@ class KVRows(ctypes.Structure):
                 ("slots", ctypes.c_void_p), ("q_out", ctypes.c_void_p)]
 
 
+_KV_ROWS = struct.Struct("@PqqiiifPPPqPPP")  # KVRows, packed in one step
+
+
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _F = ctypes.POINTER(Format)
 _A = ctypes.POINTER(Act)
@@ -107,7 +111,7 @@ _lib.hq_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.hq_set_wait_limit_ns.restype = None
 _lib.hq_kv_workspace_bytes.argtypes = [_KF, _i64, _i32]
 _lib.hq_kv_workspace_bytes.restype = _sz
-_lib.hq_kv_write.argtypes = [_KF, _KP, ctypes.POINTER(KVRows), _vp, _sz, _vp]
+_lib.hq_kv_write.argtypes = [_KF, _KP, _vp, _vp, _sz, _vp]
 _lib.hq_kv_write.restype = ctypes.c_int
 _lib.hq_kv_read.argtypes = [_KF, _KP, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_read.restype = ctypes.c_int
@@ -528,7 +532,7 @@ class KVCache:
                 raise HQArgError(w, f"{name} is {'required' if code == HQ_KV_NVFP4 else 'not used'} by a {kind} cache")
             args.add(t, name, 4, _F32)
         args.ptrs()
-        self.kind, self.device = kind, k.device
+        self.kind, self.device, self._index = kind, k.device, k.device.index
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.k_global, self.v_global = k_global, v_global
         self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, heads, page, dim
@@ -593,7 +597,7 @@ def _kv_ptrs(w, c, items):
     """Addresses of a call's tensors: items are (tensor or None, name, elements that the call reads or writes, dtype or
     None).  One look at each right tensor, because a decoding step makes this call for every layer; at the first one
     that is not, _Args judges them all and raises."""
-    dev, out = c.device.index, []
+    dev, out = c._index, []
     for t, _, n, dt in items:
         if t is None:
             out.append(None)
@@ -612,7 +616,7 @@ def _kv_ptrs(w, c, items):
 
 
 def _kv_stream(c, stream):
-    return torch._C._cuda_getCurrentRawStream(c.device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(c._index) if stream is None else stream.cuda_stream
 
 
 def _kv_table(w, page_table, batch):
@@ -655,13 +659,14 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
         (positions if R else None, "positions", T, torch.int32), (q_out, "q_out", T * Hq * D, bf16),
         (workspace, "workspace", 0, None)))
     if q_out is None:
-        q_out = _on(stream, qkv.new_empty, (T, Hq, D))
+        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=bf16, device=c.device)
         pq = q_out.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
         pws = workspace.data_ptr()
-    r = KVRows(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl, pq)
-    _check(_lib.hq_kv_write(*c._refs, ctypes.byref(r), pws, _nbytes(workspace), _kv_stream(c, stream)), w)
+    r = _KV_ROWS.pack(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn or 0, pkn or 0, pcs or 0, P, pps or 0,
+                      psl or 0, pq)
+    _check(_lib.hq_kv_write(*c._refs, r, pws, workspace.numel() * workspace.element_size(), _kv_stream(c, stream)), w)
     return q_out
 
 
@@ -710,10 +715,10 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
         (lens, "lens", B, torch.int32), (out, "out", size, torch.bfloat16), (lse, "lse", B * Hq, torch.float32),
         (workspace, "workspace", 0, None)))
     if out is None:
-        out = _on(stream, q.new_empty, (B, Hq, D))
+        out = _on(stream, torch.empty_like, q)
         po = out.data_ptr()
     if lse is None:
-        lse = _on(stream, q.new_empty, (B, Hq), dtype=torch.float32)
+        lse = _on(stream, torch.empty, (B, Hq), dtype=torch.float32, device=c.device)
         pl = lse.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, B, Hq, stream=stream)

@@ -34,6 +34,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../hq_launch.h"
 #include "../hq_ptx.cuh"
 #include "hq_kv.h"
@@ -772,9 +774,15 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 template <int KIND, int D, int NT>
 cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, float* slots, int* counters, cudaStream_t stream) {
   using C = KaCfg<KIND, D, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<KIND, D, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel has its shared memory (a bit each)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(allowed.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kv_attention_kernel<KIND, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  }
   // no more CTAs than four units each of the longest lengths
   const int64_t per = (tokens + 16 * C::TB - 1) / (16 * C::TB);
   const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
