@@ -4,11 +4,12 @@
 //   bf16; e4m3 of y / s with s = absmax / 448; or e2m1 of y / d with d = e4m3(absmax_16 / (6 g)) * g.
 // All steps are fp32; the divisions that decide a code are IEEE divisions.
 //
-// Memory-bound: every element is read once and written once.  D / 8 lanes hold a head's row, 8 dims each (one 16-byte
-// load), so a head's sum of squares and largest magnitude are shuffles inside the group, and the rotation's partner
-// dims are a lane's own or another lane's of the group.  A warp takes one token and NS steps of 256 / D heads: all its
-// rows are loaded before the first is worked on, and the angles' cosines and sines (as many bytes as two heads' rows)
-// are loaded once for all of them.  Few tokens take one step a warp instead, which spreads them over the SMs.
+// Memory-bound: every element is read once and written once, and the instructions per element decide whether that is
+// reached.  A CTA takes one token; its four warps take every fourth step of 256 / D heads of one kind (query, key or
+// value), four query steps and the first key and value step in flight at once.  D / 8 lanes hold a head's row.  For a
+// rotation by halves a lane holds four dims of the first half and their four partners, so that the rotation needs no
+// exchange between lanes and a lane's four angles serve both; otherwise it holds eight neighbouring dims.  Sums of
+// squares and largest magnitudes are shuffles inside the head's lanes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -34,164 +35,206 @@ __device__ __forceinline__ float quotient(float x, float y, float yi, bool fast)
 }
 constexpr float KW_FAST = 7.8886091e-31f;  // 2^-100
 
-template <int KIND, int D, int NS>
-__global__ void __launch_bounds__(KW_THREADS) kv_write_kernel(const KvWriteArgs a, int parts) {
-  constexpr int LPH = D / 8;      // lanes of a head's row
-  constexpr int HPW = 32 / LPH;   // heads of one step
-  constexpr int RB = kv_row_bytes(KIND, D);
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, l = lane % LPH, sub = lane / LPH;
-  const int64_t task = (int64_t)blockIdx.x * (KW_THREADS / 32) + (threadIdx.x >> 5);
-  const int64_t t = task / parts;
-  if (t >= a.T) return;
-  const int part = (int)(task - t * parts);
-  const int H = a.kv.heads, Hq = a.q_heads, all = Hq + 2 * H;
-  const int h0 = part * NS * HPW + sub, d0 = 8 * l;
+// A head's row in its lanes: dims lo .. lo + 3 and hi .. hi + 3 of each lane.
+struct Row {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ Row load_row(const uint16_t* p, int lo, int hi, bool live) {
+  Row r;
+  r.lo = live ? __ldcs(reinterpret_cast<const uint2*>(p + lo)) : make_uint2(0, 0);
+  r.hi = live ? __ldcs(reinterpret_cast<const uint2*>(p + hi)) : make_uint2(0, 0);
+  return r;
+}
+__device__ __forceinline__ void unpack_row(const Row& r, float (&x)[8]) {
+  x[0] = bf16_lo(r.lo.x), x[1] = bf16_hi(r.lo.x), x[2] = bf16_lo(r.lo.y), x[3] = bf16_hi(r.lo.y);
+  x[4] = bf16_lo(r.hi.x), x[5] = bf16_hi(r.hi.x), x[6] = bf16_lo(r.hi.y), x[7] = bf16_hi(r.hi.y);
+}
+__device__ __forceinline__ void store_row(uint16_t* p, int lo, int hi, const float (&x)[8]) {
+  *reinterpret_cast<uint2*>(p + lo) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  *reinterpret_cast<uint2*>(p + hi) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
 
-  uint4 raw[NS];
-  const uint16_t* src = a.qkv + t * a.row_stride + (int64_t)h0 * D + d0;
+template <int LPH>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int s = 0; s < NS; ++s)
-    raw[s] = h0 + s * HPW < all ? __ldcs(reinterpret_cast<const uint4*>(src + s * HPW * D)) : make_uint4(0, 0, 0, 0);
+  for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LPH>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float largest(const float (&x)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  return m;
+}
 
-  // the row's place, and its angles
-  const int64_t slot = a.slots[t];
-  const bool cached = slot >= 0 && slot < a.kv.num_pages * a.kv.page_size;
-  if (slot >= 0 && !cached && part == 0 && lane == 0) kv_report(a.status);
-  const int64_t page = cached ? slot / a.kv.page_size : 0;
-  const int off = cached ? (int)(slot - page * a.kv.page_size) : 0;
-  const int half = a.rotary >> 1;
-  const bool turn = d0 < a.rotary;
-  float cs[8], sn[8];  // the rotation is x cs + partner sn
-  int partner = lane;
-  if (a.rotary) {
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.num_positions) {
-      if (part == 0 && lane == 0) kv_report(a.status);
-      return;
-    }
-    const float* row = a.cos_sin + pos * a.rotary;
-    if (turn) {
-      if (a.interleaved) {  // pairs (2i, 2i + 1): four angles, each for two dims
-        const float4 c = *reinterpret_cast<const float4*>(row + d0 / 2);
-        const float4 s = *reinterpret_cast<const float4*>(row + half + d0 / 2);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// Norm (w: the lane's weights; on: whether there is one) and rotation of a row.  The rotated pairs are (x[i], x[i + 4])
+// for a rotation by halves, (x[2 i], x[2 i + 1]) for an interleaved one; cs, sn are their four angles'.
+template <int LPH>
+__device__ __forceinline__ void norm_rotate(float (&x)[8], bool on, const float (&w)[8], float eps, bool turn,
+                                            bool interleaved, const float (&cs)[4], const float (&sn)[4]) {
+  if (on) {
+    float sq = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = cc[i / 2], sn[i] = (i & 1) ? ss[i / 2] : -ss[i / 2];
-      } else {  // dim i pairs with i + half: eight angles
-        const int i0 = d0 < half ? d0 : d0 - half;
-        partner = d0 < half ? lane + half / 8 : lane - half / 8;
-        const float sign = d0 < half ? -1.0f : 1.0f;
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+    const float r = rsqrtf(lanes_sum<LPH>(sq) * (1.0f / (8 * LPH)) + eps);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 c = *reinterpret_cast<const float4*>(row + i0 + 4 * q);
-          const float4 s = *reinterpret_cast<const float4*>(row + half + i0 + 4 * q);
-          cs[4 * q] = c.x, cs[4 * q + 1] = c.y, cs[4 * q + 2] = c.z, cs[4 * q + 3] = c.w;
-          sn[4 * q] = sign * s.x, sn[4 * q + 1] = sign * s.y;
-          sn[4 * q + 2] = sign * s.z, sn[4 * q + 3] = sign * s.w;
-        }
-      }
-    }
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
   }
-  const uint4 wq = a.q_norm ? *reinterpret_cast<const uint4*>(a.q_norm + d0) : make_uint4(0, 0, 0, 0);
-  const uint4 wk = a.k_norm ? *reinterpret_cast<const uint4*>(a.k_norm + d0) : make_uint4(0, 0, 0, 0);
-  const bool any_norm = a.q_norm != nullptr || a.k_norm != nullptr;
-
+  if (!turn) return;
 #pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int h = h0 + s * HPW, first = h - sub;  // the lane's head, the warp's first one
-    if (first >= all) break;
-    const bool live = h < all, is_q = h < Hq, is_k = !is_q && h < Hq + H;
-    float x[8];
-    unpack_bf16x8(raw[s], x);
-    if (first < Hq + H) {  // the warp's query and key heads (its shuffles are whole)
-      if (any_norm) {
-        float sq = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        if (is_q ? a.q_norm != nullptr : (is_k && a.k_norm != nullptr)) {
-          const float r = rsqrtf(sq * (1.0f / D) + a.eps);
-          float w[8];
-          unpack_bf16x8(is_q ? wq : wk, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-        }
-      }
-      if (a.rotary) {
-        float y[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
-        }
-        if (turn && (is_q || is_k)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-        }
-      }
-    }
-    if (is_q) *reinterpret_cast<uint4*>(a.q_out + (t * Hq + h) * D + d0) = pack_bf16x8(x);
-    if (first + HPW <= Hq) continue;  // query heads only
-    // keys and values into the cache
-    const bool put = live && !is_q && cached;
-    const int64_t row = (page * H + (is_k ? h - Hq : h - Hq - H)) * a.kv.page_size + off;
-    uint8_t* dst = (is_k ? a.kv.k : a.kv.v) + row * RB;
-    if constexpr (KIND == HQ_KV_BF16) {
-      if (put) *reinterpret_cast<uint4*>(dst + 16 * l) = pack_bf16x8(x);
+  for (int i = 0; i < 4; ++i) {
+    if (interleaved) {
+      const float p = x[2 * i], q = x[2 * i + 1];
+      x[2 * i] = fmaf(p, cs[i], -q * sn[i]);
+      x[2 * i + 1] = fmaf(q, cs[i], p * sn[i]);
     } else {
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-      if constexpr (KIND == HQ_KV_E4M3) {
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float sc = __fdiv_rn(m, 448.0f), inv = __frcp_rn(sc);
-        const bool fast = sc >= KW_FAST;
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = sc > 0.0f ? pack_e4m3x2(quotient(x[2 * i], sc, inv, fast), quotient(x[2 * i + 1], sc, inv, fast)) : 0u;
-        if (put) {
-          *reinterpret_cast<uint2*>(dst + 8 * l) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-          if (l == 0) reinterpret_cast<float*>(is_k ? a.kv.k_scale : a.kv.v_scale)[row] = sc;
-        }
-      } else {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));  // a block of 16 dims is two lanes
-        const float g = put ? *(is_k ? a.kv.k_global : a.kv.v_global) : 1.0f;
-        const uint32_t sb = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
-        const float d = __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x, g), inv = __frcp_rn(d);
-        const bool fast = d >= KW_FAST;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = d > 0.0f ? quotient(x[i], d, inv, fast) : 0.0f;
-        if (put) {
-          *reinterpret_cast<uint32_t*>(dst + 4 * l) = pack_e2m1x8(y);
-          if (!(l & 1)) (is_k ? a.kv.k_scale : a.kv.v_scale)[row * (D / 16) + l / 2] = (uint8_t)sb;
-        }
-      }
+      const float p = x[i], q = x[i + 4];
+      x[i] = fmaf(p, cs[i], -q * sn[i]);
+      x[i + 4] = fmaf(q, cs[i], p * sn[i]);
     }
   }
 }
 
-template <int KIND, int D, int NS>
-cudaError_t launch_ns(const KvWriteArgs& a, int steps, cudaStream_t stream) {
-  const int parts = (steps + NS - 1) / NS;  // warps of one token
-  const int64_t ctas = (a.T * parts + KW_THREADS / 32 - 1) / (KW_THREADS / 32);
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_kernel(kv_write_kernel<KIND, D, NS>, dim3((unsigned)ctas), dim3(KW_THREADS), 0, stream, a, parts);
+// A row (dims lo .. and hi .. of each lane; NVFP4: eight neighbouring dims) into the pool.  The shuffles are the whole
+// warp's; only lanes that `put` store.
+template <int KIND, int D>
+__device__ __forceinline__ void store_held(uint8_t* codes, uint8_t* scales, const float* global, int64_t row, int l,
+                                           int lo, int hi, const float (&x)[8], bool put) {
+  uint8_t* dst = codes + row * kv_row_bytes(KIND, D);
+  if constexpr (KIND == HQ_KV_BF16) {
+    if (put) store_row(reinterpret_cast<uint16_t*>(dst), lo, hi, x);
+  } else if constexpr (KIND == HQ_KV_E4M3) {
+    const float s = __fdiv_rn(lanes_max<D / 8>(largest(x)), 448.0f), inv = __frcp_rn(s);
+    const bool fast = s >= KW_FAST;
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = s > 0.0f ? pack_e4m3x2(quotient(x[2 * i], s, inv, fast), quotient(x[2 * i + 1], s, inv, fast)) : 0u;
+    if (put) {
+      *reinterpret_cast<uint32_t*>(dst + lo) = c[0] | (c[1] << 16);
+      *reinterpret_cast<uint32_t*>(dst + hi) = c[2] | (c[3] << 16);
+      if (l == 0) reinterpret_cast<float*>(scales)[row] = s;
+    }
+  } else {
+    const float m = lanes_max<2>(largest(x)), g = *global;  // a block of 16 dims is two lanes
+    const uint32_t sb = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
+    const float d = __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x, g), inv = __frcp_rn(d);
+    const bool fast = d >= KW_FAST;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = d > 0.0f ? quotient(x[i], d, inv, fast) : 0.0f;
+    if (put) {
+      *reinterpret_cast<uint32_t*>(dst + 4 * l) = pack_e2m1x8(y);
+      if (!(l & 1)) scales[row * (D / 16) + l / 2] = (uint8_t)sb;
+    }
+  }
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(KW_THREADS) kv_write_kernel(const KvWriteArgs a) {
+  constexpr int LPH = D / 8;     // lanes of a head's row
+  constexpr int HPW = 32 / LPH;  // heads of one step
+  constexpr int WARPS = KW_THREADS / 32, NS = 4;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPH, sub = lane / LPH;
+  const int64_t t = blockIdx.x;
+  const int H = a.kv.heads, Hq = a.q_heads, R = a.rotary;
+  const bool halves = R > 0 && !a.interleaved, turn = 8 * l < R;
+  // the lane's dims: by halves of the rotated part and of the rest, or eight neighbours
+  int lo = 8 * l, hi = 8 * l + 4;
+  if (halves && turn) lo = 4 * l, hi = R / 2 + 4 * l;
+  const uint16_t* qs = a.qkv + t * a.row_stride;
+  const uint16_t* ks = qs + (int64_t)Hq * D;
+  const uint16_t* vs = ks + (int64_t)H * D;
+  const bool neighbours = KIND == HQ_KV_NVFP4 && halves;  // key rows by neighbours all the same: blocks of 16 dims
+  const int klo = neighbours ? 8 * l : lo, khi = neighbours ? 8 * l + 4 : hi;
+  const int kv0 = warp * HPW + sub;
+  Row kr = load_row(ks + (int64_t)kv0 * D, klo, khi, kv0 < H);
+  Row vr = load_row(vs + (int64_t)kv0 * D, 8 * l, 8 * l + 4, kv0 < H);
+
+  const int64_t slot = a.slots[t];
+  const bool cached = slot >= 0 && slot < a.kv.num_pages * a.kv.page_size;
+  if (slot >= 0 && !cached && threadIdx.x == 0) kv_report(a.status);
+  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* angles = nullptr;
+  if (R > 0) {
+    const int64_t pos = a.positions[t];
+    if (pos < 0 || pos >= a.num_positions) {
+      if (threadIdx.x == 0) kv_report(a.status);
+      return;
+    }
+    angles = a.cos_sin + pos * R;
+    if (turn) {
+      const float4 c = *reinterpret_cast<const float4*>(angles + 4 * l);
+      const float4 s = *reinterpret_cast<const float4*>(angles + R / 2 + 4 * l);
+      cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+      sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
+    }
+  }
+
+  // ---- query heads
+  float w[8];
+  if (a.q_norm) unpack_row(load_row(a.q_norm, lo, hi, true), w);
+  for (int h0 = warp * HPW; h0 < Hq; h0 += NS * WARPS * HPW) {
+    Row r[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int h = h0 + s * WARPS * HPW + sub;
+      r[s] = load_row(qs + (int64_t)h * D, lo, hi, h < Hq);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int h = h0 + s * WARPS * HPW + sub;
+      if (h - sub >= Hq) break;
+      float x[8];
+      unpack_row(r[s], x);
+      norm_rotate<LPH>(x, a.q_norm != nullptr, w, a.eps, turn, a.interleaved, cs, sn);
+      if (h < Hq) store_row(a.q_out + (t * Hq + h) * D, lo, hi, x);
+    }
+  }
+
+  // ---- key and value heads
+  if (!cached) return;  // (the whole CTA's token)
+  const uint32_t ps = (uint32_t)a.kv.page_size;
+  const int64_t page = slot >> 32 ? slot / ps : (uint32_t)slot / ps;
+  const int64_t row0 = page * H * ps + (slot - page * ps);
+  if (a.k_norm) unpack_row(load_row(a.k_norm, klo, khi, true), w);
+  for (int h = kv0; h - sub < H; h += WARPS * HPW) {
+    if (h != kv0) {
+      kr = load_row(ks + (int64_t)h * D, klo, khi, h < H);
+      vr = load_row(vs + (int64_t)h * D, 8 * l, 8 * l + 4, h < H);
+    }
+    float x[8];
+    unpack_row(kr, x);
+    if (!neighbours) {
+      norm_rotate<LPH>(x, a.k_norm != nullptr, w, a.eps, turn, a.interleaved, cs, sn);
+    } else {  // eight neighbouring dims pair with those of another lane
+      norm_rotate<LPH>(x, a.k_norm != nullptr, w, a.eps, false, false, cs, sn);
+      const int half = R / 2, i0 = 8 * l < half ? 8 * l : 8 * l - half;
+      const int partner = turn ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
+      const float sign = 8 * l < half ? -1.0f : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = __shfl_sync(0xffffffffu, x[i], partner);
+        if (turn) x[i] = fmaf(x[i], angles[i0 + i], sign * y * angles[half + i0 + i]);
+      }
+    }
+    store_held<KIND, D>(a.kv.k, a.kv.k_scale, a.kv.k_global, row0 + (int64_t)h * ps, l, klo, khi, x, h < H);
+    unpack_row(vr, x);
+    store_held<KIND, D>(a.kv.v, a.kv.v_scale, a.kv.v_global, row0 + (int64_t)h * ps, l, 8 * l, 8 * l + 4, x, h < H);
+  }
 }
 
 template <int KIND, int D>
 cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
-  constexpr int HPW = 256 / D;
-  const int steps = (a.q_heads + 2 * a.kv.heads + HPW - 1) / HPW;
-  // four steps a warp once that leaves every SM 16 warps
-  return a.T * steps >= 4 * 16 * 152 ? launch_ns<KIND, D, 4>(a, steps, stream) : launch_ns<KIND, D, 1>(a, steps, stream);
+  return launch_kernel(kv_write_kernel<KIND, D>, dim3((unsigned)a.T), dim3(KW_THREADS), 0, stream, a);
 }
 
 template <int KIND>
