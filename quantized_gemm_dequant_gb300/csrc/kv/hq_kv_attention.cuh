@@ -25,7 +25,8 @@
 //  - e4m3: a token's key scale multiplies its score.  Its value scale v multiplies its weight, and a weight must fit
 //    f16: the running maximum is taken over s_j + log2 v_j, so that the largest weight times its scale is about one
 //    whatever the scales' range, while l sums exp2(s_j - m) in fp32 beside it.
-//  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and o.
+//  - nvfp4: code * 2^-14 * block scale is exact in f16 (6 significant bits, a multiple of 2^-24); the global scales and
+//    2^14 go to q's scale and to o.
 //  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
 //  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
 //    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.
@@ -47,30 +48,49 @@ constexpr int KA_WARPS = 4;
 constexpr int KA_THREADS = 32 * KA_WARPS;
 constexpr int KA_ROWS = 16;          // query heads of one row tile, at most
 constexpr float KA_LAZY = 8.0f;      // the running maximum lags by at most this (log2)
+constexpr int KA_FEW = 6;            // parts of a pair that are joined without the CTA's help
 constexpr float KA_NONE = -3.0e38f;  // the running maximum of no token
 
-// Units of 16 tokens per unit of the list, CTAs per SM.
-__host__ __device__ constexpr int ka_blocks(int kind, int dim) { return kind == HQ_KV_BF16 || dim == 256 ? 1 : 2; }
+// 16-token blocks per unit of the list, resident CTAs per SM.
+__host__ __device__ constexpr int ka_blocks(int kind, int dim) {
+  return kind == HQ_KV_NVFP4 ? (dim == 256 ? 1 : 2) : (kind == HQ_KV_E4M3 && dim == 64 ? 2 : 1);
+}
 __host__ __device__ constexpr int ka_ctas(int kind, int dim, int nt) {
   return dim == 256 ? 2 : (nt == 2 ? 2 : 3);
+}
+
+// Workspace of a call, for the host (sizes) and the device: the status, then two slots per CTA for the parts of split
+// pairs, then a counter per (sequence, head, row tile).  The slots' room is that of the largest format, so that the
+// counters, which have to be zero between calls, are at one place whatever the calls' shapes are.
+constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 2);  // o, then (m, l) of each row, of 16 heads of 256 dims
+constexpr int KA_MOST_CTAS = 2;                         // per SM, of that size
+constexpr size_t ka_counters_at(int sms) {
+  return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
 }
 
 template <int KIND, int D, int NT>
 struct KaCfg {
   static constexpr int RB = kv_row_bytes(KIND, D), SB = kv_scale_bytes(KIND, D);
-  static constexpr int TB = ka_blocks(KIND, D);      // 16-token blocks of one ring slot
+  static constexpr int TB = ka_blocks(KIND, D);      // 16-token blocks of one chunk
   static constexpr int BLOCK = 16 * (RB + SB);       // a block's codes, then its scales
-  static constexpr int SLOT = TB * BLOCK;
-  static constexpr int CTAS = ka_ctas(KIND, D, NT);  // per SM
+  static constexpr int SIDE = TB * BLOCK;            // a chunk's keys, or its values
+  // A ring step is a chunk's keys and values, so that the decoding of the values fills the waits of the scores; of bf16,
+  // which has nothing to decode and twice the bytes, it is one side.
+  static constexpr bool PAIR = KIND != HQ_KV_BF16;
+  static constexpr int STEP = PAIR ? 2 * SIDE : SIDE;
+  static constexpr bool EARLY = PAIR && NT == 1 && D <= 128;  // values are read before the weights are known
+  static constexpr int CTAS = ka_ctas(KIND, D, NT);  // resident per SM
+  static constexpr size_t PART = 8 * NT * (D + 2);   // floats of a part: o, then (m, l) of each head
+  static_assert(CTAS * PART <= KA_MOST_CTAS * KA_SLOT_FLOATS, "workspace");
   static constexpr int PAD = 4;                      // floats: the lanes' stores of a head's dims meet no bank twice
   static constexpr int MERGE = KA_WARPS * 8 * (D + PAD) * 4;  // eight heads of every warp
   static constexpr bool QS = D == 256 && NT == 2;    // q's fragments in shared memory instead of registers
   static constexpr int QBYTES = QS ? D / 16 * NT * 256 : 0;
   static constexpr int FIXED = MERGE + QBYTES + 384;
   static constexpr int LIMIT = (228 * 1024) / CTAS / 128 * 128 - 1024;  // shared memory of a CTA
-  static constexpr int FIT = (LIMIT - FIXED) / (KA_WARPS * (SLOT + 4));
-  static constexpr int SLOTS = FIT < 2 ? 2 : (FIT > 12 ? 12 : FIT);
-  static constexpr int SMEM = FIXED + KA_WARPS * SLOTS * (SLOT + 4);
+  static constexpr int FIT = (LIMIT - FIXED) / (KA_WARPS * (STEP + 4));
+  static constexpr int DEPTH = FIT < 2 ? 2 : (FIT > 12 ? 12 : FIT);  // ring steps
+  static constexpr int SMEM = FIXED + KA_WARPS * DEPTH * (STEP + 4);
   static_assert(SMEM <= LIMIT, "shared memory");
   // unit u (16 bytes) of row r sits at u ^ ((r / RPL) & XM), so that eight rows' equal units lie in different banks
   static constexpr int UPR = RB / 16;
@@ -80,15 +100,6 @@ struct KaCfg {
     return (uint32_t)(r * RB + ((u ^ ((r / RPL) & XM)) << 4));
   }
 };
-
-// Workspace of a call, for the host (sizes) and the device: the status, then two slots per CTA for the parts of split
-// pairs, then a counter per (sequence, head, row tile).  A slot has room for any format's part, so that the counters,
-// which have to be zero between calls, are at one place whatever the calls' shapes are.
-constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 2);  // o, then (m, l) of each row
-constexpr int KA_MOST_CTAS = 4;                         // per SM
-constexpr size_t ka_counters_at(int sms) {
-  return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
-}
 
 #ifdef __CUDACC__
 
@@ -139,22 +150,53 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// the two values of one e2m1 byte
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t b) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
-  return h;
+// the four bytes of x, two e2m1 codes each -> four f16x2
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "mov.b32 {t0, t1, t2, t3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t0;\n\tcvt.rn.f16x2.e2m1x2 %1, t1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, t2;\n\tcvt.rn.f16x2.e2m1x2 %3, t3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(x));
 }
-// nibble i of both halves of x -> f16x2 of value * 2^-14 (unpack_e2m1x8's placement of the bits)
-__device__ __forceinline__ uint32_t e2m1_pair(uint32_t x, int i) {
-  const uint32_t y = x << (12 - 4 * i);
-  return (y & 0x80008000u) | ((y >> 3) & 0x0E000E00u);
+// The low and the high nibbles of x's four bytes as the high bytes of f16: sign on top, exponent and fraction bits at
+// f16's lowest exponent and highest fraction bits, which is the code's value times 2^-14, subnormals too.
+__device__ __forceinline__ void e2m1_bytes(uint32_t x, uint32_t& low, uint32_t& high) {
+  low = ((x << 4) & 0x80808080u) | ((x << 1) & 0x0E0E0E0Eu);
+  high = (x & 0x80808080u) | ((x >> 3) & 0x0E0E0E0Eu);
 }
+// bytes i and j of x as the high bytes of two f16
+template <int I, int J>
+__device__ __forceinline__ uint32_t f16_of_bytes(uint32_t x) {
+  return __byte_perm(x, 0, 0x4 | I << 4 | 0x4 << 8 | J << 12);
+}
+
+// counter + 1, ordered after the CTA's writes (made visible by its barrier) and before its later reads
+__device__ __forceinline__ int count_up(int* counter) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+// The list cut into W nearly equal shares: the first `more` of them have q + 1 units, the others q.
+struct KaShares {
+  uint32_t W, q, more;
+  __device__ __forceinline__ KaShares(uint32_t total, uint32_t grid) {
+    W = (total + 3) >> 2;  // four units a share (one for each warp), or as many shares as CTAs
+    W = W < grid ? W : grid;
+    q = total / W;
+    more = total - q * W;
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t c) const { return c * q + (c < more ? c : more); }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+    const uint32_t big = more * (q + 1);
+    return u < big ? u / (q + 1) : more + (u - big) / q;
+  }
+};
 
 // One sequence's share of the list of units.
 struct KaSeq {
   int n, j0, t0;  // tokens, the first that is seen, and that one's block
-  int units;      // per (head, row tile), at least one: an empty sequence's output is written too
+  uint32_t units;  // per (head, row tile), at least one: an empty sequence's output is written too
 };
 template <int TB>
 __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
@@ -165,7 +207,7 @@ __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
   s.n = (int)n;
   s.j0 = (int)j0;
   s.t0 = s.j0 & ~(KV_BLOCK - 1);
-  const int u = (s.n - s.t0 + 16 * TB - 1) / (16 * TB);
+  const uint32_t u = (uint32_t)(s.n - s.t0 + 16 * TB - 1) / (16 * TB);
   s.units = u > 0 ? u : 1;
   return s;
 }
@@ -173,17 +215,17 @@ __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
 // A walk over a CTA's share, one (sequence, head, row tile) after another.
 template <int TB>
 struct KaWalk {
-  int64_t u, hi;   // position in the list, end of the share
-  int64_t seg0;    // the pair's first unit in the list
-  int64_t b;
+  uint32_t u, hi;  // position in the list, end of the share
+  uint32_t seg0;   // the pair's first unit in the list
+  int b;
   int hr;          // head * tiles + tile
   KaSeq s;
   __device__ __forceinline__ bool done() const { return u >= hi; }
-  __device__ __forceinline__ int64_t stop() const { return seg0 + s.units < hi ? seg0 + s.units : hi; }
+  __device__ __forceinline__ uint32_t stop() const { return seg0 + s.units < hi ? seg0 + s.units : hi; }
   // tokens of the share's part of the pair
-  __device__ __forceinline__ int from() const { return s.t0 + (int)(u - seg0) * (16 * TB); }
+  __device__ __forceinline__ int from() const { return s.t0 + (int)((u - seg0) * (16 * TB)); }
   __device__ __forceinline__ int to() const {
-    const int t = s.t0 + (int)(stop() - seg0) * (16 * TB);
+    const int t = s.t0 + (int)((stop() - seg0) * (16 * TB));
     return t < s.n ? t : s.n;
   }
   __device__ __forceinline__ void next(const KvAttnArgs& a, int hrs) {
@@ -206,6 +248,95 @@ __device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, 
   if (d == 0 && a.lse) a.lse[q] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Joins the parts of a split pair, first to last, and stores its rows: parts k > 0 are at `others`, two slots apart.  A
+// function of its own, so that its registers are not the main loop's.
+template <int KIND, int D, int NT>
+__device__ __noinline__ void ka_join(const KvAttnArgs& a, const float* first, const float* others, int parts, int64_t q0,
+                                     int rows, float vg, float* merge, float* mls) {
+  using C = KaCfg<KIND, D, NT>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto part_at = [&](int k) { return k ? others + 2 * (int64_t)k * C::PART : first; };
+  if (parts <= KA_FEW) {  // every thread on its own, all loads at once
+#pragma unroll 1
+    for (int e = threadIdx.x; e < rows * (D / 4); e += KA_THREADS) {
+      const int r = e / (D / 4), d = 4 * (e % (D / 4));
+      float2 ml[KA_FEW];
+      float4 v[KA_FEW];
+      float top = KA_NONE, sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KA_FEW; ++k) {
+        if (k >= parts) break;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(part_at(k) + 8 * NT * D + 2 * r));
+        v[k] = __ldcg(reinterpret_cast<const float4*>(part_at(k) + r * D + d));
+      }
+#pragma unroll
+      for (int k = 0; k < KA_FEW; ++k)
+        if (k < parts) top = fmaxf(top, ml[k].x);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < KA_FEW; ++k)
+        if (k < parts) {
+          const float f = ex2(ml[k].x - top);
+          sum = fmaf(f, ml[k].y, sum);
+          y.x = fmaf(f, v[k].x, y.x), y.y = fmaf(f, v[k].y, y.y);
+          y.z = fmaf(f, v[k].z, y.z), y.w = fmaf(f, v[k].w, y.w);
+        }
+      ka_store(a, q0 + r, D, d, y, top, sum, vg);
+    }
+    return;
+  }
+  // a batch's factors 2^(m - top) and l are found by a warp per head, then every thread sums its dims of all parts
+  constexpr int BATCH = 64, MINE = 8 * NT * (D / 4) / KA_THREADS;
+  float* factor = merge;  // [heads][BATCH]
+  float* tops = mls;      // [heads][2]: top, sum
+  float4 y[MINE];
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int r = warp; r < rows; r += KA_WARPS) {
+    float top = KA_NONE;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(part_at(k) + 8 * NT * D + 2 * r));
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if (lane == 0) tops[2 * r] = top, tops[2 * r + 1] = 0.0f;
+  }
+  for (int k0 = 0; k0 < parts; k0 += BATCH) {
+    const int n = parts - k0 < BATCH ? parts - k0 : BATCH;
+    __syncwarp();
+    for (int r = warp; r < rows; r += KA_WARPS) {
+      float sum = 0.0f;
+      for (int k = lane; k < n; k += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_at(k0 + k) + 8 * NT * D + 2 * r));
+        const float f = ex2(ml.x - tops[2 * r]);
+        factor[r * BATCH + k] = f;
+        sum = fmaf(f, ml.y, sum);
+      }
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+      if (lane == 0) tops[2 * r + 1] += sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int e = threadIdx.x + i * KA_THREADS, r = e / (D / 4), d = 4 * (e % (D / 4));
+      if (r >= rows) break;
+#pragma unroll 16
+      for (int k = 0; k < n; ++k) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(k0 + k) + r * D + d));
+        const float f = factor[r * BATCH + k];
+        y[i].x = fmaf(f, v.x, y[i].x), y[i].y = fmaf(f, v.y, y[i].y);
+        y[i].z = fmaf(f, v.z, y[i].z), y[i].w = fmaf(f, v.w, y[i].w);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    const int e = threadIdx.x + i * KA_THREADS, r = e / (D / 4), d = 4 * (e % (D / 4));
+    if (r < rows) ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
+  }
+  __syncthreads();  // the next pair's join writes where this one's was read
+}
+
 template <int KIND, int D, int NT>
 __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     kv_attention_kernel(const KvAttnArgs a, float* slots, int* counters) {
@@ -216,19 +347,19 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem);
   uint32_t* qsm = reinterpret_cast<uint32_t*>(smem + C::MERGE);
-  int64_t* found = reinterpret_cast<int64_t*>(smem + C::MERGE + C::QBYTES);  // 3 words
-  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 64);   // [warp][8 heads][2]
+  int* found = reinterpret_cast<int*>(smem + C::MERGE + C::QBYTES);  // 2 words
+  int* last_one = found + 2;
+  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 128);  // [warp][8 heads][2]
   int64_t* scan = reinterpret_cast<int64_t*>(mls);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + C::FIXED + warp * C::SLOTS * C::SLOT;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::FIXED + KA_WARPS * C::SLOTS * C::SLOT) + warp * C::SLOTS;
+  uint8_t* ring = smem + C::FIXED + warp * C::DEPTH * C::STEP;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::FIXED + KA_WARPS * C::DEPTH * C::STEP) + warp * C::DEPTH;
   const uint32_t ring_at = smem_u32(ring);
   pdl_trigger();
   pdl_wait();
 
   // ---- this CTA's share of the units
   const int G = a.group, tiles = (G + KA_ROWS - 1) / KA_ROWS, H = a.kv.heads, hrs = H * tiles;
-  const int part_rows = G < KA_ROWS ? G : KA_ROWS;
   const int64_t per = (a.B + KA_THREADS - 1) / KA_THREADS;
   const int64_t b0 = per * threadIdx.x < a.B ? per * threadIdx.x : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
   int64_t mine = 0;
@@ -253,17 +384,20 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     total += y;
   }
   total *= hrs;
-  // every CTA that works has four units (one for each warp) or the whole list is shorter
-  const int64_t want = (total + 3) >> 2, W = want < gridDim.x ? want : gridDim.x;
-  if (blockIdx.x >= W) return;
-  const int64_t lo = total * blockIdx.x / W, hi = total * (blockIdx.x + 1) / W;
-  if (lo >= before * hrs && lo < (before + mine) * hrs) {
-    int64_t p = before;
+  if (total > INT32_MAX) {  // the list is counted in 32 bits
+    if (threadIdx.x == 0) kv_report(a.status);
+    return;
+  }
+  const KaShares sh((uint32_t)total, gridDim.x);
+  if (blockIdx.x >= sh.W) return;
+  const uint32_t lo = sh.first(blockIdx.x), start = (uint32_t)before * hrs;
+  if (lo >= start && lo < start + (uint32_t)mine * hrs) {
+    uint32_t p = start;
     for (int64_t b = b0; b < b1; ++b) {
-      const int64_t n = ka_seq<TB>(a, b).units;
-      if (lo < (p + n) * hrs) {
-        found[0] = b;
-        found[1] = p;
+      const uint32_t n = (b1 - b0 == 1 ? (uint32_t)mine : ka_seq<TB>(a, b).units) * hrs;
+      if (lo < p + n) {
+        found[0] = (int)b;
+        found[1] = (int)p;
         break;
       }
       p += n;
@@ -272,99 +406,105 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   __syncthreads();
   KaWalk<TB> at;
   at.u = lo;
-  at.hi = hi;
+  at.hi = sh.first(blockIdx.x + 1);
   at.b = found[0];
   at.s = ka_seq<TB>(a, at.b);
-  const int64_t in = lo - found[1] * hrs;
+  const uint32_t in = lo - (uint32_t)found[1];
   at.hr = (int)(in / at.s.units);
-  at.seg0 = lo - in % at.s.units;
+  at.seg0 = lo - (in - at.hr * at.s.units);
 
   // ---- the ring's front: this warp's chunks of the share, keys and values alternating
   KaWalk<TB> ahead = at;
   int next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to();
-  int64_t row = -1;            // lane i: the first row of the warp's i-th block from the last look at the table
-  int used = 32;               // blocks of it that are used up
-  bool more = true;
-  int put = 0, side = 0;
-  uint32_t word = 0;           // tokens of the chunk that are seen
-  int64_t base[TB];
-  auto issue = [&]() {
-    if (side == 0) {
-      while (more && next_tok >= next_end) {  // the share's next pair
-        ahead.next(a, hrs);
-        more = !ahead.done();
-        if (more) next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to(), used = 32;
+  int64_t row = -1;     // lane i: the first row of the warp's i-th block from the last look at the table
+  int used = 32;        // blocks of it that are used up
+  bool more = true;     // false: all of the share has been asked for
+  int put = 0, get = 0;
+  bool values = false;  // the side that is next (one side a step)
+  uint32_t word = 0;    // tokens of the chunk that are seen
+  int64_t base[TB];     // its blocks' first rows
+  auto next_chunk = [&]() {
+    while (next_tok >= next_end) {  // the share's next pair
+      ahead.next(a, hrs);
+      more = !ahead.done();
+      if (!more) return;
+      next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to(), used = 32;
+    }
+    if (used == 32) {
+      const int64_t tok = (int64_t)next_tok + STRIDE * (lane / TB) + 16 * (lane % TB);
+      row = -1;
+      if (tok < next_end) {
+        const int col = (int)((uint32_t)tok / (uint32_t)a.kv.page_size);
+        const int64_t page = a.page_table[(int64_t)ahead.b * a.table_stride + col];
+        if (page >= 0 && page < a.kv.num_pages)
+          row = (page * H + ahead.hr / tiles) * a.kv.page_size + ((int)tok - col * a.kv.page_size);
+        else
+          kv_report(a.status);
       }
-      if (more) {
-        if (used == 32) {
-          const int64_t tok = (int64_t)next_tok + STRIDE * (lane / TB) + 16 * (lane % TB);
-          row = -1;
-          if (tok < next_end) {
-            const int col = (int)((uint32_t)tok / (uint32_t)a.kv.page_size);
-            const int64_t page = a.page_table[ahead.b * a.table_stride + col];
-            if (page >= 0 && page < a.kv.num_pages)
-              row = (page * H + ahead.hr / tiles) * a.kv.page_size + ((int)tok - col * a.kv.page_size);
-            else
-              kv_report(a.status);
-          }
-          used = 0;
-        }
-        const int first = ahead.s.j0 - next_tok, last = ahead.s.n - next_tok;
-        word = FULL;
-        if (first > 0) word &= FULL << first;
-        if (last < 16 * TB) word &= FULL >> (16 * TB - last);
+      used = 0;
+    }
+    const int first = ahead.s.j0 - next_tok, last = ahead.s.n - next_tok;
+    word = FULL;
+    if (first > 0) word &= FULL << first;
+    if (last < 16 * TB) word &= FULL >> (16 * TB - last);
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-          base[i] = __shfl_sync(0xffffffffu, row, used + i);
-          if (base[i] < 0) word &= ~(0xFFFFu << (16 * i)), base[i] = 0;
+    for (int i = 0; i < TB; ++i) {
+      base[i] = __shfl_sync(0xffffffffu, row, used + i);
+      if (base[i] < 0) word &= ~(0xFFFFu << (16 * i)), base[i] = 0;
+    }
+    used += TB;
+    next_tok += STRIDE;
+  };
+  auto copy_side = [&](const uint8_t* pool, const uint8_t* scale_pool, uint32_t to) {
+#pragma unroll
+    for (int t = 0; t < TB; ++t, to += C::BLOCK) {
+      const uint8_t *codes = pool + base[t] * C::RB + lane * 16, *scales = scale_pool + base[t] * C::SB + lane * 16;
+      if (word == FULL) {
+#pragma unroll
+        for (int i = 0; i < C::RB / 32; ++i)
+          copy16(to + C::at((lane + 32 * i) / C::UPR, (lane + 32 * i) % C::UPR), codes + 512 * i);
+        if (C::SB > 0 && lane < C::SB) copy16(to + 16 * C::RB + 16 * lane, scales);
+      } else {  // rows that are not seen are zero: whatever they hold meets a weight of zero, and may be NaN
+        const uint32_t w = word >> (16 * t);
+#pragma unroll
+        for (int i = 0; i < C::RB / 32; ++i) {
+          const int r = (lane + 32 * i) / C::UPR;
+          copy16_or_zero(to + C::at(r, (lane + 32 * i) % C::UPR), codes + 512 * i, (w >> r) & 1u ? 16u : 0u);
         }
-        used += TB;
-        next_tok += STRIDE;
+        if (C::SB > 0 && lane < C::SB) copy16_or_zero(to + 16 * C::RB + 16 * lane, scales, w & 0xFFFFu ? 16u : 0u);
       }
     }
+  };
+  auto issue = [&]() {  // one ring step
+    if ((C::PAIR || !values) && more) next_chunk();
     if (more) {
-      const uint32_t slot = ring_at + put * C::SLOT;
-#pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        const uint8_t* codes = (side ? a.kv.v : a.kv.k) + base[t] * C::RB + lane * 16;
-        const uint8_t* scales = (side ? a.kv.v_scale : a.kv.k_scale) + base[t] * C::SB + lane * 16;
-        const uint32_t to = slot + t * C::BLOCK;
-        if (word == FULL) {
-#pragma unroll
-          for (int i = 0; i < C::RB / 32; ++i)
-            copy16(to + C::at((lane + 32 * i) / C::UPR, (lane + 32 * i) % C::UPR), codes + 512 * i);
-          if (C::SB > 0 && lane < C::SB) copy16(to + 16 * C::RB + 16 * lane, scales);
-        } else {  // rows that are not seen are zero: whatever they hold meets a weight of zero, and may be NaN
-          const uint32_t w = word >> (16 * t);
-#pragma unroll
-          for (int i = 0; i < C::RB / 32; ++i) {
-            const int r = (lane + 32 * i) / C::UPR;
-            copy16_or_zero(to + C::at(r, (lane + 32 * i) % C::UPR), codes + 512 * i, (w >> r) & 1u ? 16u : 0u);
-          }
-          if (C::SB > 0 && lane < C::SB) copy16_or_zero(to + 16 * C::RB + 16 * lane, scales, w & 0xFFFFu ? 16u : 0u);
-        }
+      const uint32_t to = ring_at + put * C::STEP;
+      if constexpr (C::PAIR) {
+        copy_side(a.kv.k, a.kv.k_scale, to);
+        copy_side(a.kv.v, a.kv.v_scale, to + C::SIDE);
+      } else {
+        copy_side(values ? a.kv.v : a.kv.k, nullptr, to);
       }
       if (lane == 0) masks[put] = word;
     }
     cp_async_commit();
-    put = put + 1 == C::SLOTS ? 0 : put + 1;
-    side ^= 1;
+    put = put + 1 == C::DEPTH ? 0 : put + 1;
+    values = !values;
   };
 #pragma unroll 1
-  for (int i = 0; i < C::SLOTS - 1; ++i) issue();
-  int get = 0;
+  for (int i = 0; i < C::DEPTH - 1; ++i) issue();
 
   float kg = 1.0f, vg = 1.0f;
   if constexpr (KIND == HQ_KV_NVFP4) {
     kg = *a.kv.k_global;
-    vg = *a.kv.v_global * 128.0f;  // the values' f16 are 2^-7 of them
+    vg = *a.kv.v_global * 16384.0f;
   }
   const float cap = a.softcap * 1.4426950408889634f;
 
   // ---- one pair after another
   for (; !at.done(); at.next(a, hrs)) {
     const int h = at.hr / tiles, r0 = (at.hr - h * tiles) * KA_ROWS, rows = G - r0 < KA_ROWS ? G - r0 : KA_ROWS;
-    const int64_t q0 = (at.b * H + h) * G + r0;  // the tile's first query head
+    const int64_t q0 = ((int64_t)at.b * H + h) * G + r0;  // the tile's first query head
     uint32_t qb[C::QS ? 1 : KS][NT][2];  // B fragments: head 8 x + g, two pairs of dims of each 16-dim step
     float qscale[NT][2];                 // of heads 8 x + 2 c and the next
 #pragma unroll
@@ -437,13 +577,13 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll 1
     for (int tok = at.from() + 16 * TB * warp; tok < end; tok += STRIDE) {
       // ---- keys: s^T = K q^T, two sums of every other step (a shorter chain)
-      cp_async_wait_group<C::SLOTS - 2>();
+      cp_async_wait_group<C::DEPTH - 2>();
       __syncwarp();
       issue();
-      const uint32_t kslot = ring_at + get * C::SLOT;
-      const uint8_t* kslot_p = ring + get * C::SLOT;
+      const uint32_t kslot = ring_at + get * C::STEP;
+      uint8_t* kslot_p = ring + get * C::STEP;
       const uint32_t seen = masks[get];
-      get = get + 1 == C::SLOTS ? 0 : get + 1;
+      get = get + 1 == C::DEPTH ? 0 : get + 1;
       const int lr = lane & 15, lu = lane >> 4;  // ldmatrix: 16 tokens by two units
       float s[TB][NT][4];
 #pragma unroll
@@ -483,34 +623,35 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         } else {
           // a unit is 32 dims: two steps, two block scales; lanes c = 0, 1 hold the first block's dims
           uint32_t sc[2][D / 32];  // of tokens g and g + 8
+          const uint32_t ksel = c < 2 ? 0x00 : 0x11;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
-              uint32_t x = *reinterpret_cast<const uint32_t*>(kscale + (g + 8 * i) * C::SB + 4 * w);
-              x = c < 2 ? x : x >> 8;
-              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x00));
-              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(x, 0, 0x22));
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(kscale + (g + 8 * i) * C::SB + 4 * w);
+              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(x, 0, ksel));
+              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(x, 0, ksel + 0x22));
             }
 #pragma unroll
           for (int u = 0; u < D / 32; u += 2) {
             uint32_t r[4], f[2];
             ldsm_x4(kb + C::at(lr, u + lu), r[0], r[1], r[2], r[3]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+              uint32_t y[4], z[4];
+              e2m1x8_to_f16x2(r[2 * i], y);
+              e2m1x8_to_f16x2(r[2 * i + 1], z);
 #pragma unroll
               for (int p = 0; p < 2; ++p) {
-                const uint32_t y = r[2 * i] >> (16 * p), z = r[2 * i + 1] >> (16 * p);
-                const uint32_t a0 = hmul2(e2m1x2_to_f16x2(y), sc[0][u + i]),
-                               a1 = hmul2(e2m1x2_to_f16x2(z), sc[1][u + i]),
-                               a2 = hmul2(e2m1x2_to_f16x2(y >> 8), sc[0][u + i]),
-                               a3 = hmul2(e2m1x2_to_f16x2(z >> 8), sc[1][u + i]);
+                const uint32_t a0 = hmul2(y[2 * p], sc[0][u + i]), a1 = hmul2(z[2 * p], sc[1][u + i]),
+                               a2 = hmul2(y[2 * p + 1], sc[0][u + i]), a3 = hmul2(z[2 * p + 1], sc[1][u + i]);
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                   qfrag(2 * (u + i) + p, x, f);
                   mma16<false>(s2[p][x], a0, a1, a2, a3, f[0], f[1]);
                 }
               }
+            }
           }
         }
         // ---- scores: tokens g (+ 8: i >> 1), heads 2 c (+ 1: i & 1)
@@ -543,12 +684,23 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       }
 
       // ---- values
-      cp_async_wait_group<C::SLOTS - 2>();
-      __syncwarp();
-      issue();
-      const uint32_t vslot = ring_at + get * C::SLOT;
-      uint8_t* vslot_p = ring + get * C::SLOT;
-      get = get + 1 == C::SLOTS ? 0 : get + 1;
+      uint32_t vslot = kslot + C::SIDE;
+      uint8_t* vslot_p = kslot_p + C::SIDE;
+      if constexpr (!C::PAIR) {
+        cp_async_wait_group<C::DEPTH - 2>();
+        __syncwarp();
+        issue();
+        vslot = ring_at + get * C::STEP;
+        get = get + 1 == C::DEPTH ? 0 : get + 1;
+      }
+      constexpr int VL = C::EARLY ? D * (F8 ? 1 : 2) / (F8 ? 32 : 128) : 1;  // ldmatrix of a block's values
+      uint32_t early[TB][VL][4];
+      if constexpr (C::EARLY) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int u = 0; u < VL; ++u) ldsm_x4_t(vslot + t * C::BLOCK + C::at(lr, 2 * u + lu), early[t][u]);
+      }
       float vl[TB][2];  // log2 of the value scales of tokens g and g + 8
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
@@ -618,6 +770,14 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             pb[t][x][i] = turn8x8(BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]));
           }
       // ---- o^T += V^T p^T
+      auto values_at = [&](int t, int u, uint32_t vb, uint32_t (&r)[4]) {
+        if constexpr (C::EARLY) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = early[t][u / 2][i];
+        } else {
+          ldsm_x4_t(vb + C::at(lr, u + lu), r);
+        }
+      };
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         const uint32_t vb = vslot + t * C::BLOCK;
@@ -635,7 +795,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
           for (int u = 0; u < KS; u += 2) {
             uint32_t r[4];
-            ldsm_x4_t(vb + C::at(lr, u + lu), r);
+            values_at(t, u, vb, r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t y = __byte_perm(r[2 * i], 0, 0x3120), z = __byte_perm(r[2 * i + 1], 0, 0x3120);
@@ -647,7 +807,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           }
         } else {
           // a unit is 32 dims: a lane gets dims 4 g .. 4 g + 3 of two tokens; two tiles of two of them each
-          uint32_t sc[2][D / 32];  // of tokens 2 c, 2 c + 1, and 8 on, times 2^7
+          uint32_t sc[2][D / 32];  // of tokens 2 c, 2 c + 1, and 8 on
           const uint32_t sel = g < 4 ? 0x0040u : 0x0051u;  // the first or second block's byte of each token
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -655,25 +815,32 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             for (int w = 0; w < D / 64; ++w) {
               const uint32_t y = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c) * C::SB + 4 * w);
               const uint32_t z = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c + 1) * C::SB + 4 * w);
-              sc[i][2 * w] = hmul2(e4m3x2_to_f16x2(__byte_perm(y, z, sel)), 0x58005800u);
-              sc[i][2 * w + 1] = hmul2(e4m3x2_to_f16x2(__byte_perm(y, z, sel + 0x0022u)), 0x58005800u);
+              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(y, z, sel));
+              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(y, z, sel + 0x0022u));
             }
 #pragma unroll
           for (int u = 0; u < D / 32; u += 2) {
             uint32_t r[4];
-            ldsm_x4_t(vb + C::at(lr, u + lu), r);
+            values_at(t, u, vb, r);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+              // the lane's word: dims 4 g .. 4 g + 3 of token 2 c in bytes 0, 1, of token 2 c + 1 in bytes 2, 3
+              uint32_t lo[2], hi[2];
+              e2m1_bytes(r[2 * i], lo[0], hi[0]);
+              e2m1_bytes(r[2 * i + 1], lo[1], hi[1]);
+              const uint32_t y[4] = {f16_of_bytes<0, 2>(lo[0]), f16_of_bytes<1, 3>(lo[0]), f16_of_bytes<0, 2>(hi[0]),
+                                     f16_of_bytes<1, 3>(hi[0])};  // dims 4 g + 0, 2, 1, 3
+              const uint32_t z[4] = {f16_of_bytes<0, 2>(lo[1]), f16_of_bytes<1, 3>(lo[1]), f16_of_bytes<0, 2>(hi[1]),
+                                     f16_of_bytes<1, 3>(hi[1])};
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
-                const uint32_t a0 = hmul2(e2m1_pair(r[2 * i], 2 * n), sc[0][u + i]),
-                               a1 = hmul2(e2m1_pair(r[2 * i], 2 * n + 1), sc[0][u + i]),
-                               a2 = hmul2(e2m1_pair(r[2 * i + 1], 2 * n), sc[1][u + i]),
-                               a3 = hmul2(e2m1_pair(r[2 * i + 1], 2 * n + 1), sc[1][u + i]);
+                const uint32_t a0 = hmul2(y[n], sc[0][u + i]), a1 = hmul2(y[n + 2], sc[0][u + i]),
+                               a2 = hmul2(z[n], sc[1][u + i]), a3 = hmul2(z[n + 2], sc[1][u + i]);
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
                   mma16<false>(o[2 * (u + i) + n][x], a0, a1, a2, a3, pb[t][x][0], pb[t][x][1]);
               }
+            }
           }
         }
       }
@@ -681,7 +848,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 
     // ---- join the four warps, eight heads at a time, and write the pair's result or its part
     const bool whole = at.u == at.seg0 && at.stop() == at.seg0 + at.s.units;
-    float* part = slots + (2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1)) * KA_SLOT_FLOATS;
+    float* part = slots + (2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1)) * C::PART;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
       if (8 * x >= rows) break;
@@ -730,7 +897,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           ka_store(a, q0 + 8 * x + r, D, d, y, top, sum, vg);
         } else {
           __stcg(reinterpret_cast<float4*>(part + (8 * x + r) * D + d), y);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(part + part_rows * D + 2 * (8 * x + r)), make_float2(top, sum));
+          if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NT * D + 2 * (8 * x + r)), make_float2(top, sum));
         }
       }
       __syncthreads();
@@ -738,34 +905,15 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     if (whole) continue;
 
     // ---- split pair: the last CTA to arrive joins the parts, first to last
-    const int64_t c0 = ((at.seg0 + 1) * W - 1) / total, c1 = ((at.seg0 + at.s.units) * W - 1) / total;
-    const int64_t pair = at.b * hrs + at.hr;
-    __threadfence();
+    const uint32_t c0 = sh.owner(at.seg0), c1 = sh.owner(at.seg0 + at.s.units - 1);
+    const int64_t pair = (int64_t)at.b * hrs + at.hr;
+    __syncthreads();  // the CTA's part is written; the counter's release and acquire order it and the others' parts
+    if (threadIdx.x == 0) *last_one = count_up(counters + pair) == (int)(c1 - c0);
     __syncthreads();
-    if (threadIdx.x == 0) found[2] = atomicAdd(counters + pair, 1) == (int)(c1 - c0);
-    __syncthreads();
-    if (!found[2]) continue;
-    __threadfence();
+    if (!*last_one) continue;
     const int parts = (int)(c1 - c0) + 1;
-    const int64_t s0 = 2 * c0 + (total * c0 / W == at.seg0 ? 0 : 1);  // the others' first pair is this one
-    for (int e = threadIdx.x; e < rows * (D / 4); e += KA_THREADS) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float top = KA_NONE, sum = 0.0f;
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k)
-        top = fmaxf(top, __ldcg(slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS + part_rows * D + 2 * r));
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const float* p = slots + (k ? 2 * (c0 + k) : s0) * KA_SLOT_FLOATS;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + part_rows * D + 2 * r));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
-        const float f = ex2(ml.x - top);
-        sum = fmaf(f, ml.y, sum);
-        y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
-      }
-      ka_store(a, q0 + r, D, d, y, top, sum, vg);
-    }
+    const int64_t s0 = 2 * (int64_t)c0 + (sh.first(c0) == at.seg0 ? 0 : 1);  // the others' first pair is this one
+    ka_join<KIND, D, NT>(a, slots + s0 * C::PART, slots + 2 * (int64_t)c0 * C::PART, parts, q0, rows, vg, merge, mls);
     if (threadIdx.x == 0) counters[pair] = 0;
   }
   cp_async_wait_all();

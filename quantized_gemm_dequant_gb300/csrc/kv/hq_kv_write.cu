@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../hq_launch.h"
 #include "../hq_ptx.cuh"
 #include "hq_kv.h"
@@ -26,10 +28,9 @@ constexpr int KW_THREADS = 128;
 
 // x / y rounded to nearest even from yi = RN(1 / y): RN(x yi) is faithful, its residual is exact with one FMA, and one
 // more FMA gives the correctly rounded quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  Valid while the residual stays a normal number; callers take
-// it for y >= 2^-100 and divide otherwise.
-__device__ __forceinline__ float quotient(float x, float y, float yi, bool fast) {
-  if (!fast) return __fdiv_rn(x, y);
+// System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  Valid while the residual stays a normal number: callers take
+// it for y >= 2^-100, where a quotient that can round to a nonzero code has |x| >= 2^-110, and divide otherwise.
+__device__ __forceinline__ float quotient(float x, float y, float yi) {
   const float q = __fmul_rn(x, yi);
   return __fmaf_rn(__fmaf_rn(-q, y, x), yi, q);
 }
@@ -73,174 +74,230 @@ __device__ __forceinline__ float largest(const float (&x)[8]) {
   return m;
 }
 
-// Norm (w: the lane's weights; on: whether there is one) and rotation of a row.  The rotated pairs are (x[i], x[i + 4])
-// for a rotation by halves, (x[2 i], x[2 i + 1]) for an interleaved one; cs, sn are their four angles'.
-template <int LPH>
+enum { NO_TURN = 0, BY_HALVES = 1, INTERLEAVED = 2 };
+
+// Norm (w: the lane's weights, ones where there is none) and rotation of a row, without branches, so that several rows'
+// shuffles and chains overlap.  The rotated pairs are (x[i], x[i + 4]) for a rotation by halves, (x[2 i], x[2 i + 1])
+// for an interleaved one; cs, sn are their four angles'.
+template <int LPH, int MODE>
 __device__ __forceinline__ void norm_rotate(float (&x)[8], bool on, const float (&w)[8], float eps, bool turn,
-                                            bool interleaved, const float (&cs)[4], const float (&sn)[4]) {
-  if (on) {
-    float sq = 0.0f;
+                                            const float (&cs)[4], const float (&sn)[4]) {
+  float sq = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-    const float r = rsqrtf(lanes_sum<LPH>(sq) * (1.0f / (8 * LPH)) + eps);
+  for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+  const float r = on ? rsqrtf(lanes_sum<LPH>(sq) * (1.0f / (8 * LPH)) + eps) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-  }
-  if (!turn) return;
+  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  if constexpr (MODE != NO_TURN) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (interleaved) {
-      const float p = x[2 * i], q = x[2 * i + 1];
-      x[2 * i] = fmaf(p, cs[i], -q * sn[i]);
-      x[2 * i + 1] = fmaf(q, cs[i], p * sn[i]);
-    } else {
-      const float p = x[i], q = x[i + 4];
-      x[i] = fmaf(p, cs[i], -q * sn[i]);
-      x[i + 4] = fmaf(q, cs[i], p * sn[i]);
+    for (int i = 0; i < 4; ++i) {
+      float& p = x[MODE == INTERLEAVED ? 2 * i : i];
+      float& q = x[MODE == INTERLEAVED ? 2 * i + 1 : i + 4];
+      const float p0 = p, q0 = q, p1 = fmaf(p0, cs[i], -q0 * sn[i]), q1 = fmaf(q0, cs[i], p0 * sn[i]);
+      p = turn ? p1 : p0;
+      q = turn ? q1 : q0;
     }
   }
 }
 
-// A row (dims lo .. and hi .. of each lane; NVFP4: eight neighbouring dims) into the pool.  The shuffles are the whole
-// warp's; only lanes that `put` store.
+// The scale that a lane's eight dims are divided by: e4m3's of the row, NVFP4's of the block of 16 dims (two lanes) with
+// its byte.  0 where all codes are zero.
 template <int KIND, int D>
-__device__ __forceinline__ void store_held(uint8_t* codes, uint8_t* scales, const float* global, int64_t row, int l,
-                                           int lo, int hi, const float (&x)[8], bool put) {
-  uint8_t* dst = codes + row * kv_row_bytes(KIND, D);
-  if constexpr (KIND == HQ_KV_BF16) {
-    if (put) store_row(reinterpret_cast<uint16_t*>(dst), lo, hi, x);
-  } else if constexpr (KIND == HQ_KV_E4M3) {
-    const float s = __fdiv_rn(lanes_max<D / 8>(largest(x)), 448.0f), inv = __frcp_rn(s);
-    const bool fast = s >= KW_FAST;
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = s > 0.0f ? pack_e4m3x2(quotient(x[2 * i], s, inv, fast), quotient(x[2 * i + 1], s, inv, fast)) : 0u;
-    if (put) {
-      *reinterpret_cast<uint32_t*>(dst + lo) = c[0] | (c[1] << 16);
-      *reinterpret_cast<uint32_t*>(dst + hi) = c[2] | (c[3] << 16);
-      if (l == 0) reinterpret_cast<float*>(scales)[row] = s;
-    }
+__device__ __forceinline__ float scale_of(const float (&x)[8], float g, uint32_t& byte) {
+  if constexpr (KIND == HQ_KV_E4M3) {
+    const float m = lanes_max<D / 8>(largest(x));
+    return m >= KW_FAST ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
   } else {
-    const float m = lanes_max<2>(largest(x)), g = *global;  // a block of 16 dims is two lanes
-    const uint32_t sb = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
-    const float d = __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x, g), inv = __frcp_rn(d);
-    const bool fast = d >= KW_FAST;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = d > 0.0f ? quotient(x[i], d, inv, fast) : 0.0f;
-    if (put) {
-      *reinterpret_cast<uint32_t*>(dst + 4 * l) = pack_e2m1x8(y);
-      if (!(l & 1)) scales[row * (D / 16) + l / 2] = (uint8_t)sb;
-    }
+    const float m = lanes_max<2>(largest(x));
+    byte = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
+    return __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(byte)).x, g);
   }
 }
 
+// A quantised row into the pool; x holds the quotients.
 template <int KIND, int D>
-__global__ void __launch_bounds__(KW_THREADS) kv_write_kernel(const KvWriteArgs a) {
+__device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scales, int64_t row, int l, int lo, int hi,
+                                            const float (&x)[8], float s, uint32_t byte) {
+  uint8_t* dst = codes + row * kv_row_bytes(KIND, D);
+  if constexpr (KIND == HQ_KV_E4M3) {
+    const uint32_t c0 = pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16);
+    const uint32_t c1 = pack_e4m3x2(x[4], x[5]) | (pack_e4m3x2(x[6], x[7]) << 16);
+    *reinterpret_cast<uint32_t*>(dst + lo) = s > 0.0f ? c0 : 0u;
+    *reinterpret_cast<uint32_t*>(dst + hi) = s > 0.0f ? c1 : 0u;
+    if (l == 0) reinterpret_cast<float*>(scales)[row] = s;
+  } else {
+    const uint32_t c = pack_e2m1x8(x);
+    *reinterpret_cast<uint32_t*>(dst + 4 * l) = s > 0.0f ? c : 0u;
+    if (!(l & 1)) scales[row * (D / 16) + l / 2] = (uint8_t)byte;
+  }
+}
+
+constexpr int KW_STEPS = 4;  // query steps of a warp that are kept in registers
+
+// What a warp reads of one token.
+struct Token {
+  Row q[KW_STEPS], k, v;
+  float4 cs, sn;  // the lane's four angles
+  int64_t slot;
+  int64_t pos;
+};
+
+template <int KIND, int D, int MODE>
+__global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteArgs a) {
   constexpr int LPH = D / 8;     // lanes of a head's row
   constexpr int HPW = 32 / LPH;  // heads of one step
-  constexpr int WARPS = KW_THREADS / 32, NS = 4;
+  constexpr int NEXT = KW_THREADS / 32 * HPW;
+  constexpr bool halves = MODE == BY_HALVES;
+  constexpr bool neighbours = KIND == HQ_KV_NVFP4 && halves;  // key rows by neighbours all the same: blocks of 16 dims
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPH, sub = lane / LPH;
-  const int64_t t = blockIdx.x;
   const int H = a.kv.heads, Hq = a.q_heads, R = a.rotary;
-  const bool halves = R > 0 && !a.interleaved, turn = 8 * l < R;
+  const bool turn = 8 * l < R;
   // the lane's dims: by halves of the rotated part and of the rest, or eight neighbours
   int lo = 8 * l, hi = 8 * l + 4;
   if (halves && turn) lo = 4 * l, hi = R / 2 + 4 * l;
-  const uint16_t* qs = a.qkv + t * a.row_stride;
-  const uint16_t* ks = qs + (int64_t)Hq * D;
-  const uint16_t* vs = ks + (int64_t)H * D;
-  const bool neighbours = KIND == HQ_KV_NVFP4 && halves;  // key rows by neighbours all the same: blocks of 16 dims
   const int klo = neighbours ? 8 * l : lo, khi = neighbours ? 8 * l + 4 : hi;
-  const int kv0 = warp * HPW + sub;
-  Row kr = load_row(ks + (int64_t)kv0 * D, klo, khi, kv0 < H);
-  Row vr = load_row(vs + (int64_t)kv0 * D, 8 * l, 8 * l + 4, kv0 < H);
+  const int h0 = warp * HPW + sub;
+  const int ktok = Hq * D, vtok = ktok + H * D;
 
-  const int64_t slot = a.slots[t];
-  const bool cached = slot >= 0 && slot < a.kv.num_pages * a.kv.page_size;
-  if (slot >= 0 && !cached && threadIdx.x == 0) kv_report(a.status);
-  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float* angles = nullptr;
-  if (R > 0) {
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.num_positions) {
-      if (threadIdx.x == 0) kv_report(a.status);
-      return;
+  auto read_place = [&](int64_t t, Token& x) {
+    const bool live = t < a.T;
+    x.slot = live ? a.slots[t] : -1;
+    x.pos = MODE != NO_TURN && live ? a.positions[t] : 0;
+  };
+  auto read_rows = [&](int64_t t, Token& x) {  // its position is known
+    const bool live = t < a.T;
+    const uint16_t* row = a.qkv + t * a.row_stride + h0 * D;
+#pragma unroll
+    for (int s = 0; s < KW_STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, live && h0 + s * NEXT < Hq);
+    x.k = load_row(row + ktok, klo, khi, live && h0 < H);
+    x.v = load_row(row + vtok, 8 * l, 8 * l + 4, live && h0 < H);
+    if constexpr (MODE != NO_TURN) {
+      const float* angles = a.cos_sin + (x.pos >= 0 && x.pos < a.num_positions ? x.pos : 0) * R;
+      x.cs = *reinterpret_cast<const float4*>(angles + (turn ? 4 * l : 0));
+      x.sn = *reinterpret_cast<const float4*>(angles + R / 2 + (turn ? 4 * l : 0));
     }
-    angles = a.cos_sin + pos * R;
-    if (turn) {
-      const float4 c = *reinterpret_cast<const float4*>(angles + 4 * l);
-      const float4 s = *reinterpret_cast<const float4*>(angles + R / 2 + 4 * l);
-      cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
-      sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
-    }
-  }
+  };
 
-  // ---- query heads
   float w[8];
-  if (a.q_norm) unpack_row(load_row(a.q_norm, lo, hi, true), w);
-  for (int h0 = warp * HPW; h0 < Hq; h0 += NS * WARPS * HPW) {
-    Row r[NS];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int h = h0 + s * WARPS * HPW + sub;
-      r[s] = load_row(qs + (int64_t)h * D, lo, hi, h < Hq);
-    }
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int h = h0 + s * WARPS * HPW + sub;
-      if (h - sub >= Hq) break;
-      float x[8];
-      unpack_row(r[s], x);
-      norm_rotate<LPH>(x, a.q_norm != nullptr, w, a.eps, turn, a.interleaved, cs, sn);
-      if (h < Hq) store_row(a.q_out + (t * Hq + h) * D, lo, hi, x);
-    }
-  }
-
-  // ---- key and value heads
-  if (!cached) return;  // (the whole CTA's token)
+  Row kw = {make_uint2(0x3F803F80u, 0x3F803F80u), make_uint2(0x3F803F80u, 0x3F803F80u)};  // ones
+  unpack_row(a.q_norm ? load_row(a.q_norm, lo, hi, true) : kw, w);
+  if (a.k_norm) kw = load_row(a.k_norm, klo, khi, true);
+  const bool q_on = a.q_norm != nullptr, k_on = a.k_norm != nullptr;
+  float kg = 1.0f, vg = 1.0f;
+  if constexpr (KIND == HQ_KV_NVFP4) kg = *a.kv.k_global, vg = *a.kv.v_global;
   const uint32_t ps = (uint32_t)a.kv.page_size;
-  const int64_t page = slot >> 32 ? slot / ps : (uint32_t)slot / ps;
-  const int64_t row0 = page * H * ps + (slot - page * ps);
-  if (a.k_norm) unpack_row(load_row(a.k_norm, klo, khi, true), w);
-  for (int h = kv0; h - sub < H; h += WARPS * HPW) {
-    if (h != kv0) {
-      kr = load_row(ks + (int64_t)h * D, klo, khi, h < H);
-      vr = load_row(vs + (int64_t)h * D, 8 * l, 8 * l + 4, h < H);
-    }
-    float x[8];
-    unpack_row(kr, x);
-    if (!neighbours) {
-      norm_rotate<LPH>(x, a.k_norm != nullptr, w, a.eps, turn, a.interleaved, cs, sn);
-    } else {  // eight neighbouring dims pair with those of another lane
-      norm_rotate<LPH>(x, a.k_norm != nullptr, w, a.eps, false, false, cs, sn);
-      const int half = R / 2, i0 = 8 * l < half ? 8 * l : 8 * l - half;
-      const int partner = turn ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
-      const float sign = 8 * l < half ? -1.0f : 1.0f;
+  const int64_t G = gridDim.x, slots = a.kv.num_pages * ps;
+  Token x, y, z;
+  read_place(blockIdx.x, x);
+  read_place(blockIdx.x + G, y);
+  read_rows(blockIdx.x, x);
+  for (int64_t t = blockIdx.x; t < a.T; t += G, x = y, y.slot = z.slot, y.pos = z.pos) {
+    read_rows(t + G, y);
+    read_place(t + 2 * G, z);
+    const bool cached = x.slot >= 0 && x.slot < slots;
+    const bool placed = MODE == NO_TURN || (x.pos >= 0 && x.pos < a.num_positions);
+    if (threadIdx.x == 0 && ((x.slot >= 0 && !cached) || !placed)) kv_report(a.status);
+    if (!placed) continue;
+    const float cs[4] = {x.cs.x, x.cs.y, x.cs.z, x.cs.w}, sn[4] = {x.sn.x, x.sn.y, x.sn.z, x.sn.w};
+
+    // ---- query heads
+    uint16_t* out = a.q_out + (t * Hq + h0) * D;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], partner);
-        if (turn) x[i] = fmaf(x[i], angles[i0 + i], sign * y * angles[half + i0 + i]);
+    for (int s = 0; s < KW_STEPS; ++s) {
+      float f[8];
+      unpack_row(x.q[s], f);
+      norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
+      if (h0 + s * NEXT < Hq) store_row(out + s * NEXT * D, lo, hi, f);
+    }
+    for (int h = h0 + KW_STEPS * NEXT; h - sub < Hq; h += NEXT) {
+      float f[8];
+      unpack_row(load_row(a.qkv + t * a.row_stride + (int64_t)h * D, lo, hi, h < Hq), f);
+      norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
+      if (h < Hq) store_row(out + (int64_t)(h - h0) * D, lo, hi, f);
+    }
+
+    // ---- key and value heads
+    if (!cached) continue;
+    const int64_t page = x.slot >> 32 ? x.slot / ps : (uint32_t)x.slot / ps;
+    const int64_t row0 = page * H * ps + (x.slot - page * ps);
+    for (int h = h0; h - sub < H; h += NEXT) {
+      if (h != h0) {
+        const uint16_t* row = a.qkv + t * a.row_stride + (int64_t)h * D;
+        x.k = load_row(row + ktok, klo, khi, h < H);
+        x.v = load_row(row + vtok, 8 * l, 8 * l + 4, h < H);
+      }
+      float f[8], g[8];
+      unpack_row(x.k, f);
+      unpack_row(kw, g);
+      norm_rotate<LPH, neighbours ? NO_TURN : MODE>(f, k_on, g, a.eps, turn, cs, sn);
+      if constexpr (neighbours) {  // eight neighbouring dims pair with those of another lane
+        const int half = R / 2, i0 = 8 * l < half ? 8 * l : 8 * l - half;
+        const int partner = turn ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
+        const float sign = 8 * l < half ? -1.0f : 1.0f;
+        const float* angles = a.cos_sin + x.pos * R;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = __shfl_sync(0xffffffffu, f[i], partner);
+          if (turn) f[i] = fmaf(f[i], angles[i0 + i], sign * p * angles[half + i0 + i]);
+        }
+      }
+      unpack_row(x.v, g);
+      const int64_t row = row0 + (int64_t)h * ps;
+      if constexpr (KIND == HQ_KV_BF16) {
+        if (h < H) {
+          store_row(reinterpret_cast<uint16_t*>(a.kv.k) + row * D, klo, khi, f);
+          store_row(reinterpret_cast<uint16_t*>(a.kv.v) + row * D, 8 * l, 8 * l + 4, g);
+        }
+      } else {
+        uint32_t kb = 0, vb = 0;
+        const float ks = scale_of<KIND, D>(f, kg, kb), vs = scale_of<KIND, D>(g, vg, vb);
+        if (__all_sync(0xffffffffu, (ks >= KW_FAST || ks == 0.0f) && (vs >= KW_FAST || vs == 0.0f))) {
+          const float ki = __frcp_rn(ks), vi = __frcp_rn(vs);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], ks, ki), g[i] = quotient(g[i], vs, vi);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], ks), g[i] = __fdiv_rn(g[i], vs);
+        }
+        if (h < H) {
+          store_codes<KIND, D>(a.kv.k, a.kv.k_scale, row, l, klo, khi, f, ks, kb);
+          store_codes<KIND, D>(a.kv.v, a.kv.v_scale, row, l, 8 * l, 8 * l + 4, g, vs, vb);
+        }
       }
     }
-    store_held<KIND, D>(a.kv.k, a.kv.k_scale, a.kv.k_global, row0 + (int64_t)h * ps, l, klo, khi, x, h < H);
-    unpack_row(vr, x);
-    store_held<KIND, D>(a.kv.v, a.kv.v_scale, a.kv.v_global, row0 + (int64_t)h * ps, l, 8 * l, 8 * l + 4, x, h < H);
   }
 }
 
-template <int KIND, int D>
+template <int KIND, int D, int MODE>
 cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
-  return launch_kernel(kv_write_kernel<KIND, D>, dim3((unsigned)a.T), dim3(KW_THREADS), 0, stream, a);
+  static std::atomic<int> resident{0};  // CTAs that the device holds at once
+  int n = resident.load(std::memory_order_relaxed);
+  if (n == 0) {
+    int dev = 0, sms = 0, per = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_write_kernel<KIND, D, MODE>, KW_THREADS, 0);
+    if (e != cudaSuccess) return e;
+    n = (per > 0 ? per : 1) * (sms > 0 ? sms : 1);
+    resident.store(n, std::memory_order_relaxed);
+  }
+  return launch_kernel(kv_write_kernel<KIND, D, MODE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
+                       a);
+}
+
+template <int KIND, int D>
+cudaError_t by_mode(const KvWriteArgs& a, cudaStream_t stream) {
+  if (a.rotary == 0) return launch<KIND, D, NO_TURN>(a, stream);
+  return a.interleaved ? launch<KIND, D, INTERLEAVED>(a, stream) : launch<KIND, D, BY_HALVES>(a, stream);
 }
 
 template <int KIND>
 cudaError_t by_dim(int dim, const KvWriteArgs& a, cudaStream_t stream) {
-  return dim == 64 ? launch<KIND, 64>(a, stream) : (dim == 128 ? launch<KIND, 128>(a, stream)
-                                                               : launch<KIND, 256>(a, stream));
+  return dim == 64 ? by_mode<KIND, 64>(a, stream)
+                   : (dim == 128 ? by_mode<KIND, 128>(a, stream) : by_mode<KIND, 256>(a, stream));
 }
 
 }  // namespace
