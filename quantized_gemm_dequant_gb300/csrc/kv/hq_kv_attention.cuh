@@ -79,6 +79,11 @@ struct KaCfg {
   static constexpr bool PAIR = KIND != HQ_KV_BF16;
   static constexpr int STEP = PAIR ? 2 * SIDE : SIDE;
   static constexpr bool EARLY = PAIR && NT == 1 && D <= 128;  // values are read before the weights are known
+  // Beginning and ending a pair costs a CTA about as long as streaming so many bytes (3 to 4 us): so many units of the
+  // list are the pair's own.  Without them the CTAs with more pairs were up to a fifth later than the others (a batch
+  // of 64 e4m3 sequences: 99 us, with them 94 to 96).
+  static constexpr int PAIR_BYTES = KIND == HQ_KV_NVFP4 ? 49152 : 81920;
+  static constexpr int EXTRA = PAIR_BYTES / (2 * SIDE) > 0 ? PAIR_BYTES / (2 * SIDE) : 1;
   static constexpr int CTAS = ka_ctas(KIND, D, NT);  // resident per SM
   static constexpr size_t PART = 8 * NT * (D + 2);   // floats of a part: o, then (m, l) of each head
   static_assert(CTAS * PART <= KA_MOST_CTAS * KA_SLOT_FLOATS, "workspace");
@@ -171,6 +176,10 @@ __device__ __forceinline__ uint32_t f16_of_bytes(uint32_t x) {
   return __byte_perm(x, 0, 0x4 | I << 4 | 0x4 << 8 | J << 12);
 }
 
+// L2 line i of a range, if it has one
+__device__ __forceinline__ void ka_prefetch(const void* p, int64_t bytes, int64_t i) {
+  if (i * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)p + i * 128));
+}
 // counter + 1, ordered after the CTA's writes (made visible by its barrier) and before its later reads
 __device__ __forceinline__ int count_up(int* counter) {
   int old;
@@ -180,8 +189,9 @@ __device__ __forceinline__ int count_up(int* counter) {
 // The list cut into W nearly equal shares: the first `more` of them have q + 1 units, the others q.
 struct KaShares {
   uint32_t W, q, more;
-  __device__ __forceinline__ KaShares(uint32_t total, uint32_t grid) {
-    W = (total + 3) >> 2;  // four units a share (one for each warp), or as many shares as CTAs
+  // least: units of a share at least, for few tokens
+  __device__ __forceinline__ KaShares(uint32_t total, uint32_t grid, uint32_t least) {
+    W = (total + least - 1) / least;
     W = W < grid ? W : grid;
     q = total / W;
     more = total - q * W;
@@ -196,9 +206,10 @@ struct KaShares {
 // One sequence's share of the list of units.
 struct KaSeq {
   int n, j0, t0;  // tokens, the first that is seen, and that one's block
-  uint32_t units;  // per (head, row tile), at least one: an empty sequence's output is written too
+  uint32_t units;  // per (head, row tile): X for the pair itself, then its tokens' (one at least: an empty sequence's
+                   // output is written too)
 };
-template <int TB>
+template <int TB, int X>
 __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
   KaSeq s;
   int64_t n = a.lens[b];
@@ -208,12 +219,12 @@ __device__ __forceinline__ KaSeq ka_seq(const KvAttnArgs& a, int64_t b) {
   s.j0 = (int)j0;
   s.t0 = s.j0 & ~(KV_BLOCK - 1);
   const uint32_t u = (uint32_t)(s.n - s.t0 + 16 * TB - 1) / (16 * TB);
-  s.units = u > 0 ? u : 1;
+  s.units = X + (u > 0 ? u : 1);
   return s;
 }
 
 // A walk over a CTA's share, one (sequence, head, row tile) after another.
-template <int TB>
+template <int TB, int X>
 struct KaWalk {
   uint32_t u, hi;  // position in the list, end of the share
   uint32_t seg0;   // the pair's first unit in the list
@@ -222,10 +233,12 @@ struct KaWalk {
   KaSeq s;
   __device__ __forceinline__ bool done() const { return u >= hi; }
   __device__ __forceinline__ uint32_t stop() const { return seg0 + s.units < hi ? seg0 + s.units : hi; }
-  // tokens of the share's part of the pair
-  __device__ __forceinline__ int from() const { return s.t0 + (int)((u - seg0) * (16 * TB)); }
+  // the share's part of the pair: whether there are tokens' units in it, and all of them; the tokens
+  __device__ __forceinline__ bool any() const { return stop() > seg0 + X; }
+  __device__ __forceinline__ bool whole() const { return u <= seg0 + X && stop() == seg0 + s.units; }
+  __device__ __forceinline__ int from() const { return s.t0 + (u > seg0 + X ? (int)((u - seg0 - X) * (16 * TB)) : 0); }
   __device__ __forceinline__ int to() const {
-    const int t = s.t0 + (int)((stop() - seg0) * (16 * TB));
+    const int t = s.t0 + (any() ? (int)((stop() - seg0 - X) * (16 * TB)) : 0);
     return t < s.n ? t : s.n;
   }
   __device__ __forceinline__ void next(const KvAttnArgs& a, int hrs) {
@@ -234,7 +247,7 @@ struct KaWalk {
     seg0 = u;
     if (++hr == hrs) {
       hr = 0;
-      s = ka_seq<TB>(a, ++b);
+      s = ka_seq<TB, X>(a, ++b);
     }
   }
 };
@@ -356,6 +369,9 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::FIXED + KA_WARPS * C::DEPTH * C::STEP) + warp * C::DEPTH;
   const uint32_t ring_at = smem_u32(ring);
   pdl_trigger();
+  // While the previous kernel ends, the lengths and the page table move to L2 (a hint: nothing is read before the wait).
+  ka_prefetch(a.lens, a.B * 4, (int64_t)blockIdx.x * KA_THREADS + threadIdx.x);
+  ka_prefetch(a.page_table, a.B * a.table_stride * 4, (int64_t)(gridDim.x - 1 - blockIdx.x) * KA_THREADS + threadIdx.x);
   pdl_wait();
 
   // ---- this CTA's share of the units
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   const int64_t b0 = per * threadIdx.x < a.B ? per * threadIdx.x : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
   int64_t mine = 0;
   for (int64_t b = b0; b < b1; ++b) {
-    mine += ka_seq<TB>(a, b).units;
+    mine += ka_seq<TB, C::EXTRA>(a, b).units;
     if (blockIdx.x == 0 && (a.lens[b] < 0 || a.lens[b] > a.most)) kv_report(a.status);
   }
   int64_t before = mine;  // inclusive sum over the warp's lanes, then exclusive over the CTA
@@ -388,13 +404,13 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     if (threadIdx.x == 0) kv_report(a.status);
     return;
   }
-  const KaShares sh((uint32_t)total, gridDim.x);
+  const KaShares sh((uint32_t)total, gridDim.x, 4 + C::EXTRA);
   if (blockIdx.x >= sh.W) return;
   const uint32_t lo = sh.first(blockIdx.x), start = (uint32_t)before * hrs;
   if (lo >= start && lo < start + (uint32_t)mine * hrs) {
     uint32_t p = start;
     for (int64_t b = b0; b < b1; ++b) {
-      const uint32_t n = (b1 - b0 == 1 ? (uint32_t)mine : ka_seq<TB>(a, b).units) * hrs;
+      const uint32_t n = (b1 - b0 == 1 ? (uint32_t)mine : ka_seq<TB, C::EXTRA>(a, b).units) * hrs;
       if (lo < p + n) {
         found[0] = (int)b;
         found[1] = (int)p;
@@ -404,17 +420,17 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     }
   }
   __syncthreads();
-  KaWalk<TB> at;
+  KaWalk<TB, C::EXTRA> at;
   at.u = lo;
   at.hi = sh.first(blockIdx.x + 1);
   at.b = found[0];
-  at.s = ka_seq<TB>(a, at.b);
+  at.s = ka_seq<TB, C::EXTRA>(a, at.b);
   const uint32_t in = lo - (uint32_t)found[1];
   at.hr = (int)(in / at.s.units);
   at.seg0 = lo - (in - at.hr * at.s.units);
 
   // ---- the ring's front: this warp's chunks of the share, keys and values alternating
-  KaWalk<TB> ahead = at;
+  KaWalk<TB, C::EXTRA> ahead = at;
   int next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to();
   int64_t row = -1;     // lane i: the first row of the warp's i-th block from the last look at the table
   int used = 32;        // blocks of it that are used up
@@ -503,6 +519,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 
   // ---- one pair after another
   for (; !at.done(); at.next(a, hrs)) {
+    if (!at.any()) continue;  // the share ends before the pair's first token
     const int h = at.hr / tiles, r0 = (at.hr - h * tiles) * KA_ROWS, rows = G - r0 < KA_ROWS ? G - r0 : KA_ROWS;
     const int64_t q0 = ((int64_t)at.b * H + h) * G + r0;  // the tile's first query head
     uint32_t qb[C::QS ? 1 : KS][NT][2];  // B fragments: head 8 x + g, two pairs of dims of each 16-dim step
@@ -847,7 +864,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     }
 
     // ---- join the four warps, eight heads at a time, and write the pair's result or its part
-    const bool whole = at.u == at.seg0 && at.stop() == at.seg0 + at.s.units;
+    const bool whole = at.whole();
     float* part = slots + (2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1)) * C::PART;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -905,14 +922,14 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     if (whole) continue;
 
     // ---- split pair: the last CTA to arrive joins the parts, first to last
-    const uint32_t c0 = sh.owner(at.seg0), c1 = sh.owner(at.seg0 + at.s.units - 1);
+    const uint32_t c0 = sh.owner(at.seg0 + C::EXTRA), c1 = sh.owner(at.seg0 + at.s.units - 1);
     const int64_t pair = (int64_t)at.b * hrs + at.hr;
     __syncthreads();  // the CTA's part is written; the counter's release and acquire order it and the others' parts
     if (threadIdx.x == 0) *last_one = count_up(counters + pair) == (int)(c1 - c0);
     __syncthreads();
     if (!*last_one) continue;
     const int parts = (int)(c1 - c0) + 1;
-    const int64_t s0 = 2 * (int64_t)c0 + (sh.first(c0) == at.seg0 ? 0 : 1);  // the others' first pair is this one
+    const int64_t s0 = 2 * (int64_t)c0 + (sh.first(c0) >= at.seg0 ? 0 : 1);  // the others' first pair is this one
     ka_join<KIND, D, NT>(a, slots + s0 * C::PART, slots + 2 * (int64_t)c0 * C::PART, parts, q0, rows, vg, merge, mls);
     if (threadIdx.x == 0) counters[pair] = 0;
   }
@@ -931,10 +948,10 @@ cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, float* slots
     if (e != cudaSuccess) return e;
     if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_release);
   }
-  // no more CTAs than four units each of the longest lengths
+  // no more CTAs than the longest lengths make shares
   const int64_t per = (tokens + 16 * C::TB - 1) / (16 * C::TB);
   const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
-  const int64_t want = (pairs * (per > 0 ? per : 1) + 3) / 4, all = (int64_t)C::CTAS * sms;
+  const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4), all = (int64_t)C::CTAS * sms;
   return launch_kernel(kv_attention_kernel<KIND, D, NT>, dim3((unsigned)(want < all ? want : all)), dim3(KA_THREADS),
                        C::SMEM, stream, a, slots, counters);
 }
