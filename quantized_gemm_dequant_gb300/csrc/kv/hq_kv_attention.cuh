@@ -13,8 +13,8 @@
 //    partial results in the workspace, and the last CTA to arrive joins them in order.  The lengths are read on the
 //    device, so a captured call follows them.
 //  - The four warps of a CTA each stream every fourth chunk of 16 or 32 tokens through a ring of their own in shared
-//    memory (cp.async, 16 bytes a lane, one slot per chunk and side); no barrier but the warp's own until a pair's
-//    parts are joined.  The ring runs ahead across pairs.
+//    memory (cp.async, 16 bytes a lane); no barrier but the warp's own until a pair's parts are joined.  The ring runs
+//    ahead across pairs.  Two or three CTAs per SM, as their registers allow, hide each other's ends of pairs.
 //  - Products run on mma.sync m16n8k16 with 16 tokens as the rows and 8 query heads as the columns, s^T = K q^T and
 //    o^T = V^T p^T: the codes are the A operand of both, so their decoding is shared by up to 16 heads, and a group of
 //    8 heads wastes nothing.  Between the two, movmatrix turns p.  (A tcgen05 tile would need the decoded operands
@@ -180,12 +180,14 @@ __device__ __forceinline__ uint32_t f16_of_bytes(uint32_t x) {
 __device__ __forceinline__ void ka_prefetch(const void* p, int64_t bytes, int64_t i) {
   if (i * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)p + i * 128));
 }
+
 // counter + 1, ordered after the CTA's writes (made visible by its barrier) and before its later reads
 __device__ __forceinline__ int count_up(int* counter) {
   int old;
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
   return old;
 }
+
 // The list cut into W nearly equal shares: the first `more` of them have q + 1 units, the others q.
 struct KaShares {
   uint32_t W, q, more;
@@ -203,9 +205,9 @@ struct KaShares {
   }
 };
 
-// One sequence's share of the list of units.
+// One sequence's place in the list of units.
 struct KaSeq {
-  int n, j0, t0;  // tokens, the first that is seen, and that one's block
+  int n, j0, t0;   // tokens, the first that is seen, and that one's block
   uint32_t units;  // per (head, row tile): X for the pair itself, then its tokens' (one at least: an empty sequence's
                    // output is written too)
 };
@@ -255,10 +257,10 @@ struct KaWalk {
 // One row's result: 4 dims of o, and lse
 __device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, int d, float4 y, float top, float sum,
                                          float gain) {
-  const float inv = sum > 0.0f ? gain / sum : 0.0f;
+  const float inv = sum == 0.0f ? 0.0f : gain / sum;  // a NaN stays one
   *reinterpret_cast<uint2*>(a.out + q * D + d) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  if (d == 0 && a.lse) a.lse[q] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (d == 0 && a.lse) a.lse[q] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Joins the parts of a split pair, first to last, and stores its rows: parts k > 0 are at `others`, two slots apart.  A
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
         for (int i = 0; i < TB * NT * 4; ++i) {
           float& y = (&s[0][0][0])[i];
-          y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(fminf(y, 80.0f))));
+          y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(y > 80.0f ? 80.0f : y)));
         }
       }
       if (seen != FULL) {
@@ -724,8 +726,12 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         vl[t][0] = vl[t][1] = 0.0f;
         if constexpr (F8) {  // a scale under 2^-100 counts as that: its values are as good as zero
           const uint8_t* vscale = vslot_p + t * C::BLOCK + 16 * C::RB;
-          vl[t][0] = lg2(fmaxf(*reinterpret_cast<const float*>(vscale + 4 * g), 7.8886091e-31f));
-          vl[t][1] = lg2(fmaxf(*reinterpret_cast<const float*>(vscale + 4 * g + 32), 7.8886091e-31f));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float v = *reinterpret_cast<const float*>(vscale + 4 * g + 32 * i);
+            vl[t][i] = lg2(v < 7.8886091e-31f ? 7.8886091e-31f : v);
+            if (seen != FULL && !((seen >> (16 * t + g + 8 * i)) & 1u)) vl[t][i] = 0.0f;  // whatever is there
+          }
         }
       }
       if constexpr (KIND == HQ_KV_NVFP4) {

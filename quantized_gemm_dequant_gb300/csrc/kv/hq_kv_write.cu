@@ -11,6 +11,7 @@
 // exchange between lanes and a lane's four angles serve both; otherwise it holds eight neighbouring dims.  Sums of
 // squares and largest magnitudes are shuffles inside the head's lanes.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -35,6 +36,7 @@ __device__ __forceinline__ float quotient(float x, float y, float yi) {
   return __fmaf_rn(__fmaf_rn(-q, y, x), yi, q);
 }
 constexpr float KW_FAST = 7.8886091e-31f;  // 2^-100
+__device__ __forceinline__ bool quick(float y) { return y == 0.0f || (y >= KW_FAST && y < INFINITY); }
 
 // A head's row in its lanes: dims lo .. lo + 3 and hi .. hi + 3 of each lane.
 struct Row {
@@ -106,7 +108,7 @@ template <int KIND, int D>
 __device__ __forceinline__ float scale_of(const float (&x)[8], float g, uint32_t& byte) {
   if constexpr (KIND == HQ_KV_E4M3) {
     const float m = lanes_max<D / 8>(largest(x));
-    return m >= KW_FAST ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
+    return m >= KW_FAST && m < INFINITY ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
   } else {
     const float m = lanes_max<2>(largest(x));
     byte = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
       } else {
         uint32_t kb = 0, vb = 0;
         const float ks = scale_of<KIND, D>(f, kg, kb), vs = scale_of<KIND, D>(g, vg, vb);
-        if (__all_sync(0xffffffffu, (ks >= KW_FAST || ks == 0.0f) && (vs >= KW_FAST || vs == 0.0f))) {
+        if (__all_sync(0xffffffffu, quick(ks) && quick(vs))) {
           const float ki = __frcp_rn(ks), vi = __frcp_rn(vs);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], ks, ki), g[i] = quotient(g[i], vs, vi);

@@ -152,6 +152,27 @@ def test_codes_are_the_oracles(lib, D):
             assert np.array_equal(got, codes.reshape(T, heads, -1)[keep]), (kind, side)
 
 
+def test_infinities_and_nan_in_a_row(lib):
+    """An infinite value makes its e4m3 row's scale infinite and itself NaN, the others' codes zero, as x / s does; a NaN
+    is itself alone.  Other rows are as without it."""
+    T, H, D = 4, 1, 64
+    x = _rows(3, T, H, H, D)
+    x = torch.where(x == 0, torch.ones_like(x), x)
+    clean = lib.make_kv_cache("e4m3", 1, 16, H, D)
+    _call(lib, clean, x.cuda(), torch.arange(T), H)
+    x.view(T, 3, D)[1, 1:, 5] = float("inf")
+    x.view(T, 3, D)[2, 1:, 7] = float("nan")
+    c = lib.make_kv_cache("e4m3", 1, 16, H, D)
+    _call(lib, c, x.cuda(), torch.arange(T), H)
+    for side in ("k", "v"):
+        codes, s, was = getattr(c, side)[0, 0].cpu(), getattr(c, side + "_scale")[0, 0].cpu(), getattr(clean, side)[0, 0].cpu()
+        assert torch.isinf(s[1]) and (codes[1, 5] & 0x7F) == 0x7F
+        rest = torch.arange(D) != 5
+        assert not (codes[1][rest] & 0x7F).any()
+        assert torch.isfinite(s[2]) and (codes[2, 7] & 0x7F) == 0x7F and ((codes[2][torch.arange(D) != 7] & 0x7F) != 0x7F).all()
+        assert torch.equal(codes[[0, 3]], was[[0, 3]])
+
+
 @pytest.mark.parametrize("kind", K.KINDS)
 def test_rows_of_a_wider_tensor(lib, kind):
     """The rows of a projection that computes more than q, k and v: strided rows give what contiguous ones give."""

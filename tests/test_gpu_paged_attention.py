@@ -155,6 +155,45 @@ def test_bad_indices_are_left_out_and_reported(lib, kind):
     _check(got, K.attention(c, q, table, lens, 64 ** -0.5))
 
 
+@pytest.mark.parametrize("kind", K.KINDS)
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_nan_in_a_seen_place_is_not_hidden(lib, kind, softcap):
+    """A NaN key makes its heads' rows NaN, a NaN value its dims', in that sequence and key-value head alone."""
+    lens, page, D = [300, 300, 40], 16, 64
+    table, pages = K.tables(lens, page)
+    c = _cache(lib, kind, pages, page, 2, D, 7)
+    for b, side, j in ((0, "k", 290), (1, "v", 5)):  # (sequence 0, head 0, key 290), (sequence 1, head 1, value 5)
+        p, o = int(table[b, j // page]), j % page
+        if kind == "bf16":
+            getattr(c, side)[p, b, o, 3] = float("nan")
+        elif kind == "e4m3":
+            getattr(c, side)[p, b, o, 3] = 0x7F
+        else:  # e2m1 has no NaN: the block's scale
+            getattr(c, side + "_scale")[p, b, o, 0] = 0x7F
+            getattr(c, side)[p, b, o, :8] = 0x11  # codes that are not zero
+    q = _q(2, 3, 8, D)
+    out, lse = lib.paged_attention(c, q, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), softcap=softcap)
+    torch.cuda.synchronize()
+    want, wl, bo, bl = K.attention(c, q, table, lens, D ** -0.5, softcap=softcap)
+    got = K.f64(out)
+    nan = np.zeros_like(got, bool)
+    nan[0, :4] = True
+    nan[1, 4:, 3 if kind != "nvfp4" else slice(0, 16)] = True
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(np.isnan(K.f64(lse)), nan.all(-1))
+    assert np.all(np.abs(got - want)[~nan] <= bo[~nan])
+
+
+def test_nan_value_scale_is_not_hidden(lib):
+    lens = [20, 20]
+    table, pages = K.tables(lens, 16)
+    c = _cache(lib, "e4m3", pages, 16, 1, 64, 7)
+    c.v_scale[int(table[0, 1]), 0, 2] = float("nan")
+    out, _ = lib.paged_attention(c, _q(2, 2, 2, 64), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert out[0].isnan().all() and not out[1].isnan().any()
+
+
 def test_empty_batch_and_empty_table(lib):
     c = _cache(lib, "bf16", 2, 16, 2, 64, 0)
     out, lse = lib.paged_attention(c, _q(0, 0, 4, 64), torch.empty((0, 3), dtype=torch.int32, device="cuda"),
