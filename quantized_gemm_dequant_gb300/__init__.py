@@ -167,7 +167,6 @@ _SCALE_BYTES = {HQ_S_BF16: 2, HQ_S_UE4M3: 1, HQ_S_UE8M0: 1}
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
-_I64 = (torch.int64,)
 _U8 = (torch.uint8,)
 
 
@@ -587,6 +586,12 @@ def _on(stream, make, *a, **k):
         return make(*a, **k)
 
 
+# A decoding step makes these calls for every layer, so a call whose tensors are right looks at each of them once, in
+# place; at the first one that is not, _kv_ptrs judges them all and raises.
+_bf16, _f32, _i32t, _i64t = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _kv_cache(w, cache):
     if not isinstance(cache, KVCache):
         raise HQArgError(w, f"cache must be a KVCache, not {type(cache).__name__}")
@@ -594,29 +599,18 @@ def _kv_cache(w, cache):
 
 
 def _kv_ptrs(w, c, items):
-    """Addresses of a call's tensors: items are (tensor or None, name, elements that the call reads or writes, dtype or
-    None).  One look at each right tensor, because a decoding step makes this call for every layer; at the first one
-    that is not, _Args judges them all and raises."""
-    dev, out = c._index, []
-    for t, _, n, dt in items:
-        if t is None:
-            out.append(None)
-        elif (isinstance(t, torch.Tensor) and (t.dtype is dt or dt is None) and t.get_device() == dev
-              and t.numel() >= n and t.is_contiguous()):
-            out.append(t.data_ptr())
-        else:
-            break
-    else:
-        if torch._C._cuda_getDevice() == dev:
-            return out
+    """Addresses of a call's tensors, each checked: items are (tensor or None, name, elements that the call reads or
+    writes, dtype or None)."""
     args = _Args(w)
     for t, name, n, dt in items:
         args.add(t, name, n * (dt.itemsize if dt else 1), (dt,) if dt else None)
     return [None if p is None else p.value for p in args.add(c.k, "cache.k").ptrs()][:-1]
 
 
-def _kv_stream(c, stream):
-    return torch._C._cuda_getCurrentRawStream(c._index) if stream is None else stream.cuda_stream
+def _kv_right(t, dtype, elements, dev):
+    """Whether an optional tensor of a call is right."""
+    return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+                         and t.numel() >= elements and t.is_contiguous())
 
 
 def _kv_table(w, page_table, batch):
@@ -652,21 +646,30 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
             raise HQArgError(w, "cos_sin has no angles; pass None for no rotation")
         if positions is None:
             raise HQArgError(w, "positions are required with cos_sin")
-    bf16 = torch.bfloat16
-    px, psl, pqn, pkn, pcs, pps, pq, pws = _kv_ptrs(w, c, (
-        (x, "qkv", row if x is not qkv else T * row, bf16), (slots, "slots", T, torch.int64),
-        (q_norm, "q_norm", D, bf16), (k_norm, "k_norm", D, bf16), (cos_sin, "cos_sin", P * R, torch.float32),
-        (positions if R else None, "positions", T, torch.int32), (q_out, "q_out", T * Hq * D, bf16),
-        (workspace, "workspace", 0, None)))
+    dev = c._index
+    if (x.dtype is _bf16 and x.get_device() == dev and x.is_contiguous() and _device() == dev
+            and _kv_right(slots, _i64t, T, dev) and slots is not None and _kv_right(q_norm, _bf16, D, dev)
+            and _kv_right(k_norm, _bf16, D, dev) and _kv_right(cos_sin, _f32, 0, dev)
+            and (R == 0 or _kv_right(positions, _i32t, T, dev)) and _kv_right(q_out, _bf16, T * Hq * D, dev)
+            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+        px, psl = x.data_ptr(), slots.data_ptr()
+        pqn, pkn = 0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr()
+        pcs, pps = (cos_sin.data_ptr(), positions.data_ptr()) if R else (0, 0)
+    else:
+        px, psl, pqn, pkn, pcs, pps, _, _ = (p or 0 for p in _kv_ptrs(w, c, (
+            (x, "qkv", row if x is not qkv else T * row, _bf16), (slots, "slots", T, _i64t),
+            (q_norm, "q_norm", D, _bf16), (k_norm, "k_norm", D, _bf16), (cos_sin, "cos_sin", P * R, _f32),
+            (positions if R else None, "positions", T, _i32t), (q_out, "q_out", T * Hq * D, _bf16),
+            (workspace, "workspace", 0, None))))
     if q_out is None:
-        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=bf16, device=c.device)
-        pq = q_out.data_ptr()
+        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=_bf16, device=c.device)
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-        pws = workspace.data_ptr()
-    r = _KV_ROWS.pack(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn or 0, pkn or 0, pcs or 0, P, pps or 0,
-                      psl or 0, pq)
-    _check(_lib.hq_kv_write(*c._refs, r, pws, workspace.numel() * workspace.element_size(), _kv_stream(c, stream)), w)
+    r = _KV_ROWS.pack(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl, q_out.data_ptr())
+    st = _lib.hq_kv_write(*c._refs, r, workspace.data_ptr(), workspace.nbytes,
+                          _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
     return q_out
 
 
@@ -678,23 +681,27 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
     c = _kv_cache(w, cache)
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
         raise HQArgError(w, "starts must be a 1-D [B + 1] tensor")
-    B, total, bf16 = starts.shape[0] - 1, int(total), torch.bfloat16
+    B, total = starts.shape[0] - 1, int(total)
     size = total * c.num_heads * c.head_dim
     ko, vo = (None, None) if out is None else out
-    cols = _kv_table(w, page_table, B)
-    pt, pst, pf, pk, pv, pws = _kv_ptrs(w, c, (
-        (page_table, "page_table", B * cols, torch.int32), (starts, "starts", B + 1, torch.int64),
-        (first, "first", B, torch.int32), (ko, "out[0]", size, bf16), (vo, "out[1]", size, bf16),
-        (workspace, "workspace", 0, None)))
+    cols, dev = _kv_table(w, page_table, B), c._index
+    if (_kv_right(page_table, _i32t, 0, dev) and _kv_right(starts, _i64t, 0, dev) and _kv_right(first, _i32t, B, dev)
+            and _kv_right(ko, _bf16, size, dev) and _kv_right(vo, _bf16, size, dev) and _device() == dev
+            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+        pt, pst, pf = page_table.data_ptr(), starts.data_ptr(), None if first is None else first.data_ptr()
+    else:
+        pt, pst, pf, _, _, _ = _kv_ptrs(w, c, (
+            (page_table, "page_table", B * cols, _i32t), (starts, "starts", B + 1, _i64t), (first, "first", B, _i32t),
+            (ko, "out[0]", size, _bf16), (vo, "out[1]", size, _bf16), (workspace, "workspace", 0, None)))
     if out is None:
-        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=bf16, device=c.device)
+        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=_bf16, device=c.device)
                   for _ in range(2))
-        pk, pv = ko.data_ptr(), vo.data_ptr()
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-        pws = workspace.data_ptr()
-    _check(_lib.hq_kv_read(*c._refs, pt, cols, pst, pf, B, total, pk, pv, pws, _nbytes(workspace),
-                           _kv_stream(c, stream)), w)
+    st = _lib.hq_kv_read(*c._refs, pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr(), workspace.data_ptr(),
+                         workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
     return ko, vo
 
 
@@ -709,20 +716,26 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != c.head_dim:
         raise HQArgError(w, f"q must be a 3-D [B, q_heads, {c.head_dim}] tensor")
     B, Hq, D = q.shape
-    size, cols = B * Hq * D, _kv_table(w, page_table, B)
-    pq, pt, pn, po, pl, pws = _kv_ptrs(w, c, (
-        (q, "q", size, torch.bfloat16), (page_table, "page_table", B * cols, torch.int32),
-        (lens, "lens", B, torch.int32), (out, "out", size, torch.bfloat16), (lse, "lse", B * Hq, torch.float32),
-        (workspace, "workspace", 0, None)))
+    cols, dev = _kv_table(w, page_table, B), c._index
+    if (q.dtype is _bf16 and q.get_device() == dev and q.is_contiguous() and _device() == dev
+            and page_table.dtype is _i32t and page_table.get_device() == dev and page_table.is_contiguous()
+            and lens is not None and _kv_right(lens, _i32t, B, dev) and _kv_right(out, _bf16, B * Hq * D, dev)
+            and _kv_right(lse, _f32, B * Hq, dev)
+            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+        pq, pt, pn = q.data_ptr(), page_table.data_ptr(), lens.data_ptr()
+    else:
+        pq, pt, pn, _, _, _ = _kv_ptrs(w, c, (
+            (q, "q", B * Hq * D, _bf16), (page_table, "page_table", B * cols, _i32t), (lens, "lens", B, _i32t),
+            (out, "out", B * Hq * D, _bf16), (lse, "lse", B * Hq, _f32), (workspace, "workspace", 0, None)))
     if out is None:
         out = _on(stream, torch.empty_like, q)
-        po = out.data_ptr()
     if lse is None:
-        lse = _on(stream, torch.empty, (B, Hq), dtype=torch.float32, device=c.device)
-        pl = lse.data_ptr()
+        lse = _on(stream, torch.empty, (B, Hq), dtype=_f32, device=c.device)
     if workspace is None:
         workspace = make_kv_workspace(c, B, Hq, stream=stream)
-        pws = workspace.data_ptr()
-    _check(_lib.hq_paged_attention(*c._refs, pq, Hq, pt, cols, pn, B, D ** -0.5 if scale is None else scale, window,
-                                   softcap, po, pl, pws, _nbytes(workspace), _kv_stream(c, stream)), w)
+    st = _lib.hq_paged_attention(*c._refs, pq, Hq, pt, cols, pn, B, D ** -0.5 if scale is None else scale, window,
+                                 softcap, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
     return out, lse
