@@ -405,24 +405,35 @@ HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* ca
                               int64_t total, void* k_out, void* v_out, void* workspace, size_t ws_bytes,
                               hq_stream_t stream);
 
+/* One hq_paged_attention call. */
+typedef struct {
+  const void* q;             /* bf16 [B][num_q_heads][head_dim]; the new token's own key and value are already cached */
+  const int32_t* page_table; /* int32 [B][table_stride]; entries past a sequence's last page are not read */
+  int64_t table_stride;
+  const int32_t* lens;       /* int32 [B], 0 <= lens[b] <= table_stride * page_size and 2^30 */
+  int64_t B;                 /* sequences, >= 0 */
+  int64_t window;            /* tokens that are seen, 0 = all of them */
+  int32_t num_q_heads;       /* a multiple of the format's num_heads */
+  float scale;
+  float softcap;             /* 0 = none */
+  void* out;                 /* bf16 [B][num_q_heads][head_dim] */
+  float* lse;                /* fp32 [B][num_q_heads], natural logarithm, or NULL */
+} hq_kv_attention_t;
+
 /* Attention of one new token per sequence over its cached tokens.  Query head h reads key-value head
  * h / (num_q_heads / num_heads).  With n = lens[b], for the tokens j in [max(0, n - window), n):
  *   s_j = scale * (q . k_j), or softcap * tanh(scale * (q . k_j) / softcap) when softcap > 0
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
- * A sequence of length 0 gives out = 0 and lse = -inf.
- *   q           bf16 [B][num_q_heads][head_dim]; the new token's own key and value are already in the cache
- *   page_table  int32 [B][table_stride]; entries past the sequence's last page are not read
- *   lens        int32 [B], 0 <= lens[b] <= table_stride * page_size and 2^30
- *   window      tokens that are seen, 0 = all of them
- *   out         bf16 [B][num_q_heads][head_dim];  lse  fp32 [B][num_q_heads] (natural logarithm) or NULL
+ * A sequence of length 0 gives out = 0 and lse = -inf.  Places that are not seen may hold anything.
  * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) are rounded to the
- * values' 16-bit type before they multiply them.  A length outside its range is taken as the nearest end of it, and
- * tokens on a page outside the pools are left out; both record HQ_ERR_INVALID_ARG.  Results do not depend on timing:
- * the length is split by a fixed rule and the parts are joined in order.  One kernel. */
-HQ_API hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const void* q,
-                                      int32_t num_q_heads, const int32_t* page_table, int64_t table_stride,
-                                      const int32_t* lens, int64_t B, float scale, int64_t window, float softcap,
-                                      void* out, float* lse, void* workspace, size_t ws_bytes, hq_stream_t stream);
+ * values' 16-bit type before they multiply them.  E4M3 scales are not negative; a value scale under 2^-100 counts as
+ * 2^-100.  A length outside its range is taken as the nearest end of it, and tokens on a page outside the pools are
+ * left out; both record HQ_ERR_INVALID_ARG, as do lengths that make more than 2^31 units of 16 tokens and heads (then
+ * nothing is written).  Results do not depend on timing: the length is split by a fixed rule and the parts are joined
+ * in order.  One kernel. */
+HQ_API hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache,
+                                      const hq_kv_attention_t* args, void* workspace, size_t ws_bytes,
+                                      hq_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 HQ_API const char* hq_status_string(hq_status_t status);

@@ -68,13 +68,21 @@ class KVRows(ctypes.Structure):
                 ("slots", ctypes.c_void_p), ("q_out", ctypes.c_void_p)]
 
 
-_KV_ROWS = struct.Struct("@PqqiiifPPPqPPP")  # KVRows, packed in one step
+class KVAttention(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("B", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("num_q_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
+# KVRows and KVAttention, packed in one step
+_KV_ROWS, _KV_ATTENTION = struct.Struct("@PqqiiifPPPqPPP"), struct.Struct("@PPqPqqiffPP")
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _F = ctypes.POINTER(Format)
 _A = ctypes.POINTER(Act)
-_KF, _KP, _f32 = ctypes.POINTER(KVFormat), ctypes.POINTER(KVPools), ctypes.c_float
+_KF = ctypes.POINTER(KVFormat)
 _lib.hq_packed_bytes.argtypes = [_F]
 _lib.hq_packed_bytes.restype = _sz
 _lib.hq_pack_weights.argtypes = [_F, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -111,12 +119,11 @@ _lib.hq_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.hq_set_wait_limit_ns.restype = None
 _lib.hq_kv_workspace_bytes.argtypes = [_KF, _i64, _i32]
 _lib.hq_kv_workspace_bytes.restype = _sz
-_lib.hq_kv_write.argtypes = [_KF, _KP, _vp, _vp, _sz, _vp]
+_lib.hq_kv_write.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_write.restype = ctypes.c_int
-_lib.hq_kv_read.argtypes = [_KF, _KP, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.hq_kv_read.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_read.restype = ctypes.c_int
-_lib.hq_paged_attention.argtypes = [_KF, _KP, _vp, _i32, _vp, _i64, _vp, _i64, _f32, _i64, _f32, _vp, _vp, _vp, _sz,
-                                    _vp]
+_lib.hq_paged_attention.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_paged_attention.restype = ctypes.c_int
 _lib.hq_status_string.argtypes = [ctypes.c_int]
 _lib.hq_status_string.restype = ctypes.c_char_p
@@ -539,7 +546,7 @@ class KVCache:
         # the handle keeps the pools alive and their addresses with them: they must not be resized
         self._pools = KVPools(*(None if t is None else t.data_ptr() for t in
                                 (k, v, k_scale, v_scale, k_global, v_global)))
-        self._refs = ctypes.byref(self.fmt), ctypes.byref(self._pools)
+        self._at = ctypes.addressof(self.fmt), ctypes.addressof(self._pools)
 
 
 def make_kv_cache(kind, num_pages, page_size, num_heads, head_dim, k_amax=None, v_amax=None, device="cuda"):
@@ -662,11 +669,12 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
             (positions if R else None, "positions", T, _i32t), (q_out, "q_out", T * Hq * D, _bf16),
             (workspace, "workspace", 0, None))))
     if q_out is None:
-        q_out = _on(stream, torch.empty, (T, Hq, D), dtype=_bf16, device=c.device)
+        q_out = (torch.empty((T, Hq, D), dtype=_bf16, device=c.device) if stream is None else
+                 _on(stream, torch.empty, (T, Hq, D), dtype=_bf16, device=c.device))
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
     r = _KV_ROWS.pack(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl, q_out.data_ptr())
-    st = _lib.hq_kv_write(*c._refs, r, workspace.data_ptr(), workspace.nbytes,
+    st = _lib.hq_kv_write(*c._at, r, workspace.data_ptr(), workspace.nbytes,
                           _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
         raise HQError(st, w)
@@ -694,11 +702,11 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
             (page_table, "page_table", B * cols, _i32t), (starts, "starts", B + 1, _i64t), (first, "first", B, _i32t),
             (ko, "out[0]", size, _bf16), (vo, "out[1]", size, _bf16), (workspace, "workspace", 0, None)))
     if out is None:
-        ko, vo = (_on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=_bf16, device=c.device)
-                  for _ in range(2))
+        ko = _on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=_bf16, device=c.device)
+        vo = _on(stream, torch.empty_like, ko)
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-    st = _lib.hq_kv_read(*c._refs, pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr(), workspace.data_ptr(),
+    st = _lib.hq_kv_read(*c._at, pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr(), workspace.data_ptr(),
                          workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
         raise HQError(st, w)
@@ -724,17 +732,19 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
             and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
         pq, pt, pn = q.data_ptr(), page_table.data_ptr(), lens.data_ptr()
     else:
-        pq, pt, pn, _, _, _ = _kv_ptrs(w, c, (
+        pq, pt, pn, _, _, _ = (p or 0 for p in _kv_ptrs(w, c, (
             (q, "q", B * Hq * D, _bf16), (page_table, "page_table", B * cols, _i32t), (lens, "lens", B, _i32t),
-            (out, "out", B * Hq * D, _bf16), (lse, "lse", B * Hq, _f32), (workspace, "workspace", 0, None)))
+            (out, "out", B * Hq * D, _bf16), (lse, "lse", B * Hq, _f32), (workspace, "workspace", 0, None))))
     if out is None:
-        out = _on(stream, torch.empty_like, q)
+        out = torch.empty_like(q) if stream is None else _on(stream, torch.empty_like, q)
     if lse is None:
-        lse = _on(stream, torch.empty, (B, Hq), dtype=_f32, device=c.device)
+        lse = (torch.empty((B, Hq), dtype=_f32, device=c.device) if stream is None else
+               _on(stream, torch.empty, (B, Hq), dtype=_f32, device=c.device))
     if workspace is None:
         workspace = make_kv_workspace(c, B, Hq, stream=stream)
-    st = _lib.hq_paged_attention(*c._refs, pq, Hq, pt, cols, pn, B, D ** -0.5 if scale is None else scale, window,
-                                 softcap, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+    x = _KV_ATTENTION.pack(pq, pt, cols, pn, B, window, Hq, D ** -0.5 if scale is None else scale, softcap,
+                           out.data_ptr(), lse.data_ptr())
+    st = _lib.hq_paged_attention(*c._at, x, workspace.data_ptr(), workspace.nbytes,
                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
         raise HQError(st, w)

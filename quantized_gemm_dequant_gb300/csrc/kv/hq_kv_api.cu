@@ -161,42 +161,42 @@ hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, co
   return launched(launch_kv_read(fmt->kind, fmt->head_dim, a, (cudaStream_t)stream));
 }
 
-hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const void* q,
-                               int32_t num_q_heads, const int32_t* page_table, int64_t table_stride,
-                               const int32_t* lens, int64_t B, float scale, int64_t window, float softcap, void* out,
-                               float* lse, void* workspace, size_t ws_bytes, hq_stream_t stream) {
+hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_attention_t* x,
+                               void* workspace, size_t ws_bytes, hq_stream_t stream) {
   hq_status_t st = check_format(fmt);
   if (st != HQ_OK) return st;
-  if ((st = check_q_heads(fmt, num_q_heads)) != HQ_OK) return st;
-  if (B < 0 || B * num_q_heads > kMaxRows || B > kMaxRows || table_stride < 0 || table_stride > kMaxRows ||
-      window < 0 || !isfinite(scale) || !(softcap >= 0.0f) || isinf(softcap))
+  if (!x) return HQ_ERR_INVALID_ARG;
+  if ((st = check_q_heads(fmt, x->num_q_heads)) != HQ_OK) return st;
+  if (x->B < 0 || x->B > kMaxRows || x->B * x->num_q_heads > kMaxRows || x->table_stride < 0 ||
+      x->table_stride > kMaxRows || x->window < 0 || !isfinite(x->scale) || !(x->softcap >= 0.0f) || isinf(x->softcap))
     return HQ_ERR_INVALID_ARG;
-  if (B == 0) return HQ_OK;
+  if (x->B == 0) return HQ_OK;
   if ((st = check_cache(fmt, cache)) != HQ_OK) return st;
-  if (!q || (table_stride && !page_table) || !lens || !out) return HQ_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(lse, 4))
+  if (!x->q || (x->table_stride && !x->page_table) || !x->lens || !x->out) return HQ_ERR_INVALID_ARG;
+  if (!aligned(x->q, 16) || !aligned(x->page_table, 4) || !aligned(x->lens, 4) || !aligned(x->out, 16) ||
+      !aligned(x->lse, 4))
     return HQ_ERR_ALIGNMENT;
-  if ((st = check_workspace(fmt, B, num_q_heads, workspace, ws_bytes)) != HQ_OK) return st;
+  if ((st = check_workspace(fmt, x->B, x->num_q_heads, workspace, ws_bytes)) != HQ_OK) return st;
   KvAttnArgs a;
   a.kv = view(fmt, cache);
-  a.q = (const uint16_t*)q;
-  a.group = num_q_heads / fmt->num_heads;
-  a.page_table = page_table;
-  a.table_stride = table_stride;
-  a.lens = lens;
-  a.B = B;
-  const int64_t most = table_stride * fmt->page_size;
+  a.q = (const uint16_t*)x->q;
+  a.group = x->num_q_heads / fmt->num_heads;
+  a.page_table = x->page_table;
+  a.table_stride = x->table_stride;
+  a.lens = x->lens;
+  a.B = x->B;
+  const int64_t most = x->table_stride * fmt->page_size;
   a.most = most < kMaxRows ? most : kMaxRows;
-  a.scale = scale;
-  a.window = window;
-  a.softcap = softcap;
-  a.out = (uint16_t*)out;
-  a.lse = lse;
+  a.scale = x->scale;
+  a.window = x->window;
+  a.softcap = x->softcap;
+  a.out = (uint16_t*)x->out;
+  a.lse = x->lse;
   a.status = (int*)workspace;
   const int sms = num_sms();
   float* slots = reinterpret_cast<float*>((uint8_t*)workspace + KV_HEADER_BYTES);
   int* counters = reinterpret_cast<int*>((uint8_t*)workspace + ka_counters_at(sms));
-  const int64_t seen = window > 0 && window < a.most ? window + KV_BLOCK : a.most;
+  const int64_t seen = a.window > 0 && a.window < a.most ? a.window + KV_BLOCK : a.most;
   const auto launch = fmt->kind == HQ_KV_BF16 ? launch_kv_attention_bf16
                                               : (fmt->kind == HQ_KV_E4M3 ? launch_kv_attention_e4m3
                                                                          : launch_kv_attention_nvfp4);

@@ -35,18 +35,22 @@ def test_attention_arguments_are_checked():
     hq = _hq()
     L, f = hq._lib, _fmt(hq)
     c = hq.KVPools(0x10000, 0x20000, 0x30000, 0x40000, None, None)
-    ok = dict(fmt=ctypes.byref(f), cache=ctypes.byref(c), q=0x50000, hq=8, table=0x60000, stride=4, lens=0x70000, B=0,
-              scale=1.0, window=0, cap=0.0, out=0x80000, lse=None, ws=0x90000, n=1 << 40, stream=None)
-    call = lambda **k: L.hq_paged_attention(*{**ok, **k}.values())  # noqa: E731
+    ok = dict(q=0x50000, page_table=0x60000, table_stride=4, lens=0x70000, B=0, window=0, num_q_heads=8, scale=1.0,
+              softcap=0.0, out=0x80000, lse=None)
+
+    def call(fmt=ctypes.byref(f), cache=ctypes.byref(c), ws=0x90000, n=1 << 40, **k):
+        return L.hq_paged_attention(fmt, cache, ctypes.byref(hq.KVAttention(**{**ok, **k})), ws, n, None)
+    assert ctypes.sizeof(hq.KVAttention) == hq._KV_ATTENTION.size and ctypes.sizeof(hq.KVRows) == hq._KV_ROWS.size
     assert call() == hq.HQ_OK  # no sequences
+    assert L.hq_paged_attention(ctypes.byref(f), ctypes.byref(c), None, 0x90000, 1 << 40, None) == hq.HQ_ERR_INVALID_ARG
     bad = ctypes.byref(hq.KVPools(0x10008, 0x20000, 0x30000, 0x40000, None, None))
     none = ctypes.byref(hq.KVPools(0x10000, 0x20000, None, 0x40000, None, None))
-    for over, code in ((dict(fmt=None), hq.HQ_ERR_INVALID_ARG), (dict(hq=7), hq.HQ_ERR_INVALID_ARG),
+    for over, code in ((dict(fmt=None), hq.HQ_ERR_INVALID_ARG), (dict(num_q_heads=7), hq.HQ_ERR_INVALID_ARG),
                        (dict(B=-1), hq.HQ_ERR_INVALID_ARG), (dict(window=-1), hq.HQ_ERR_INVALID_ARG),
-                       (dict(scale=float("nan")), hq.HQ_ERR_INVALID_ARG), (dict(cap=-1.0), hq.HQ_ERR_INVALID_ARG),
+                       (dict(scale=float("nan")), hq.HQ_ERR_INVALID_ARG), (dict(softcap=-1.0), hq.HQ_ERR_INVALID_ARG),
                        (dict(B=2, cache=None), hq.HQ_ERR_INVALID_ARG), (dict(B=2, cache=none), hq.HQ_ERR_INVALID_ARG),
                        (dict(B=2, cache=bad), hq.HQ_ERR_ALIGNMENT), (dict(B=2, q=None), hq.HQ_ERR_INVALID_ARG),
-                       (dict(B=2, table=None), hq.HQ_ERR_INVALID_ARG), (dict(B=2, q=0x50002), hq.HQ_ERR_ALIGNMENT),
+                       (dict(B=2, page_table=None), hq.HQ_ERR_INVALID_ARG), (dict(B=2, q=0x50002), hq.HQ_ERR_ALIGNMENT),
                        (dict(B=2, ws=None), hq.HQ_ERR_WORKSPACE), (dict(B=2, n=8), hq.HQ_ERR_WORKSPACE),
                        (dict(B=1 << 29), hq.HQ_ERR_INVALID_ARG)):
         assert call(**over) == code, over
