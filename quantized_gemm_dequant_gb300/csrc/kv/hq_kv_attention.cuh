@@ -25,8 +25,7 @@
 //  - e4m3: a token's key scale multiplies its score.  Its value scale v multiplies its weight, and a weight must fit
 //    f16: the running maximum is taken over s_j + log2 v_j, so that the largest weight times its scale is about one
 //    whatever the scales' range, while l sums exp2(s_j - m) in fp32 beside it.
-//  - nvfp4: code * 2^-14 * block scale is exact in f16 (6 significant bits, a multiple of 2^-24); the global scales and
-//    2^14 go to q's scale and to o.
+//  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and to o.
 //  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
 //  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
 //    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.
@@ -164,16 +163,15 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(x));
 }
-// The low and the high nibbles of x's four bytes as the high bytes of f16: sign on top, exponent and fraction bits at
-// f16's lowest exponent and highest fraction bits, which is the code's value times 2^-14, subnormals too.
-__device__ __forceinline__ void e2m1_bytes(uint32_t x, uint32_t& low, uint32_t& high) {
-  low = ((x << 4) & 0x80808080u) | ((x << 1) & 0x0E0E0E0Eu);
-  high = (x & 0x80808080u) | ((x >> 3) & 0x0E0E0E0Eu);
-}
-// bytes i and j of x as the high bytes of two f16
-template <int I, int J>
-__device__ __forceinline__ uint32_t f16_of_bytes(uint32_t x) {
-  return __byte_perm(x, 0, 0x4 | I << 4 | 0x4 << 8 | J << 12);
+// both halves the low, or the high half
+template <int HALF>
+__device__ __forceinline__ uint32_t dup16(uint32_t x) {
+  uint32_t d;
+  if constexpr (HALF)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(x));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(x));
+  return d;
 }
 
 // L2 line i of a range, if it has one
@@ -515,7 +513,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   float kg = 1.0f, vg = 1.0f;
   if constexpr (KIND == HQ_KV_NVFP4) {
     kg = *a.kv.k_global;
-    vg = *a.kv.v_global * 16384.0f;
+    vg = *a.kv.v_global;
   }
   const float cap = a.softcap * 1.4426950408889634f;
 
@@ -641,29 +639,38 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           }
         } else {
           // a unit is 32 dims: two steps, two block scales; lanes c = 0, 1 hold the first block's dims
-          uint32_t sc[2][D / 32];  // of tokens g and g + 8
-          const uint32_t ksel = c < 2 ? 0x00 : 0x11;
+          uint32_t sc[2][D / 64];  // of tokens g and g + 8, two units' each
+          const uint32_t ksel = c < 2 ? 0x6420 : 0x7531;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* from = kscale + (g + 8 * i) * C::SB;
+            if constexpr (D == 64) {
+              sc[i][0] = e4m3x2_to_f16x2(__byte_perm(*reinterpret_cast<const uint32_t*>(from), 0, ksel));
+            } else {
 #pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(kscale + (g + 8 * i) * C::SB + 4 * w);
-              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(x, 0, ksel));
-              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(x, 0, ksel + 0x22));
+              for (int w = 0; w < D / 128; ++w) {
+                const uint2 x = *reinterpret_cast<const uint2*>(from + 8 * w);
+                const uint32_t y = __byte_perm(x.x, x.y, ksel);
+                sc[i][2 * w] = e4m3x2_to_f16x2(y);
+                sc[i][2 * w + 1] = e4m3x2_to_f16x2(y >> 16);
+              }
             }
+          }
 #pragma unroll
           for (int u = 0; u < D / 32; u += 2) {
             uint32_t r[4], f[2];
             ldsm_x4(kb + C::at(lr, u + lu), r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+              const uint32_t s0 = i ? dup16<1>(sc[0][u / 2]) : dup16<0>(sc[0][u / 2]),
+                             s1 = i ? dup16<1>(sc[1][u / 2]) : dup16<0>(sc[1][u / 2]);
               uint32_t y[4], z[4];
               e2m1x8_to_f16x2(r[2 * i], y);
               e2m1x8_to_f16x2(r[2 * i + 1], z);
 #pragma unroll
               for (int p = 0; p < 2; ++p) {
-                const uint32_t a0 = hmul2(y[2 * p], sc[0][u + i]), a1 = hmul2(z[2 * p], sc[1][u + i]),
-                               a2 = hmul2(y[2 * p + 1], sc[0][u + i]), a3 = hmul2(z[2 * p + 1], sc[1][u + i]);
+                const uint32_t a0 = hmul2(y[2 * p], s0), a1 = hmul2(z[2 * p], s1), a2 = hmul2(y[2 * p + 1], s0),
+                               a3 = hmul2(z[2 * p + 1], s1);
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                   qfrag(2 * (u + i) + p, x, f);
@@ -831,34 +838,43 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         } else {
           // a unit is 32 dims: a lane gets dims 4 g .. 4 g + 3 of two tokens; two tiles of two of them each
           uint32_t sc[2][D / 32];  // of tokens 2 c, 2 c + 1, and 8 on
-          const uint32_t sel = g < 4 ? 0x0040u : 0x0051u;  // the first or second block's byte of each token
+          const uint32_t vsel = g < 4 ? 0x6240 : 0x7351;  // the first or second block of each of two units
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* from = vscale + (8 * i + 2 * c) * C::SB;
+            uint32_t x[D / 64], y[D / 64];
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
-              const uint32_t y = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c) * C::SB + 4 * w);
-              const uint32_t z = *reinterpret_cast<const uint32_t*>(vscale + (8 * i + 2 * c + 1) * C::SB + 4 * w);
-              sc[i][2 * w] = e4m3x2_to_f16x2(__byte_perm(y, z, sel));
-              sc[i][2 * w + 1] = e4m3x2_to_f16x2(__byte_perm(y, z, sel + 0x0022u));
+              if constexpr (D == 128) {
+                if (w == 0) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(from);
+                  x[0] = v.x, x[1] = v.y, y[0] = v.z, y[1] = v.w;
+                }
+              } else {
+                x[w] = *reinterpret_cast<const uint32_t*>(from + 4 * w);
+                y[w] = *reinterpret_cast<const uint32_t*>(from + C::SB + 4 * w);
+              }
+              const uint32_t z = __byte_perm(x[w], y[w], vsel);
+              sc[i][2 * w] = e4m3x2_to_f16x2(z);
+              sc[i][2 * w + 1] = e4m3x2_to_f16x2(z >> 16);
             }
+          }
 #pragma unroll
           for (int u = 0; u < D / 32; u += 2) {
             uint32_t r[4];
             values_at(t, u, vb, r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              // the lane's word: dims 4 g .. 4 g + 3 of token 2 c in bytes 0, 1, of token 2 c + 1 in bytes 2, 3
-              uint32_t lo[2], hi[2];
-              e2m1_bytes(r[2 * i], lo[0], hi[0]);
-              e2m1_bytes(r[2 * i + 1], lo[1], hi[1]);
-              const uint32_t y[4] = {f16_of_bytes<0, 2>(lo[0]), f16_of_bytes<1, 3>(lo[0]), f16_of_bytes<0, 2>(hi[0]),
-                                     f16_of_bytes<1, 3>(hi[0])};  // dims 4 g + 0, 2, 1, 3
-              const uint32_t z[4] = {f16_of_bytes<0, 2>(lo[1]), f16_of_bytes<1, 3>(lo[1]), f16_of_bytes<0, 2>(hi[1]),
-                                     f16_of_bytes<1, 3>(hi[1])};
+              // the lane's word: dims 4 g .. 4 g + 3 of token 2 c, then of token 2 c + 1
+              uint32_t y[4], z[4];
+              e2m1x8_to_f16x2(r[2 * i], y);
+              e2m1x8_to_f16x2(r[2 * i + 1], z);
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
-                const uint32_t a0 = hmul2(y[n], sc[0][u + i]), a1 = hmul2(y[n + 2], sc[0][u + i]),
-                               a2 = hmul2(z[n], sc[1][u + i]), a3 = hmul2(z[n + 2], sc[1][u + i]);
+                const uint32_t a0 = hmul2(__byte_perm(y[n], y[n + 2], 0x5410), sc[0][u + i]),
+                               a1 = hmul2(__byte_perm(y[n], y[n + 2], 0x7632), sc[0][u + i]),
+                               a2 = hmul2(__byte_perm(z[n], z[n + 2], 0x5410), sc[1][u + i]),
+                               a3 = hmul2(__byte_perm(z[n], z[n + 2], 0x7632), sc[1][u + i]);
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
                   mma16<false>(o[2 * (u + i) + n][x], a0, a1, a2, a3, pb[t][x][0], pb[t][x][1]);
