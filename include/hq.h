@@ -343,7 +343,7 @@ typedef struct {
   int32_t page_size; /* tokens per page, a multiple of 16, at most 1024 */
   int32_t num_heads; /* key-value heads, 1 .. 1024 */
   int32_t head_dim;  /* 64, 128 or 256 */
-  int64_t num_pages; /* pages of each pool, 1 .. 2^31 - 1 */
+  int64_t num_pages; /* pages of each pool, >= 1; num_pages * num_heads * page_size / 16 below 2^31 */
 } hq_kv_format_t;
 
 /* The pools (device pointers, 16-byte aligned).  k, v: [num_pages][num_heads][page_size] rows of 2 * head_dim (BF16),

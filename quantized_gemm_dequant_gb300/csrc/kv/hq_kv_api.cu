@@ -24,7 +24,9 @@ hq_status_t check_format(const hq_kv_format_t* f) {
   if (f->page_size < 1 || f->page_size > 1024 || f->num_heads < 1 || f->num_heads > kMaxHeads || f->num_pages < 1 ||
       f->num_pages > INT32_MAX)
     return HQ_ERR_INVALID_ARG;
-  return f->page_size % KV_BLOCK ? HQ_ERR_ALIGNMENT : HQ_OK;
+  if (f->page_size % KV_BLOCK) return HQ_ERR_ALIGNMENT;
+  // the kernels count a pool's 16-token blocks in 31 bits: more than any device holds
+  return f->num_pages * f->num_heads * (f->page_size / KV_BLOCK) > INT32_MAX ? HQ_ERR_INVALID_ARG : HQ_OK;
 }
 
 hq_status_t check_q_heads(const hq_kv_format_t* f, int32_t num_q_heads) {

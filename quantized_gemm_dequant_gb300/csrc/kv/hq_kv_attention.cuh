@@ -203,6 +203,11 @@ struct KaShares {
   }
 };
 
+template <bool V>
+struct KaFlag {
+  static constexpr bool value = V;
+};
+
 // One sequence's place in the list of units.
 struct KaSeq {
   int n, j0, t0;   // tokens, the first that is seen, and that one's block
@@ -432,13 +437,13 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   // ---- the ring's front: this warp's chunks of the share, keys and values alternating
   KaWalk<TB, C::EXTRA> ahead = at;
   int next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to();
-  int64_t row = -1;     // lane i: the first row of the warp's i-th block from the last look at the table
+  int place = -1;       // lane i: the place in the pools (in blocks) of the warp's i-th block from the last look at the table
   int used = 32;        // blocks of it that are used up
   bool more = true;     // false: all of the share has been asked for
   int put = 0, get = 0;
   bool values = false;  // the side that is next (one side a step)
   uint32_t word = 0;    // tokens of the chunk that are seen
-  int64_t base[TB];     // its blocks' first rows
+  int base[TB];         // its blocks' places
   auto next_chunk = [&]() {
     while (next_tok >= next_end) {  // the share's next pair
       ahead.next(a, hrs);
@@ -448,12 +453,12 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     }
     if (used == 32) {
       const int64_t tok = (int64_t)next_tok + STRIDE * (lane / TB) + 16 * (lane % TB);
-      row = -1;
+      place = -1;
       if (tok < next_end) {
         const int col = (int)((uint32_t)tok / (uint32_t)a.kv.page_size);
         const int64_t page = a.page_table[(int64_t)ahead.b * a.table_stride + col];
         if (page >= 0 && page < a.kv.num_pages)
-          row = (page * H + ahead.hr / tiles) * a.kv.page_size + ((int)tok - col * a.kv.page_size);
+          place = (int)(((page * H + ahead.hr / tiles) * a.kv.page_size + ((int)tok - col * a.kv.page_size)) / KV_BLOCK);
         else
           kv_report(a.status);
       }
@@ -465,29 +470,38 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     if (last < 16 * TB) word &= FULL >> (16 * TB - last);
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
-      base[i] = __shfl_sync(0xffffffffu, row, used + i);
+      base[i] = __shfl_sync(0xffffffffu, place, used + i);
       if (base[i] < 0) word &= ~(0xFFFFu << (16 * i)), base[i] = 0;
     }
     used += TB;
     next_tok += STRIDE;
   };
-  auto copy_side = [&](const uint8_t* pool, const uint8_t* scale_pool, uint32_t to) {
+  // one side of the chunk; rows that are not seen are zero: whatever they hold meets a weight of zero, and may be NaN
+  auto copy_side = [&](const uint8_t* pool, const uint8_t* scale_pool, uint32_t to, auto whole) {
+    constexpr bool all = decltype(whole)::value;
 #pragma unroll
-    for (int t = 0; t < TB; ++t, to += C::BLOCK) {
-      const uint8_t *codes = pool + base[t] * C::RB + lane * 16, *scales = scale_pool + base[t] * C::SB + lane * 16;
-      if (word == FULL) {
+    for (int t = 0; t < TB; ++t) {
+      const uint8_t* codes = pool + (uint64_t)(uint32_t)base[t] * (16 * C::RB) + lane * 16;
+      const uint32_t w = word >> (16 * t);
 #pragma unroll
-        for (int i = 0; i < C::RB / 32; ++i)
-          copy16(to + C::at((lane + 32 * i) / C::UPR, (lane + 32 * i) % C::UPR), codes + 512 * i);
-        if (C::SB > 0 && lane < C::SB) copy16(to + 16 * C::RB + 16 * lane, scales);
-      } else {  // rows that are not seen are zero: whatever they hold meets a weight of zero, and may be NaN
-        const uint32_t w = word >> (16 * t);
+      for (int i = 0; i < C::RB / 32; ++i) {
+        const int r = (lane + 32 * i) / C::UPR;
+        const uint32_t at = to + t * C::BLOCK + C::at(r, (lane + 32 * i) % C::UPR);
+        if constexpr (all) copy16(at, codes + 512 * i);
+        else copy16_or_zero(at, codes + 512 * i, (w >> r) & 1u ? 16u : 0u);
+      }
+    }
+    if constexpr (C::SB > 0) {  // SB lanes a block
+      constexpr int ONCE = TB * C::SB <= 32 ? TB : 1;
 #pragma unroll
-        for (int i = 0; i < C::RB / 32; ++i) {
-          const int r = (lane + 32 * i) / C::UPR;
-          copy16_or_zero(to + C::at(r, (lane + 32 * i) % C::UPR), codes + 512 * i, (w >> r) & 1u ? 16u : 0u);
+      for (int t = 0; t < TB; t += ONCE) {
+        if (lane < ONCE * C::SB) {
+          const int k = ONCE > 1 && lane >= C::SB ? 1 : 0, l = lane - k * C::SB;
+          const uint8_t* scales = scale_pool + (uint64_t)(uint32_t)(k ? base[TB - 1] : base[t]) * (16 * C::SB) + 16 * l;
+          const uint32_t at = to + (t + k) * C::BLOCK + 16 * C::RB + 16 * l;
+          if constexpr (all) copy16(at, scales);
+          else copy16_or_zero(at, scales, (word >> (16 * (t + k))) & 0xFFFFu ? 16u : 0u);
         }
-        if (C::SB > 0 && lane < C::SB) copy16_or_zero(to + 16 * C::RB + 16 * lane, scales, w & 0xFFFFu ? 16u : 0u);
       }
     }
   };
@@ -495,12 +509,16 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     if ((C::PAIR || !values) && more) next_chunk();
     if (more) {
       const uint32_t to = ring_at + put * C::STEP;
-      if constexpr (C::PAIR) {
-        copy_side(a.kv.k, a.kv.k_scale, to);
-        copy_side(a.kv.v, a.kv.v_scale, to + C::SIDE);
-      } else {
-        copy_side(values ? a.kv.v : a.kv.k, nullptr, to);
-      }
+      auto copy = [&](auto whole) {
+        if constexpr (C::PAIR) {
+          copy_side(a.kv.k, a.kv.k_scale, to, whole);
+          copy_side(a.kv.v, a.kv.v_scale, to + C::SIDE, whole);
+        } else {
+          copy_side(values ? a.kv.v : a.kv.k, nullptr, to, whole);
+        }
+      };
+      if (word == FULL) copy(KaFlag<true>());
+      else copy(KaFlag<false>());
       if (lane == 0) masks[put] = word;
     }
     cp_async_commit();

@@ -23,7 +23,7 @@ def test_formats_are_checked():
     assert size() >= 4
     for over in (dict(kind=0), dict(kind=4), dict(head_dim=96), dict(head_dim=0), dict(page_size=0), dict(page_size=24),
                  dict(page_size=2048), dict(num_heads=0), dict(num_heads=2000), dict(num_pages=0),
-                 dict(num_pages=1 << 31)):
+                 dict(num_pages=1 << 31), dict(num_pages=1 << 27, num_heads=16)):
         assert size(**over) == 0, over
     f = ctypes.byref(_fmt(hq))
     assert L.hq_kv_workspace_bytes(f, -1, 8) == 0 and L.hq_kv_workspace_bytes(f, 4, 3) == 0
