@@ -73,11 +73,11 @@ struct KaCfg {
   static constexpr int TB = ka_blocks(KIND, D);      // 16-token blocks of one chunk
   static constexpr int BLOCK = 16 * (RB + SB);       // a block's codes, then its scales
   static constexpr int SIDE = TB * BLOCK;            // a chunk's keys, or its values
-  // A ring step is a chunk's keys and values, so that the decoding of the values fills the waits of the scores; of bf16,
-  // which has nothing to decode and twice the bytes, it is one side.
+  // A ring step is a chunk's keys and values, one wait and one look at the table for both; of bf16, which has twice the
+  // bytes, it is one side.
   static constexpr bool PAIR = KIND != HQ_KV_BF16;
   static constexpr int STEP = PAIR ? 2 * SIDE : SIDE;
-  static constexpr bool EARLY = PAIR && NT == 1 && D <= 128;  // values are read before the weights are known
+  static constexpr int SUMS = PAIR ? 1 : 2;  // of a score: every other 16 dims of bf16 apart, a shorter chain
   // Beginning and ending a pair costs a CTA about as long as streaming so many bytes (3 to 4 us): so many units of the
   // list are the pair's own.  Without them the CTAs with more pairs were up to a fifth later than the others (a batch
   // of 64 e4m3 sequences: 99 us, with them 94 to 96).
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     const int end = at.to();
 #pragma unroll 1
     for (int tok = at.from() + 16 * TB * warp; tok < end; tok += STRIDE) {
-      // ---- keys: s^T = K q^T, two sums of every other step (a shorter chain)
+      // ---- keys: s^T = K q^T
       cp_async_wait_group<C::DEPTH - 2>();
       __syncwarp();
       issue();
@@ -625,9 +625,9 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       for (int t = 0; t < TB; ++t) {
         const uint32_t kb = kslot + t * C::BLOCK;
         const uint8_t* kscale = kslot_p + t * C::BLOCK + 16 * C::RB;
-        float s2[2][NT][4];
+        float s2[C::SUMS][NT][4];
 #pragma unroll
-        for (int i = 0; i < 2 * NT * 4; ++i) (&s2[0][0][0])[i] = 0.0f;
+        for (int i = 0; i < C::SUMS * NT * 4; ++i) (&s2[0][0][0])[i] = 0.0f;
         if constexpr (BF) {
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
                 qfrag(k + i, x, f);
-                mma16<false>(s2[i][x], a0, a1, a2, a3, f[0], f[1]);
+                mma16<false>(s2[0][x], a0, a1, a2, a3, f[0], f[1]);
               }
             }
           }
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                   qfrag(2 * (u + i) + p, x, f);
-                  mma16<false>(s2[p][x], a0, a1, a2, a3, f[0], f[1]);
+                  mma16<false>(s2[0][x], a0, a1, a2, a3, f[0], f[1]);
                 }
               }
             }
@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            s[t][x][i] = (s2[0][x][i] + s2[1][x][i]) * (F8 ? qscale[x][i & 1] * ks[i >> 1] : qscale[x][i & 1]);
+            s[t][x][i] = (C::SUMS == 2 ? s2[0][x][i] + s2[C::SUMS - 1][x][i] : s2[0][x][i]) *
+                         (F8 ? qscale[x][i & 1] * ks[i >> 1] : qscale[x][i & 1]);
       }
       if (a.softcap > 0.0f) {  // cap * tanh(y) = cap * (1 - 2 / (1 + e^2y)); the scores hold 2 y log2 e
 #pragma unroll
@@ -736,14 +737,6 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         issue();
         vslot = ring_at + get * C::STEP;
         get = get + 1 == C::DEPTH ? 0 : get + 1;
-      }
-      constexpr int VL = C::EARLY ? D * (F8 ? 1 : 2) / (F8 ? 32 : 128) : 1;  // ldmatrix of a block's values
-      uint32_t early[TB][VL][4];
-      if constexpr (C::EARLY) {
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-          for (int u = 0; u < VL; ++u) ldsm_x4_t(vslot + t * C::BLOCK + C::at(lr, 2 * u + lu), early[t][u]);
       }
       float vl[TB][2];  // log2 of the value scales of tokens g and g + 8
 #pragma unroll
@@ -818,14 +811,6 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             pb[t][x][i] = turn8x8(BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]));
           }
       // ---- o^T += V^T p^T
-      auto values_at = [&](int t, int u, uint32_t vb, uint32_t (&r)[4]) {
-        if constexpr (C::EARLY) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = early[t][u / 2][i];
-        } else {
-          ldsm_x4_t(vb + C::at(lr, u + lu), r);
-        }
-      };
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         const uint32_t vb = vslot + t * C::BLOCK;
@@ -843,7 +828,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
           for (int u = 0; u < KS; u += 2) {
             uint32_t r[4];
-            values_at(t, u, vb, r);
+            ldsm_x4_t(vb + C::at(lr, u + lu), r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t y = __byte_perm(r[2 * i], 0, 0x3120), z = __byte_perm(r[2 * i + 1], 0, 0x3120);
@@ -880,7 +865,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
           for (int u = 0; u < D / 32; u += 2) {
             uint32_t r[4];
-            values_at(t, u, vb, r);
+            ldsm_x4_t(vb + C::at(lr, u + lu), r);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               // the lane's word: dims 4 g .. 4 g + 3 of token 2 c, then of token 2 c + 1
