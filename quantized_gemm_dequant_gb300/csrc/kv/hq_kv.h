@@ -86,12 +86,12 @@ struct KvAttnArgs {
 
 cudaError_t launch_kv_write(int kind, int dim, const KvWriteArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_read(int kind, int dim, const KvReadArgs& a, cudaStream_t stream);
-// sms: of the device; tokens: the most that one sequence sees; slots, counters: places in the workspace
-cudaError_t launch_kv_attention_bf16(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots,
-                                    int* counters, cudaStream_t stream);
-cudaError_t launch_kv_attention_e4m3(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots,
-                                    int* counters, cudaStream_t stream);
-cudaError_t launch_kv_attention_nvfp4(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots,
-                                    int* counters, cudaStream_t stream);
+// sms: of the device; tokens: the most that one sequence sees
+cudaError_t launch_kv_attention_bf16(int dim, const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* workspace,
+                                    cudaStream_t stream);
+cudaError_t launch_kv_attention_e4m3(int dim, const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* workspace,
+                                    cudaStream_t stream);
+cudaError_t launch_kv_attention_nvfp4(int dim, const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* workspace,
+                                    cudaStream_t stream);
 
 }  // namespace hq

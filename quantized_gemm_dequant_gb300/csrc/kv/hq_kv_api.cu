@@ -196,13 +196,11 @@ hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* c
   a.lse = x->lse;
   a.status = (int*)workspace;
   const int sms = num_sms();
-  float* slots = reinterpret_cast<float*>((uint8_t*)workspace + KV_HEADER_BYTES);
-  int* counters = reinterpret_cast<int*>((uint8_t*)workspace + ka_counters_at(sms));
   const int64_t seen = a.window > 0 && a.window < a.most ? a.window + KV_BLOCK : a.most;
   const auto launch = fmt->kind == HQ_KV_BF16 ? launch_kv_attention_bf16
                                               : (fmt->kind == HQ_KV_E4M3 ? launch_kv_attention_e4m3
                                                                          : launch_kv_attention_nvfp4);
-  return launched(launch(fmt->head_dim, a, sms, seen, slots, counters, (cudaStream_t)stream));
+  return launched(launch(fmt->head_dim, a, sms, seen, (uint8_t*)workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -48,6 +48,8 @@ constexpr int KA_THREADS = 32 * KA_WARPS;
 constexpr int KA_ROWS = 16;          // query heads of one row tile, at most
 constexpr float KA_LAZY = 8.0f;      // the running maximum lags by at most this (log2)
 constexpr int KA_FEW = 6;            // parts of a pair that are joined without the CTA's help
+constexpr int KA_GROUP = 16;         // CTAs whose parts of a pair with many are joined first, to one part
+constexpr int KA_MANY = 24;          // parts from more than which that is done
 constexpr float KA_NONE = -3.0e38f;  // the running maximum of no token
 
 // 16-token blocks per unit of the list, resident CTAs per SM.
@@ -59,12 +61,16 @@ __host__ __device__ constexpr int ka_ctas(int kind, int dim, int nt) {
 }
 
 // Workspace of a call, for the host (sizes) and the device: the status, then two slots per CTA for the parts of split
-// pairs, then a counter per (sequence, head, row tile).  The slots' room is that of the largest format, so that the
-// counters, which have to be zero between calls, are at one place whatever the calls' shapes are.
+// pairs, then two counters per KA_GROUP CTAs, then one per (sequence, head, row tile).  The slots' room is that of the
+// largest format, so that the counters, which have to be zero between calls, are at one place whatever the calls' shapes
+// are.
 constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 2);  // o, then (m, l) of each row, of 16 heads of 256 dims
 constexpr int KA_MOST_CTAS = 2;                         // per SM, of that size
-constexpr size_t ka_counters_at(int sms) {
+constexpr size_t ka_group_counters_at(int sms) {
   return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
+}
+constexpr size_t ka_counters_at(int sms) {  // (at most four CTAs per SM)
+  return ka_group_counters_at(sms) + 2 * (4 * (size_t)sms / KA_GROUP + 1) * sizeof(int);
 }
 
 template <int KIND, int D, int NT>
@@ -266,15 +272,15 @@ __device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, 
   if (d == 0 && a.lse) a.lse[q] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins the parts of a split pair, first to last, and stores its rows: parts k > 0 are at `others`, two slots apart.  A
-// function of its own, so that its registers are not the main loop's.
+// Joins `parts` parts of a split pair in order: slot `first`, then slots others + k apart.  The result goes to the
+// pair's rows, or, as one part, to slot `first` again. 
 template <int KIND, int D, int NT>
-__device__ __noinline__ void ka_join(const KvAttnArgs& a, const float* first, const float* others, int parts, int64_t q0,
-                                     int rows, float vg, float* merge, float* mls) {
+__device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint32_t first, uint32_t others, uint32_t apart,
+                                     int parts, bool to_part, int64_t q0, int rows, float vg, float* merge, float* mls) {
   using C = KaCfg<KIND, D, NT>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto part_at = [&](int k) { return k ? others + 2 * (int64_t)k * C::PART : first; };
-  if (parts <= KA_FEW) {  // every thread on its own, all loads at once
+  auto part_at = [&](int k) { return slots + (k ? others + k * apart : first) * C::PART; };
+  if (parts <= KA_FEW && !to_part) {  // every thread on its own, all loads at once
 #pragma unroll 1
     for (int e = threadIdx.x; e < rows * (D / 4); e += KA_THREADS) {
       const int r = e / (D / 4), d = 4 * (e % (D / 4));
@@ -350,14 +356,54 @@ __device__ __noinline__ void ka_join(const KvAttnArgs& a, const float* first, co
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
     const int e = threadIdx.x + i * KA_THREADS, r = e / (D / 4), d = 4 * (e % (D / 4));
-    if (r < rows) ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
+    if (r >= rows) continue;
+    if (!to_part) {
+      ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
+    } else {  // (all parts have been read)
+      __stcg(reinterpret_cast<float4*>(part_at(0) + r * D + d), y[i]);
+      if (d == 0) __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(tops[2 * r], tops[2 * r + 1]));
+    }
   }
   __syncthreads();  // the next pair's join writes where this one's was read
 }
 
+// A split pair whose part this CTA has written: the last CTA to arrive joins the parts, first to last; of many, the last
+// of every KA_GROUP CTAs joins theirs first.  The pair's units are seg0 .. end - 1 of the list.  A function of its own,
+// so that its registers are not the main loop's.
+template <int KIND, int D, int NT>
+__device__ __noinline__ void ka_split(const KvAttnArgs& a, const KaShares sh, uint32_t seg0, uint32_t end, int64_t pair,
+                                      float* slots, int* groups, int* counters, int* last_one, int64_t q0, int rows,
+                                      float vg, float* merge, float* mls) {
+  const uint32_t c0 = sh.owner(seg0 + KaCfg<KIND, D, NT>::EXTRA), c1 = sh.owner(end - 1);
+  const uint32_t s0 = 2 * c0 + (sh.first(c0) >= seg0 ? 0 : 1);  // the first part's slot; others' first pair is this
+  auto last_of = [&](int* counter, uint32_t n) {  // whether this CTA is; its part is written
+    __syncthreads();  // the counter's release and acquire order it and the others' parts
+    if (threadIdx.x == 0) {
+      *last_one = count_up(counter) == (int)(n - 1);
+      if (*last_one) *counter = 0;
+    }
+    __syncthreads();
+    return *last_one != 0;
+  };
+  uint32_t parts = c1 - c0 + 1, others = 2 * c0, apart = 2;
+  if (parts > KA_MANY) {
+    const uint32_t gr = blockIdx.x / KA_GROUP, from = c0 > gr * KA_GROUP ? c0 : gr * KA_GROUP;
+    const uint32_t n = (c1 < gr * KA_GROUP + KA_GROUP - 1 ? c1 : gr * KA_GROUP + KA_GROUP - 1) - from + 1;
+    if (n > 1) {  // two counters: a pair that comes from the group before, one that begins in this group and leaves it
+      if (!last_of(groups + 2 * gr + (c0 < gr * KA_GROUP ? 0 : 1), n)) return;
+      ka_join<KIND, D, NT>(a, slots, from == c0 ? s0 : 2 * from, 2 * from, 2, n, true, q0, rows, vg, merge, mls);
+    }
+    parts = c1 / KA_GROUP - c0 / KA_GROUP + 1;
+    others = 2 * (c0 / KA_GROUP * KA_GROUP);
+    apart = 2 * KA_GROUP;
+  }
+  if (last_of(counters + pair, parts))
+    ka_join<KIND, D, NT>(a, slots, s0, others, apart, parts, false, q0, rows, vg, merge, mls);
+}
+
 template <int KIND, int D, int NT>
 __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
-    kv_attention_kernel(const KvAttnArgs a, float* slots, int* counters) {
+    kv_attention_kernel(const KvAttnArgs a, float* slots, int* groups, int* counters) {
   using C = KaCfg<KIND, D, NT>;
   constexpr bool BF = KIND == HQ_KV_BF16, F8 = KIND == HQ_KV_E4M3;
   constexpr int KS = D / 16, TB = C::TB, STRIDE = 16 * TB * KA_WARPS;
@@ -946,23 +992,14 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     }
     if (whole) continue;
 
-    // ---- split pair: the last CTA to arrive joins the parts, first to last
-    const uint32_t c0 = sh.owner(at.seg0 + C::EXTRA), c1 = sh.owner(at.seg0 + at.s.units - 1);
-    const int64_t pair = (int64_t)at.b * hrs + at.hr;
-    __syncthreads();  // the CTA's part is written; the counter's release and acquire order it and the others' parts
-    if (threadIdx.x == 0) *last_one = count_up(counters + pair) == (int)(c1 - c0);
-    __syncthreads();
-    if (!*last_one) continue;
-    const int parts = (int)(c1 - c0) + 1;
-    const int64_t s0 = 2 * (int64_t)c0 + (sh.first(c0) >= at.seg0 ? 0 : 1);  // the others' first pair is this one
-    ka_join<KIND, D, NT>(a, slots + s0 * C::PART, slots + 2 * (int64_t)c0 * C::PART, parts, q0, rows, vg, merge, mls);
-    if (threadIdx.x == 0) counters[pair] = 0;
+    ka_split<KIND, D, NT>(a, sh, at.seg0, at.seg0 + at.s.units, (int64_t)at.b * hrs + at.hr, slots, groups, counters,
+                          last_one, q0, rows, vg, merge, mls);
   }
   cp_async_wait_all();
 }
 
 template <int KIND, int D, int NT>
-cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, float* slots, int* counters, cudaStream_t stream) {
+cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* workspace, cudaStream_t stream) {
   using C = KaCfg<KIND, D, NT>;
   static std::atomic<uint64_t> allowed{0};  // devices on which the kernel has its shared memory (a bit each)
   int dev = 0;
@@ -978,19 +1015,21 @@ cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, float* slots
   const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
   const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4), all = (int64_t)C::CTAS * sms;
   return launch_kernel(kv_attention_kernel<KIND, D, NT>, dim3((unsigned)(want < all ? want : all)), dim3(KA_THREADS),
-                       C::SMEM, stream, a, slots, counters);
+                       C::SMEM, stream, a, reinterpret_cast<float*>(workspace + KV_HEADER_BYTES),
+                       reinterpret_cast<int*>(workspace + ka_group_counters_at(sms)),
+                       reinterpret_cast<int*>(workspace + ka_counters_at(sms)));
 }
 
 template <int KIND>
-cudaError_t launch_ka_dim(int dim, const KvAttnArgs& a, int sms, int64_t tokens, float* slots, int* counters,
+cudaError_t launch_ka_dim(int dim, const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* workspace,
                           cudaStream_t stream) {
   if (a.group <= 8)
-    return dim == 64 ? launch_ka<KIND, 64, 1>(a, sms, tokens, slots, counters, stream)
-                     : (dim == 128 ? launch_ka<KIND, 128, 1>(a, sms, tokens, slots, counters, stream)
-                                   : launch_ka<KIND, 256, 1>(a, sms, tokens, slots, counters, stream));
-  return dim == 64 ? launch_ka<KIND, 64, 2>(a, sms, tokens, slots, counters, stream)
-                   : (dim == 128 ? launch_ka<KIND, 128, 2>(a, sms, tokens, slots, counters, stream)
-                                 : launch_ka<KIND, 256, 2>(a, sms, tokens, slots, counters, stream));
+    return dim == 64 ? launch_ka<KIND, 64, 1>(a, sms, tokens, workspace, stream)
+                     : (dim == 128 ? launch_ka<KIND, 128, 1>(a, sms, tokens, workspace, stream)
+                                   : launch_ka<KIND, 256, 1>(a, sms, tokens, workspace, stream));
+  return dim == 64 ? launch_ka<KIND, 64, 2>(a, sms, tokens, workspace, stream)
+                   : (dim == 128 ? launch_ka<KIND, 128, 2>(a, sms, tokens, workspace, stream)
+                                 : launch_ka<KIND, 256, 2>(a, sms, tokens, workspace, stream));
 }
 
 #endif  // __CUDACC__

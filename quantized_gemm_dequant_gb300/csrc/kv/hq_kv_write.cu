@@ -144,7 +144,10 @@ struct Token {
   int64_t pos;
 };
 
-template <int KIND, int D, int MODE>
+// MORE: a warp has at least two query steps beyond those that its registers hold; they are loaded as many at a time (56
+// heads of 256 dims: 243 us one by one, 194 so).  With one beyond them it is loaded on its own: the batch's registers
+// cost 32 heads of 128 dims 38.4 us -> 40.2.
+template <int KIND, int D, int MODE, bool MORE>
 __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteArgs a) {
   constexpr int LPH = D / 8;     // lanes of a head's row
   constexpr int HPW = 32 / LPH;  // heads of one step
@@ -213,7 +216,20 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
       norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
       if (h0 + s * NEXT < Hq) store_row(out + s * NEXT * D, lo, hi, f);
     }
-    for (int h = h0 + KW_STEPS * NEXT; h - sub < Hq; h += NEXT) {
+    for (int h = h0 + KW_STEPS * NEXT; MORE && h - sub < Hq; h += KW_STEPS * NEXT) {
+      const uint16_t* row = a.qkv + t * a.row_stride + (int64_t)h * D;
+#pragma unroll
+      for (int s = 0; s < KW_STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, h + s * NEXT < Hq);
+#pragma unroll
+      for (int s = 0; s < KW_STEPS; ++s) {
+        float f[8];
+        unpack_row(x.q[s], f);
+        norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
+        if (h + s * NEXT < Hq) store_row(out + (int64_t)(h - h0 + s * NEXT) * D, lo, hi, f);
+      }
+    }
+
+    for (int h = h0 + KW_STEPS * NEXT; !MORE && h - sub < Hq; h += NEXT) {
       float f[8];
       unpack_row(load_row(a.qkv + t * a.row_stride + (int64_t)h * D, lo, hi, h < Hq), f);
       norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
@@ -272,8 +288,8 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
   }
 }
 
-template <int KIND, int D, int MODE>
-cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
+template <int KIND, int D, int MODE, bool MORE>
+cudaError_t launch_more(const KvWriteArgs& a, cudaStream_t stream) {
   static std::atomic<int> resident{0};  // CTAs that the device holds at once
   int n = resident.load(std::memory_order_relaxed);
   if (n == 0) {
@@ -281,13 +297,19 @@ cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_write_kernel<KIND, D, MODE>, KW_THREADS, 0);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_write_kernel<KIND, D, MODE, MORE>, KW_THREADS, 0);
     if (e != cudaSuccess) return e;
     n = (per > 0 ? per : 1) * (sms > 0 ? sms : 1);
     resident.store(n, std::memory_order_relaxed);
   }
-  return launch_kernel(kv_write_kernel<KIND, D, MODE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
+  return launch_kernel(kv_write_kernel<KIND, D, MODE, MORE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
                        a);
+}
+
+template <int KIND, int D, int MODE>
+cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
+  return a.q_heads > (KW_STEPS + 1) * (KW_THREADS / 32) * (256 / D) ? launch_more<KIND, D, MODE, true>(a, stream)
+                                                              : launch_more<KIND, D, MODE, false>(a, stream);
 }
 
 template <int KIND, int D>

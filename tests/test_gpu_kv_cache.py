@@ -122,6 +122,26 @@ def test_write(lib, kind, D, R, interleaved, norm, T, heads, group):
         assert not rest.any()
 
 
+@pytest.mark.parametrize("D,heads,group", [(256, 2, 9), (256, 5, 8), (128, 4, 10), (64, 16, 9)])
+def test_write_many_heads(lib, D, heads, group):
+    """More query heads than a CTA keeps in registers (one step over, and many), more key heads than one step."""
+    T, Hq, page, pages = 5, heads * group, 16, 2
+    c = lib.make_kv_cache("e4m3", pages, page, heads, D)
+    x, slots, pos = _rows(1, T, Hq, heads, D), torch.arange(T), torch.arange(T, dtype=torch.int32) * 7
+    w, cs = _weight(4, D), _angles(50, D)
+    q = _call(lib, c, x.cuda(), slots, Hq, q_norm=w, k_norm=w, positions=pos, cos_sin=cs)
+    h = x.view(T, -1, D)
+    for got, part in ((K.f64(q), h[:, :Hq]), (None, h[:, Hq:Hq + heads])):
+        want = K.norm_rotate(part, w, 1e-6, cs, pos, False)
+        mag = _magnitude(part, w, 1e-6, D, False)
+        if got is not None:
+            assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + F32 * mag + 1e-37)
+        else:
+            _check_held(c, "k", slots, want, mag)
+    v = K.f64(h[:, Hq + heads:])
+    _check_held(c, "v", slots, v, np.abs(v))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_codes_are_the_oracles(lib, D):
     """No norm, no rotation: codes and scales bit for bit those of the oracle's quantisers, keys and values alike."""

@@ -85,9 +85,11 @@ def test_scales(lib, kind, scale, gain):
 
 @pytest.mark.parametrize("kind", K.KINDS)
 @pytest.mark.parametrize("lens,heads,group", [([20011], 1, 8), ([9000, 1, 0, 4097, 2], 2, 3),
-                                              ([700] * 40, 4, 2), (list(range(200)), 1, 4)])
+                                              ([700] * 40, 4, 2), (list(range(200)), 1, 4),
+                                              ([30000, 1, 25003], 1, 2), ([60001], 1, 9), ([3, 9000, 12000, 8000], 1, 1)])
 def test_long_and_many(lib, kind, lens, heads, group):
-    """Lengths split over many CTAs, and many sequences in one CTA's share."""
+    """Lengths split over many CTAs (a few parts, and so many that they are joined in groups first), and many sequences
+    in one CTA's share."""
     _check(*_case(lib, kind, 128, heads, group, 16, lens))
 
 
