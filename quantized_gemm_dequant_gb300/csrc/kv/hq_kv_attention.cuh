@@ -47,9 +47,9 @@ constexpr int KA_WARPS = 4;
 constexpr int KA_THREADS = 32 * KA_WARPS;
 constexpr int KA_ROWS = 16;          // query heads of one row tile, at most
 constexpr float KA_LAZY = 8.0f;      // the running maximum lags by at most this (log2)
-constexpr int KA_FEW = 6;            // parts of a pair that are joined without the CTA's help
 constexpr int KA_GROUP = 16;         // CTAs whose parts of a pair with many are joined first, to one part
 constexpr int KA_MANY = 24;          // parts from more than which that is done
+constexpr int KA_MOST = 32 * KA_GROUP;  // CTAs, so that a join has 32 parts at most
 constexpr float KA_NONE = -3.0e38f;  // the running maximum of no token
 
 // 16-token blocks per unit of the list, resident CTAs per SM.
@@ -69,8 +69,8 @@ constexpr int KA_MOST_CTAS = 2;                         // per SM, of that size
 constexpr size_t ka_group_counters_at(int sms) {
   return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
 }
-constexpr size_t ka_counters_at(int sms) {  // (at most four CTAs per SM)
-  return ka_group_counters_at(sms) + 2 * (4 * (size_t)sms / KA_GROUP + 1) * sizeof(int);
+constexpr size_t ka_counters_at(int sms) {
+  return ka_group_counters_at(sms) + 2 * (KA_MOST / KA_GROUP) * sizeof(int);
 }
 
 template <int KIND, int D, int NT>
@@ -272,95 +272,77 @@ __device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, 
   if (d == 0 && a.lse) a.lse[q] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins `parts` parts of a split pair in order: slot `first`, then slots others + k apart.  The result goes to the
-// pair's rows, or, as one part, to slot `first` again. 
+// Joins at most 32 parts of a split pair in order: slot `first`, then slots others + k apart.  The result goes to the
+// pair's rows, or, as one part, to slot `first` again.  Bound by latency: a thread's 16 to 32 loads of o are in flight
+// while a warp per head finds the factors 2^(m - top), a part per lane.
 template <int KIND, int D, int NT>
-__device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint32_t first, uint32_t others, uint32_t apart,
-                                     int parts, bool to_part, int64_t q0, int rows, float vg, float* merge, float* mls) {
+__device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint32_t first, uint32_t others,
+                                        uint32_t apart, int parts, bool to_part, int64_t q0, int rows, float vg,
+                                        float* merge, float* mls) {
   using C = KaCfg<KIND, D, NT>;
+  constexpr int MINE = 8 * NT * (D / 4) / KA_THREADS, AHEAD = MINE >= 4 ? 4 : 16 / MINE, HEADS = 8 * NT / KA_WARPS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto part_at = [&](int k) { return slots + (k ? others + k * apart : first) * C::PART; };
-  if (parts <= KA_FEW && !to_part) {  // every thread on its own, all loads at once
-#pragma unroll 1
-    for (int e = threadIdx.x; e < rows * (D / 4); e += KA_THREADS) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      float2 ml[KA_FEW];
-      float4 v[KA_FEW];
-      float top = KA_NONE, sum = 0.0f;
+  float* factor = merge;  // [head][32]
+  float* tops = mls;      // [head][2]: top, sum
+  float4 v[AHEAD][MINE], y[MINE];
+  auto take = [&](int k0) {
 #pragma unroll
-      for (int k = 0; k < KA_FEW; ++k) {
-        if (k >= parts) break;
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(part_at(k) + 8 * NT * D + 2 * r));
-        v[k] = __ldcg(reinterpret_cast<const float4*>(part_at(k) + r * D + d));
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int e = 4 * (threadIdx.x + i * KA_THREADS);
+        v[k][i] = k0 + k < parts && e < rows * D ? __ldcg(reinterpret_cast<const float4*>(part_at(k0 + k) + e))
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+  };
+  take(0);
+  float2 ml[HEADS];
 #pragma unroll
-      for (int k = 0; k < KA_FEW; ++k)
-        if (k < parts) top = fmaxf(top, ml[k].x);
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < KA_FEW; ++k)
-        if (k < parts) {
-          const float f = ex2(ml[k].x - top);
-          sum = fmaf(f, ml[k].y, sum);
-          y.x = fmaf(f, v[k].x, y.x), y.y = fmaf(f, v[k].y, y.y);
-          y.z = fmaf(f, v[k].z, y.z), y.w = fmaf(f, v[k].w, y.w);
-        }
-      ka_store(a, q0 + r, D, d, y, top, sum, vg);
-    }
-    return;
+  for (int i = 0; i < HEADS; ++i) {
+    const int r = warp + i * KA_WARPS;
+    ml[i] = lane < parts && r < rows ? __ldcg(reinterpret_cast<const float2*>(part_at(lane) + 8 * NT * D + 2 * r))
+                                     : make_float2(KA_NONE, 0.0f);
   }
-  // a batch's factors 2^(m - top) and l are found by a warp per head, then every thread sums its dims of all parts
-  constexpr int BATCH = 64, MINE = 8 * NT * (D / 4) / KA_THREADS;
-  float* factor = merge;  // [heads][BATCH]
-  float* tops = mls;      // [heads][2]: top, sum
-  float4 y[MINE];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int r = warp + i * KA_WARPS;
+    float top = ml[i].x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = ex2(ml[i].x - top);
+    float sum = f * ml[i].y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    factor[r * 32 + lane] = f;
+    if (lane == 0) tops[2 * r] = top, tops[2 * r + 1] = sum;
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < MINE; ++i) y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int r = warp; r < rows; r += KA_WARPS) {
-    float top = KA_NONE;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(part_at(k) + 8 * NT * D + 2 * r));
+#pragma unroll 1
+  for (int k0 = 0;;) {
 #pragma unroll
-    for (int i = 1; i < 32; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if (lane == 0) tops[2 * r] = top, tops[2 * r + 1] = 0.0f;
-  }
-  for (int k0 = 0; k0 < parts; k0 += BATCH) {
-    const int n = parts - k0 < BATCH ? parts - k0 : BATCH;
-    __syncwarp();
-    for (int r = warp; r < rows; r += KA_WARPS) {
-      float sum = 0.0f;
-      for (int k = lane; k < n; k += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_at(k0 + k) + 8 * NT * D + 2 * r));
-        const float f = ex2(ml.x - tops[2 * r]);
-        factor[r * BATCH + k] = f;
-        sum = fmaf(f, ml.y, sum);
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int r = 4 * (threadIdx.x + i * KA_THREADS) / D;
+        const float f = k0 + k < parts ? factor[r * 32 + k0 + k] : 0.0f;
+        y[i].x = fmaf(f, v[k][i].x, y[i].x), y[i].y = fmaf(f, v[k][i].y, y[i].y);
+        y[i].z = fmaf(f, v[k][i].z, y[i].z), y[i].w = fmaf(f, v[k][i].w, y[i].w);
       }
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-      if (lane == 0) tops[2 * r + 1] += sum;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-      const int e = threadIdx.x + i * KA_THREADS, r = e / (D / 4), d = 4 * (e % (D / 4));
-      if (r >= rows) break;
-#pragma unroll 16
-      for (int k = 0; k < n; ++k) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(k0 + k) + r * D + d));
-        const float f = factor[r * BATCH + k];
-        y[i].x = fmaf(f, v.x, y[i].x), y[i].y = fmaf(f, v.y, y[i].y);
-        y[i].z = fmaf(f, v.z, y[i].z), y[i].w = fmaf(f, v.w, y[i].w);
-      }
-    }
-    __syncthreads();
+    k0 += AHEAD;
+    if (k0 >= parts) break;
+    take(k0);
   }
 #pragma unroll
   for (int i = 0; i < MINE; ++i) {
-    const int e = threadIdx.x + i * KA_THREADS, r = e / (D / 4), d = 4 * (e % (D / 4));
+    const int e = 4 * (threadIdx.x + i * KA_THREADS), r = e / D, d = e % D;
     if (r >= rows) continue;
     if (!to_part) {
       ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
-    } else {  // (all parts have been read)
-      __stcg(reinterpret_cast<float4*>(part_at(0) + r * D + d), y[i]);
+    } else {  // (all (m, l) have been read, and o's dims are this thread's alone)
+      __stcg(reinterpret_cast<float4*>(part_at(0) + e), y[i]);
       if (d == 0) __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(tops[2 * r], tops[2 * r + 1]));
     }
   }
@@ -1013,7 +995,7 @@ cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* wor
   // no more CTAs than the longest lengths make shares
   const int64_t per = (tokens + 16 * C::TB - 1) / (16 * C::TB);
   const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
-  const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4), all = (int64_t)C::CTAS * sms;
+  const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4), all = C::CTAS * sms < KA_MOST ? C::CTAS * sms : KA_MOST;
   return launch_kernel(kv_attention_kernel<KIND, D, NT>, dim3((unsigned)(want < all ? want : all)), dim3(KA_THREADS),
                        C::SMEM, stream, a, reinterpret_cast<float*>(workspace + KV_HEADER_BYTES),
                        reinterpret_cast<int*>(workspace + ka_group_counters_at(sms)),
