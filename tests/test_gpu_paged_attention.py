@@ -70,6 +70,21 @@ def test_window(lib, kind, window):
     _check(*_case(lib, kind, 64, 2, 4, 16, LENS, window=window), f"window {window}")
 
 
+def test_pages_before_the_window_may_be_gone(lib):
+    """A server frees a page once the window has left it: its table entry is not read."""
+    lens, page, window = [300, 100, 17], 16, 40
+    table, pages = K.tables(lens, page)
+    c = _cache(lib, "e4m3", pages, page, 2, 64, 3)
+    gone = table.clone()
+    for b, n in enumerate(lens):
+        gone[b, :max(0, n - window) // page] = -1
+    q, ws = _q(1, 3, 8, 64), lib.make_kv_workspace(c, 3, 8)
+    got = lib.paged_attention(c, q, gone.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), window=window, workspace=ws)
+    torch.cuda.synchronize()
+    assert lib.last_device_status(ws) == lib.HQ_OK
+    _check(got, K.attention(c, q, table, lens, 64 ** -0.5, window))
+
+
 @pytest.mark.parametrize("kind", K.KINDS)
 @pytest.mark.parametrize("softcap", [0.5, 30.0])
 def test_softcap(lib, kind, softcap):
