@@ -393,17 +393,23 @@ HQ_API size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, in
 HQ_API hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* rows,
                                void* workspace, size_t ws_bytes, hq_stream_t stream);
 
-/* Cached tokens back as contiguous bf16 rows (values as the cache holds them, rounded to nearest even).
- *   page_table  int32 [B][table_stride]: sequence b's page ids; entries past its last page are not read
- *   starts      int64 [B + 1], ascending: sequence b's tokens go to rows starts[b] .. starts[b + 1] - 1
- *   first       int32 [B]: index in its sequence of the first token that is read, or NULL for 0
- *   total       rows of k_out and v_out, bf16 [total][num_heads][head_dim]
- * Rows that no sequence covers, and tokens whose page is past the table's row or the pools, are left unwritten; the
- * latter, and a sequence that ends past `total`, record HQ_ERR_INVALID_ARG.  One kernel. */
-HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const int32_t* page_table,
-                              int64_t table_stride, const int64_t* starts, const int32_t* first, int64_t B,
-                              int64_t total, void* k_out, void* v_out, void* workspace, size_t ws_bytes,
-                              hq_stream_t stream);
+/* One hq_kv_read call. */
+typedef struct {
+  const int32_t* page_table; /* int32 [B][table_stride]: sequence b's page ids; entries past its last page are not read */
+  int64_t table_stride;
+  const int64_t* starts;     /* int64 [B + 1], ascending: sequence b's tokens go to rows starts[b] .. starts[b + 1] - 1 */
+  const int32_t* first;      /* int32 [B]: index in its sequence of the first token that is read, or NULL for 0 */
+  int64_t B;                 /* sequences, >= 0 */
+  int64_t total;             /* rows of k_out and v_out, >= 0 */
+  void* k_out;               /* bf16 [total][num_heads][head_dim] */
+  void* v_out;
+} hq_kv_read_t;
+
+/* Cached tokens back as contiguous bf16 rows (values as the cache holds them, rounded to nearest even).  Rows that no
+ * sequence covers, and tokens whose page is past the table's row or the pools, are left unwritten; the latter, and a
+ * sequence that ends past `total`, record HQ_ERR_INVALID_ARG.  One kernel. */
+HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_read_t* args,
+                              void* workspace, size_t ws_bytes, hq_stream_t stream);
 
 /* One hq_paged_attention call. */
 typedef struct {

@@ -75,8 +75,15 @@ class KVAttention(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
-# KVRows and KVAttention, packed in one step
-_KV_ROWS, _KV_ATTENTION = struct.Struct("@PqqiiifPPPqPPP"), struct.Struct("@PPqPqqiffPP")
+class KVRead(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("starts", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("B", ctypes.c_int64), ("total", ctypes.c_int64),
+                ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
+
+
+# KVRows, KVRead and KVAttention, packed in one step
+_KV_ROWS, _KV_READ = struct.Struct("@PqqiiifPPPqPPP"), struct.Struct("@PqPPqqPP")
+_KV_ATTENTION = struct.Struct("@PPqPqqiffPP")
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -121,7 +128,7 @@ _lib.hq_kv_workspace_bytes.argtypes = [_KF, _i64, _i32]
 _lib.hq_kv_workspace_bytes.restype = _sz
 _lib.hq_kv_write.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_write.restype = ctypes.c_int
-_lib.hq_kv_read.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.hq_kv_read.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_read.restype = ctypes.c_int
 _lib.hq_paged_attention.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_paged_attention.restype = ctypes.c_int
@@ -696,18 +703,24 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
     if (_kv_right(page_table, _i32t, 0, dev) and _kv_right(starts, _i64t, 0, dev) and _kv_right(first, _i32t, B, dev)
             and _kv_right(ko, _bf16, size, dev) and _kv_right(vo, _bf16, size, dev) and _device() == dev
             and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
-        pt, pst, pf = page_table.data_ptr(), starts.data_ptr(), None if first is None else first.data_ptr()
+        pt, pst, pf = page_table.data_ptr(), starts.data_ptr(), 0 if first is None else first.data_ptr()
     else:
-        pt, pst, pf, _, _, _ = _kv_ptrs(w, c, (
+        pt, pst, pf, _, _, _ = (p or 0 for p in _kv_ptrs(w, c, (
             (page_table, "page_table", B * cols, _i32t), (starts, "starts", B + 1, _i64t), (first, "first", B, _i32t),
-            (ko, "out[0]", size, _bf16), (vo, "out[1]", size, _bf16), (workspace, "workspace", 0, None)))
+            (ko, "out[0]", size, _bf16), (vo, "out[1]", size, _bf16), (workspace, "workspace", 0, None))))
     if out is None:
-        ko = _on(stream, torch.empty, (total, c.num_heads, c.head_dim), dtype=_bf16, device=c.device)
-        vo = _on(stream, torch.empty_like, ko)
+        shape = (total, c.num_heads, c.head_dim)
+        if stream is None:
+            ko = torch.empty(shape, dtype=_bf16, device=c.device)
+            vo = torch.empty_like(ko)
+        else:
+            ko = _on(stream, torch.empty, shape, dtype=_bf16, device=c.device)
+            vo = _on(stream, torch.empty_like, ko)
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-    st = _lib.hq_kv_read(*c._at, pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr(), workspace.data_ptr(),
-                         workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    x = _KV_READ.pack(pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr())
+    st = _lib.hq_kv_read(*c._at, x, workspace.data_ptr(), workspace.nbytes,
+                         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
         raise HQError(st, w)
     return ko, vo

@@ -135,30 +135,30 @@ hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, c
   return launched(launch_kv_write(fmt->kind, fmt->head_dim, a, (cudaStream_t)stream));
 }
 
-hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const int32_t* page_table,
-                       int64_t table_stride, const int64_t* starts, const int32_t* first, int64_t B, int64_t total,
-                       void* k_out, void* v_out, void* workspace, size_t ws_bytes, hq_stream_t stream) {
+hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_read_t* x, void* workspace,
+                       size_t ws_bytes, hq_stream_t stream) {
   hq_status_t st = check_format(fmt);
   if (st != HQ_OK) return st;
-  if (B < 0 || B > kMaxRows || total < 0 || total > ((int64_t)1 << 34) || table_stride < 0 || table_stride > kMaxRows)
+  if (!x || x->B < 0 || x->B > kMaxRows || x->total < 0 || x->total > ((int64_t)1 << 34) || x->table_stride < 0 ||
+      x->table_stride > kMaxRows)
     return HQ_ERR_INVALID_ARG;
-  if (B == 0 || total == 0) return HQ_OK;
+  if (x->B == 0 || x->total == 0) return HQ_OK;
   if ((st = check_cache(fmt, cache)) != HQ_OK) return st;
-  if ((table_stride && !page_table) || !starts || !k_out || !v_out) return HQ_ERR_INVALID_ARG;
-  if (!aligned(page_table, 4) || !aligned(starts, 8) || !aligned(first, 4) || !aligned(k_out, 16) ||
-      !aligned(v_out, 16))
+  if ((x->table_stride && !x->page_table) || !x->starts || !x->k_out || !x->v_out) return HQ_ERR_INVALID_ARG;
+  if (!aligned(x->page_table, 4) || !aligned(x->starts, 8) || !aligned(x->first, 4) || !aligned(x->k_out, 16) ||
+      !aligned(x->v_out, 16))
     return HQ_ERR_ALIGNMENT;
   if ((st = check_workspace(fmt, 0, 1, workspace, ws_bytes)) != HQ_OK) return st;
   KvReadArgs a;
   a.kv = view(fmt, cache);
-  a.page_table = page_table;
-  a.table_stride = table_stride;
-  a.starts = starts;
-  a.first = first;
-  a.B = B;
-  a.total = total;
-  a.k_out = (uint16_t*)k_out;
-  a.v_out = (uint16_t*)v_out;
+  a.page_table = x->page_table;
+  a.table_stride = x->table_stride;
+  a.starts = x->starts;
+  a.first = x->first;
+  a.B = x->B;
+  a.total = x->total;
+  a.k_out = (uint16_t*)x->k_out;
+  a.v_out = (uint16_t*)x->v_out;
   a.status = (int*)workspace;
   return launched(launch_kv_read(fmt->kind, fmt->head_dim, a, (cudaStream_t)stream));
 }

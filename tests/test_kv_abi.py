@@ -79,13 +79,15 @@ def test_read_arguments_are_checked():
     hq = _hq()
     L, f = hq._lib, _fmt(hq)
     c = ctypes.byref(hq.KVPools(0x10000, 0x20000, 0x30000, 0x40000, None, None))
-    ok = dict(fmt=ctypes.byref(f), cache=c, table=0x50000, stride=4, starts=0x60000, first=None, B=2, total=0,
-              k=0x70000, v=0x80000, ws=0x90000, n=1 << 20, stream=None)
-    call = lambda **k: L.hq_kv_read(*{**ok, **k}.values())  # noqa: E731
+    ok = dict(page_table=0x50000, table_stride=4, starts=0x60000, first=None, B=2, total=0, k_out=0x70000, v_out=0x80000)
+    call = lambda ws=0x90000, n=1 << 20, **k: L.hq_kv_read(  # noqa: E731
+        ctypes.byref(f), c, ctypes.byref(hq.KVRead(**{**ok, **k})), ws, n, None)
+    assert ctypes.sizeof(hq.KVRead) == hq._KV_READ.size
     assert call() == hq.HQ_OK and call(B=0, total=5) == hq.HQ_OK
+    assert L.hq_kv_read(ctypes.byref(f), c, None, 0x90000, 1 << 20, None) == hq.HQ_ERR_INVALID_ARG
     for over, code in ((dict(B=-1), hq.HQ_ERR_INVALID_ARG), (dict(total=-1), hq.HQ_ERR_INVALID_ARG),
-                       (dict(total=3, starts=None), hq.HQ_ERR_INVALID_ARG), (dict(total=3, k=None), hq.HQ_ERR_INVALID_ARG),
-                       (dict(total=3, v=0x80008), hq.HQ_ERR_ALIGNMENT), (dict(total=3, ws=None), hq.HQ_ERR_WORKSPACE)):
+                       (dict(total=3, starts=None), hq.HQ_ERR_INVALID_ARG), (dict(total=3, k_out=None), hq.HQ_ERR_INVALID_ARG),
+                       (dict(total=3, v_out=0x80008), hq.HQ_ERR_ALIGNMENT), (dict(total=3, ws=None), hq.HQ_ERR_WORKSPACE)):
         assert call(**over) == code, over
 
 
