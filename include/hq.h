@@ -388,7 +388,7 @@ HQ_API size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, in
  *   (a, b) -> (a cos - b sin, b cos + a sin)       for the rotated pairs, angles of the row's position
  * query heads are rounded once to bf16 into q_out; key heads, and value heads as they are, go to the row's slot,
  * rounded once to the cache's format (nearest even, saturating; a scale of zero gives zero codes, and an e2m1 zero has
- * no sign).  A row whose position is outside [0, num_positions) is skipped whole, a row whose slot is past the pools
+ * no sign).  A NaN stays one: as its bf16 value, its e4m3 code, or its NVFP4 block's scale.  A row whose position is outside [0, num_positions) is skipped whole, a row whose slot is past the pools
  * is not cached; both record HQ_ERR_INVALID_ARG.  Two rows of one call must not name one slot.  One kernel. */
 HQ_API hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* rows,
                                void* workspace, size_t ws_bytes, hq_stream_t stream);

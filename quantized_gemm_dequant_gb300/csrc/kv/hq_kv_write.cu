@@ -65,16 +65,21 @@ __device__ __forceinline__ float lanes_sum(float v) {
   for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-template <int LPH>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int o = LPH / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+// the larger of two; KEEP: a NaN if either is one
+template <bool KEEP>
+__device__ __forceinline__ float larger(float a, float b) {
+  if constexpr (!KEEP) return fmaxf(a, b);
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
-__device__ __forceinline__ float largest(const float (&x)[8]) {
+template <int LPH, bool KEEP>
+__device__ __forceinline__ float lanes_largest(const float (&x)[8]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) m = larger<KEEP>(m, fabsf(x[i]));
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) m = larger<KEEP>(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
@@ -105,17 +110,25 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool on, const float 
 }
 
 // The scale that a lane's eight dims are divided by: e4m3's of the row, NVFP4's of the block of 16 dims (two lanes) with
-// its byte.  0 where all codes are zero.
+// its byte.  0 where all codes are zero.  A NaN is a code of its own in e4m3 and does not count for the scale; e2m1 has
+// none, so it makes its block's scale NaN.
 template <int KIND, int D>
 __device__ __forceinline__ float scale_of(const float (&x)[8], float g, uint32_t& byte) {
   if constexpr (KIND == HQ_KV_E4M3) {
-    const float m = lanes_max<D / 8>(largest(x));
+    const float m = lanes_largest<D / 8, false>(x);
     return m >= KW_FAST && m < INFINITY ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
   } else {
-    const float m = lanes_max<2>(largest(x));
+    const float m = lanes_largest<2, true>(x);
     byte = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
     return __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(byte)).x, g);
   }
+}
+
+// What a lane's dims are divided by: the scale, or one for e4m3's zero scale, whose dims are zeros (or so small that
+// they become zeros) and NaN.
+template <int KIND>
+__device__ __forceinline__ float divisor(float s) {
+  return KIND == HQ_KV_E4M3 && s == 0.0f ? 1.0f : s;
 }
 
 // A quantised row into the pool; x holds the quotients.
@@ -126,8 +139,9 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scales, int
   if constexpr (KIND == HQ_KV_E4M3) {
     const uint32_t c0 = pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16);
     const uint32_t c1 = pack_e4m3x2(x[4], x[5]) | (pack_e4m3x2(x[6], x[7]) << 16);
-    *reinterpret_cast<uint32_t*>(dst + lo) = s > 0.0f ? c0 : 0u;
-    *reinterpret_cast<uint32_t*>(dst + hi) = s > 0.0f ? c1 : 0u;
+    const uint32_t keep = s > 0.0f ? ~0u : 0x7F7F7F7Fu;  // of a zero scale no sign, but a NaN
+    *reinterpret_cast<uint32_t*>(dst + lo) = c0 & keep;
+    *reinterpret_cast<uint32_t*>(dst + hi) = c1 & keep;
     if (l == 0) reinterpret_cast<float*>(scales)[row] = s;
   } else {
     const uint32_t c = pack_e2m1x8(x);
@@ -273,13 +287,14 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
       } else {
         uint32_t kb = 0, vb = 0;
         const float ks = scale_of<KIND, D>(f, kg, kb), vs = scale_of<KIND, D>(g, vg, vb);
-        if (__all_sync(0xffffffffu, quick(ks) && quick(vs))) {
-          const float ki = __frcp_rn(ks), vi = __frcp_rn(vs);
+        const float kd = divisor<KIND>(ks), vd = divisor<KIND>(vs);
+        if (__all_sync(0xffffffffu, quick(kd) && quick(vd))) {
+          const float ki = __frcp_rn(kd), vi = __frcp_rn(vd);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], ks, ki), g[i] = quotient(g[i], vs, vi);
+          for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], kd, ki), g[i] = quotient(g[i], vd, vi);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], ks), g[i] = __fdiv_rn(g[i], vs);
+          for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], kd), g[i] = __fdiv_rn(g[i], vd);
         }
         if (h < H) {
           store_codes<KIND, D>(a.kv.k, a.kv.k_scale, row, l, klo, khi, f, ks, kb);

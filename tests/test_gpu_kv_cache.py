@@ -193,6 +193,40 @@ def test_infinities_and_nan_in_a_row(lib):
         assert torch.equal(codes[[0, 3]], was[[0, 3]])
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("kind", K.KINDS)
+def test_nan_is_kept(lib, kind, norm):
+    """A NaN is read back as one: alone (of NVFP4 with its block of 16 dims), among zeros, in a row of nothing else; a
+    norm makes the key's whole row NaN.  Other heads and rows are as without it."""
+    T, Hq, H, D = 4, 2, 2, 64
+    x = _rows(3, T, Hq, H, D)
+    w = _weight(4, D) if norm else None
+    def held(rows):
+        c = lib.make_kv_cache(kind, 1, 16, H, D, k_amax=30.0, v_amax=60.0)
+        q = _call(lib, c, rows.cuda(), torch.arange(T), Hq, q_norm=w, k_norm=w)
+        return q, K.cache_values(c, "k")[0, :, :T], K.cache_values(c, "v")[0, :, :T]  # [H, T, D]
+    clean = held(x)
+    y = x.clone()
+    h = y.view(T, Hq + 2 * H, D)
+    for side in (Hq, Hq + H):
+        h[1, side, 37] = float("nan")  # row 1's keys and values are zeros
+        h[2, side + 1, 5] = float("nan")
+        h[3, side] = float("nan")
+    got = held(y)
+    assert torch.equal(got[0], clean[0])
+    for i, side in ((1, "k"), (2, "v")):
+        want = np.zeros((H, T, D), bool)
+        if side == "k" and norm:
+            want[0, 1] = want[1, 2] = want[0, 3] = True
+        else:
+            want[0, 1, slice(32, 48) if kind == "nvfp4" else 37] = True
+            want[1, 2, slice(0, 16) if kind == "nvfp4" else 5] = True
+            want[0, 3] = True
+        assert np.array_equal(np.isnan(got[i]), want), side
+        for head, t in ((0, 0), (1, 0), (1, 1), (0, 2), (1, 3)):
+            assert np.array_equal(got[i][head, t], clean[i][head, t])
+
+
 @pytest.mark.parametrize("kind", K.KINDS)
 def test_rows_of_a_wider_tensor(lib, kind):
     """The rows of a projection that computes more than q, k and v: strided rows give what contiguous ones give."""
