@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest magnitude goes to [1, 2)
-        e = top == 0.0f ? 0 : (e < -100 ? -100 : (e > 100 ? 100 : e));
+        e = top == 0.0f ? 0 : (e < -120 ? -120 : (e > 120 ? 120 : e));  // (both powers are normal numbers)
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
         back = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
@@ -777,12 +777,12 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         vl[t][0] = vl[t][1] = 0.0f;
-        if constexpr (F8) {  // a scale under 2^-100 counts as that: its values are as good as zero
+        if constexpr (F8) {  // a scale under 2^-80 counts as that: its values are as good as zero, and l cannot overflow
           const uint8_t* vscale = vslot_p + t * C::BLOCK + 16 * C::RB;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float v = *reinterpret_cast<const float*>(vscale + 4 * g + 32 * i);
-            vl[t][i] = lg2(v < 7.8886091e-31f ? 7.8886091e-31f : v);
+            vl[t][i] = lg2(v < 8.2718061e-25f ? 8.2718061e-25f : v);
             if (seen != FULL && !((seen >> (16 * t + g + 8 * i)) & 1u)) vl[t][i] = 0.0f;  // whatever is there
           }
         }

@@ -126,6 +126,41 @@ def test_value_scales_far_apart(lib):
 
 
 @pytest.mark.parametrize("kind", K.KINDS)
+@pytest.mark.parametrize("power", [-126, -110, 110, 126])
+def test_queries_of_any_magnitude(lib, kind, power):
+    """Queries at the ends of bf16's range: with scores below 2^-90 the weights are equal; with scores far apart (keys
+    +-1 in one dim, or its block) the larger one's value is the result."""
+    D, n = 64, 20
+    c = lib.make_kv_cache(kind, 2, 16, 1, D, k_amax=1.0, v_amax=4.0)
+    x = torch.zeros(n, 3, D)
+    x[:, 1, 3] = -1.0
+    x[7, 1, 3] = 1.0
+    x[:, 2] = torch.randn(n, D, generator=torch.Generator().manual_seed(1)).clamp(-4, 4)
+    lib.kv_write(c, x.to(torch.bfloat16).reshape(n, -1).cuda(), torch.arange(n).cuda(), 1)
+    q = torch.zeros(1, 1, D, dtype=torch.bfloat16)
+    q[0, 0, 3] = 2.0 ** power
+    out, lse = lib.paged_attention(c, q.cuda(), torch.tensor([[0, 1]], dtype=torch.int32).cuda(),
+                                   torch.tensor([n], dtype=torch.int32).cuda(), scale=0.25)
+    torch.cuda.synchronize()
+    v = K.cache_values(c, "v").transpose(0, 2, 1, 3).reshape(32, D)[:n]
+    want = v[7] if power > 0 else v.mean(0)
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11  # the weights' roundings, then the output's
+    assert np.all(np.abs(K.f64(out)[0, 0] - want) <= 2.0 ** -8 * np.abs(want) + (u + 2.0 ** -18) * np.abs(v).max())
+    want = 2.0 ** (power - 2) * K.cache_values(c, "k")[0, 0, 7, 3] if power > 0 else np.log(n)
+    assert abs(float(lse) - want) <= 2.0 ** -18 * want
+
+
+def test_zero_values_of_the_longest_sequences(lib):
+    """e4m3, one page named over and over: 2^29 tokens of equal scores and values with a zero scale."""
+    page, n = 1024, 2 ** 29
+    c = lib.make_kv_cache("e4m3", 1, page, 1, 64)
+    table = torch.zeros(1, n // page, dtype=torch.int32).cuda()
+    out, lse = lib.paged_attention(c, _q(1, 1, 2, 64), table, torch.tensor([n], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert not out.any() and torch.all((lse.cpu() - 29 * np.log(2.0)).abs() <= 2.0 ** -18 + 29 * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("kind", K.KINDS)
 def test_all_value_scales_zero(lib, kind):
     lens = [50]
     table, pages = K.tables(lens, 16)
