@@ -6,10 +6,12 @@
 //
 // Memory-bound: every element is read once and written once, and the instructions per element decide whether that is
 // reached.  A CTA takes one token; its four warps take every fourth step of 256 / D heads of one kind (query, key or
-// value), four query steps and the first key and value step in flight at once.  D / 8 lanes hold a head's row.  For a
-// rotation by halves a lane holds four dims of the first half and their four partners, so that the rotation needs no
-// exchange between lanes and a lane's four angles serve both; otherwise it holds eight neighbouring dims.  Sums of
-// squares and largest magnitudes are shuffles inside the head's lanes.
+// value), up to four query steps and the first key and value step in flight at once.  Where the heads do not fill the
+// warps' steps, the warps take their places in turn from token to token, since a CTA holds its room on the SM until its
+// slowest warp is done (8 / 1 heads of 128 dims, 20000 tokens e4m3: 78 us without, 63 so).  D / 8 lanes hold a head's
+// row.  For a rotation by halves a lane holds four dims of the first half and their four partners, so that the rotation
+// needs no exchange between lanes and a lane's four angles serve both; otherwise it holds eight neighbouring dims.  Sums
+// of squares and largest magnitudes are shuffles inside the head's lanes.
 // Measured on a GB300, 8192 tokens of 32 query and 8 key-value heads of 128 dims into e4m3: 38.7 us, 73% of the measured
 // copy bandwidth (a warp per token and two heads: 160; without the next token on its way: 47).
 #include <cuda_runtime.h>
@@ -109,18 +111,30 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool on, const float 
   }
 }
 
+// NVFP4's global scale of one side and what block scales are divided by
+struct Global {
+  float g, six, inverse;  // g, 6 g, 1 / (6 g)
+  bool quick;             // quotient() may divide by 6 g
+  __device__ __forceinline__ explicit Global(float x) : g(x) {
+    six = __fmul_rn(6.0f, x);
+    inverse = __frcp_rn(six);
+    quick = six >= KW_FAST && six < INFINITY;
+  }
+};
+
 // The scale that a lane's eight dims are divided by: e4m3's of the row, NVFP4's of the block of 16 dims (two lanes) with
 // its byte.  0 where all codes are zero.  A NaN is a code of its own in e4m3 and does not count for the scale; e2m1 has
 // none, so it makes its block's scale NaN.
 template <int KIND, int D>
-__device__ __forceinline__ float scale_of(const float (&x)[8], float g, uint32_t& byte) {
+__device__ __forceinline__ float scale_of(const float (&x)[8], const Global& g, uint32_t& byte) {
   if constexpr (KIND == HQ_KV_E4M3) {
     const float m = lanes_largest<D / 8, false>(x);
     return m >= KW_FAST && m < INFINITY ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
   } else {
     const float m = lanes_largest<2, true>(x);
-    byte = g > 0.0f ? pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.0f, g)), 0.0f) & 0xFFu : 0u;
-    return __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(byte)).x, g);
+    const float y = g.quick && m < INFINITY ? quotient(m, g.six, g.inverse) : __fdiv_rn(m, g.six);
+    byte = g.g > 0.0f ? pack_e4m3x2(y, 0.0f) & 0xFFu : 0u;
+    return __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(byte)).x, g.g);
   }
 }
 
@@ -150,20 +164,24 @@ __device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scales, int
   }
 }
 
-constexpr int KW_STEPS = 4;  // query steps of a warp that are kept in registers
-
 // What a warp reads of one token.
+template <int STEPS>
 struct Token {
-  Row q[KW_STEPS], k, v;
+  Row q[STEPS], k, v;
   float4 cs, sn;  // the lane's four angles
   int64_t slot;
   int64_t pos;
 };
 
+constexpr int KW_STEPS = 4;  // query steps of a warp that are kept in registers, at most
+
+// STEPS: query steps of a warp that are kept in registers, 1, 2 or KW_STEPS.  A step without heads costs its instructions
+// all the same (with KW_STEPS alone: 16 / 4 heads of 128 dims, 9029 tokens NVFP4 35.1 us, so 27.5; 8 / 1 heads, 20000
+// tokens e4m3 63 and 41).  Five CTAs per SM where one step leaves the registers are no faster.
 // MORE: a warp has at least two query steps beyond those that its registers hold; they are loaded as many at a time (56
 // heads of 256 dims: 243 us one by one, 194 so).  With one beyond them it is loaded on its own: the batch's registers
 // cost 32 heads of 128 dims 38.4 us -> 40.2.
-template <int KIND, int D, int MODE, bool MORE>
+template <int KIND, int D, int MODE, int STEPS, bool MORE>
 __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteArgs a) {
   constexpr int LPH = D / 8;     // lanes of a head's row
   constexpr int HPW = 32 / LPH;  // heads of one step
@@ -179,19 +197,21 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
   int lo = 8 * l, hi = 8 * l + 4;
   if (halves && turn) lo = 4 * l, hi = R / 2 + 4 * l;
   const int klo = neighbours ? 8 * l : lo, khi = neighbours ? 8 * l + 4 : hi;
-  const int h0 = warp * HPW + sub;
+  int h0 = warp * HPW + sub;  // the lane's first head of the token; the warps take the places in turn
   const int ktok = Hq * D, vtok = ktok + H * D;
 
-  auto read_place = [&](int64_t t, Token& x) {
+  auto read_place = [&](int64_t t, Token<STEPS>& x) {
     const bool live = t < a.T;
     x.slot = live ? a.slots[t] : -1;
     x.pos = MODE != NO_TURN && live ? a.positions[t] : 0;
   };
-  auto read_rows = [&](int64_t t, Token& x) {  // its position is known
+  const int by = H % NEXT || Hq % NEXT ? HPW : 0;
+  auto next_h0 = [&](int h) { return h + by < NEXT ? h + by : h + by - NEXT; };
+  auto read_rows = [&](int64_t t, int h0, Token<STEPS>& x) {  // its position is known
     const bool live = t < a.T;
     const uint16_t* row = a.qkv + t * a.row_stride + h0 * D;
 #pragma unroll
-    for (int s = 0; s < KW_STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, live && h0 + s * NEXT < Hq);
+    for (int s = 0; s < STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, live && h0 + s * NEXT < Hq);
     x.k = load_row(row + ktok, klo, khi, live && h0 < H);
     x.v = load_row(row + vtok, 8 * l, 8 * l + 4, live && h0 < H);
     if constexpr (MODE != NO_TURN) {
@@ -206,16 +226,15 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
   unpack_row(a.q_norm ? load_row(a.q_norm, lo, hi, true) : kw, w);
   if (a.k_norm) kw = load_row(a.k_norm, klo, khi, true);
   const bool q_on = a.q_norm != nullptr, k_on = a.k_norm != nullptr;
-  float kg = 1.0f, vg = 1.0f;
-  if constexpr (KIND == HQ_KV_NVFP4) kg = *a.kv.k_global, vg = *a.kv.v_global;
+  const Global kg(KIND == HQ_KV_NVFP4 ? *a.kv.k_global : 1.0f), vg(KIND == HQ_KV_NVFP4 ? *a.kv.v_global : 1.0f);
   const uint32_t ps = (uint32_t)a.kv.page_size;
   const int64_t G = gridDim.x, slots = a.kv.num_pages * ps;
-  Token x, y, z;
+  Token<STEPS> x, y, z;
   read_place(blockIdx.x, x);
   read_place(blockIdx.x + G, y);
-  read_rows(blockIdx.x, x);
-  for (int64_t t = blockIdx.x; t < a.T; t += G, x = y, y.slot = z.slot, y.pos = z.pos) {
-    read_rows(t + G, y);
+  read_rows(blockIdx.x, h0, x);
+  for (int64_t t = blockIdx.x; t < a.T; t += G, x = y, y.slot = z.slot, y.pos = z.pos, h0 = next_h0(h0)) {
+    read_rows(t + G, next_h0(h0), y);
     read_place(t + 2 * G, z);
     const bool cached = x.slot >= 0 && x.slot < slots;
     const bool placed = MODE == NO_TURN || (x.pos >= 0 && x.pos < a.num_positions);
@@ -226,18 +245,18 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
     // ---- query heads
     uint16_t* out = a.q_out + (t * Hq + h0) * D;
 #pragma unroll
-    for (int s = 0; s < KW_STEPS; ++s) {
+    for (int s = 0; s < STEPS; ++s) {
       float f[8];
       unpack_row(x.q[s], f);
       norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
       if (h0 + s * NEXT < Hq) store_row(out + s * NEXT * D, lo, hi, f);
     }
-    for (int h = h0 + KW_STEPS * NEXT; MORE && h - sub < Hq; h += KW_STEPS * NEXT) {
+    for (int h = h0 + STEPS * NEXT; MORE && h - sub < Hq; h += STEPS * NEXT) {
       const uint16_t* row = a.qkv + t * a.row_stride + (int64_t)h * D;
 #pragma unroll
-      for (int s = 0; s < KW_STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, h + s * NEXT < Hq);
+      for (int s = 0; s < STEPS; ++s) x.q[s] = load_row(row + s * NEXT * D, lo, hi, h + s * NEXT < Hq);
 #pragma unroll
-      for (int s = 0; s < KW_STEPS; ++s) {
+      for (int s = 0; s < STEPS; ++s) {
         float f[8];
         unpack_row(x.q[s], f);
         norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
@@ -245,7 +264,7 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
       }
     }
 
-    for (int h = h0 + KW_STEPS * NEXT; !MORE && h - sub < Hq; h += NEXT) {
+    for (int h = h0 + STEPS * NEXT; !MORE && h - sub < Hq; h += NEXT) {
       float f[8];
       unpack_row(load_row(a.qkv + t * a.row_stride + (int64_t)h * D, lo, hi, h < Hq), f);
       norm_rotate<LPH, MODE>(f, q_on, w, a.eps, turn, cs, sn);
@@ -270,11 +289,17 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
         const int half = R / 2, i0 = 8 * l < half ? 8 * l : 8 * l - half;
         const int partner = turn ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
         const float sign = 8 * l < half ? -1.0f : 1.0f;
-        const float* angles = a.cos_sin + x.pos * R;
+        const float4* angles = reinterpret_cast<const float4*>(a.cos_sin + x.pos * R + (turn ? i0 : 0));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = __shfl_sync(0xffffffffu, f[i], partner);
-          if (turn) f[i] = fmaf(f[i], angles[i0 + i], sign * p * angles[half + i0 + i]);
+        for (int i = 0; i < 2; ++i) {
+          const float4 ac = angles[i], as = angles[half / 4 + i];
+          const float kc[4] = {ac.x, ac.y, ac.z, ac.w}, kn[4] = {as.x, as.y, as.z, as.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& y = f[4 * i + j];
+            const float p = __shfl_sync(0xffffffffu, y, partner);
+            if (turn) y = fmaf(y, kc[j], sign * p * kn[j]);
+          }
         }
       }
       unpack_row(x.v, g);
@@ -305,8 +330,8 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
   }
 }
 
-template <int KIND, int D, int MODE, bool MORE>
-cudaError_t launch_more(const KvWriteArgs& a, cudaStream_t stream) {
+template <int KIND, int D, int MODE, int STEPS, bool MORE>
+cudaError_t launch_steps(const KvWriteArgs& a, cudaStream_t stream) {
   static std::atomic<int> resident{0};  // CTAs that the device holds at once
   int n = resident.load(std::memory_order_relaxed);
   if (n == 0) {
@@ -314,19 +339,22 @@ cudaError_t launch_more(const KvWriteArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_write_kernel<KIND, D, MODE, MORE>, KW_THREADS, 0);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_write_kernel<KIND, D, MODE, STEPS, MORE>, KW_THREADS, 0);
     if (e != cudaSuccess) return e;
     n = (per > 0 ? per : 1) * (sms > 0 ? sms : 1);
     resident.store(n, std::memory_order_relaxed);
   }
-  return launch_kernel(kv_write_kernel<KIND, D, MODE, MORE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
+  return launch_kernel(kv_write_kernel<KIND, D, MODE, STEPS, MORE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
                        a);
 }
 
 template <int KIND, int D, int MODE>
 cudaError_t launch(const KvWriteArgs& a, cudaStream_t stream) {
-  return a.q_heads > (KW_STEPS + 1) * (KW_THREADS / 32) * (256 / D) ? launch_more<KIND, D, MODE, true>(a, stream)
-                                                              : launch_more<KIND, D, MODE, false>(a, stream);
+  constexpr int NEXT = KW_THREADS / 32 * (256 / D);
+  if (a.q_heads <= NEXT) return launch_steps<KIND, D, MODE, 1, false>(a, stream);
+  if (a.q_heads <= 2 * NEXT) return launch_steps<KIND, D, MODE, 2, false>(a, stream);
+  return a.q_heads > (KW_STEPS + 1) * NEXT ? launch_steps<KIND, D, MODE, KW_STEPS, true>(a, stream)
+                                           : launch_steps<KIND, D, MODE, KW_STEPS, false>(a, stream);
 }
 
 template <int KIND, int D>
