@@ -31,8 +31,8 @@
 //    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.
 //
 // Measured on a GB300 (6.69 TB/s measured copy), 8 query heads of 128 dims per key-value head unless said: bf16, 24
-// sequences of up to 5000 tokens, 4 query heads: 42.9 us, 89% of copy; e4m3, 64 of up to 16384: 92.1 us, 90%; e4m3, one
-// of 131072, 4 query heads: 51.5 us, 80%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 27.7 us, 71%; NVFP4,
+// sequences of up to 5000 tokens, 4 query heads: 43.1 us, 88% of copy; e4m3, 64 of up to 16384: 93.5 us, 89%; e4m3, one
+// of 131072, 4 query heads: 52.2 us, 79%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 28.1 us, 70%; NVFP4,
 // 128 of up to 8192: 133 us, 69% (bound by the instructions of decoding: 2.2 a cycle, half on the integer pipe).
 #pragma once
 #include <cuda_runtime.h>
