@@ -32,7 +32,7 @@
 //
 // Measured on a GB300 (6.69 TB/s measured copy), 8 query heads of 128 dims per key-value head unless said: bf16, 24
 // sequences of up to 5000 tokens, 4 query heads: 43.1 us, 88% of copy; e4m3, 64 of up to 16384: 93.5 us, 89%; e4m3, one
-// of 131072, 4 query heads: 52.2 us, 79%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 28.1 us, 70%; NVFP4,
+// of 131072, 4 query heads: 52.2 us, 79%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 27.4 us, 72%; NVFP4,
 // 128 of up to 8192: 133 us, 69% (bound by the instructions of decoding: 2.2 a cycle, half on the integer pipe).
 #pragma once
 #include <cuda_runtime.h>
@@ -87,10 +87,10 @@ struct KaCfg {
   static constexpr int BLOCK = 16 * (RB + SB);       // a block's codes, then its scales
   static constexpr int SIDE = TB * BLOCK;            // a chunk's keys, or its values
   // A ring step is a chunk's keys and values, one wait and one look at the table for both; of bf16, which has twice the
-  // bytes, it is one side.
+  // bytes, it is one side.  (Of e4m3 heads of 256 dims one side a step makes five steps of two: 80 us -> 86.)
   static constexpr bool PAIR = KIND != HQ_KV_BF16;
   static constexpr int STEP = PAIR ? 2 * SIDE : SIDE;
-  static constexpr int SUMS = PAIR ? 1 : 2;  // of a score: every other 16 dims of bf16 apart, a shorter chain
+  static constexpr int SUMS = KIND == HQ_KV_BF16 ? 2 : 1;  // of a score: every other 16 dims of bf16 apart, a shorter chain
   // Beginning and ending a pair costs a CTA about as long as streaming so many bytes (3 to 4 us): so many units of the
   // list are the pair's own.  Without them the CTAs with more pairs were up to a fifth later than the others (a batch
   // of 64 e4m3 sequences: 99 us, with them 94 to 96).
@@ -100,7 +100,10 @@ struct KaCfg {
   static constexpr size_t PART = 8 * NT * (D + 2);   // floats of a part: o, then (m, l) of each head
   static_assert(CTAS * PART <= KA_MOST_CTAS * KA_SLOT_FLOATS, "workspace");
   static constexpr int PAD = 4;                      // floats: the lanes' stores of a head's dims meet no bank twice
-  static constexpr int MERGE = KA_WARPS * 8 * (D + PAD) * 4;  // eight heads of every warp
+  // heads of every warp that are joined at a time: with eight of 256 dims the ring of bf16 would have two steps instead
+  // of three (33 sequences with a window of 1024: 28.1 us, so 27.4)
+  static constexpr int JOIN = KIND == HQ_KV_BF16 && D == 256 && NT == 1 ? 4 : 8;
+  static constexpr int MERGE = KA_WARPS * JOIN * (D + PAD) * 4;
   static constexpr bool QS = D == 256 && NT == 2;    // q's fragments in shared memory instead of registers
   static constexpr int QBYTES = QS ? D / 16 * NT * 256 : 0;
   static constexpr int FIXED = MERGE + QBYTES + 384;
@@ -923,7 +926,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       }
     }
 
-    // ---- join the four warps, eight heads at a time, and write the pair's result or its part
+    // ---- join the four warps, C::JOIN heads at a time, and write the pair's result or its part
     const bool whole = at.whole();
     float* part = slots + (2 * (int64_t)blockIdx.x + (at.u == lo ? 0 : 1)) * C::PART;
 #pragma unroll
@@ -937,47 +940,55 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           mls[(warp * 8 + 2 * c + k) * 2] = m[x][k];
           mls[(warp * 8 + 2 * c + k) * 2 + 1] = l[x][k];
         }
-        float* to = merge + (warp * 8 + 2 * c + k) * (D + C::PAD);
-        if constexpr (BF) {
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < 8 && 8 * x + j0 < rows; j0 += C::JOIN) {
+        if (C::JOIN == 8 || (2 * c >= j0 && 2 * c < j0 + C::JOIN)) {
 #pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            to[16 * j + g] = o[j][x][k];
-            to[16 * j + 8 + g] = o[j][x][k + 2];
+          for (int k = 0; k < 2; ++k) {
+            float* to = merge + (warp * C::JOIN + 2 * c + k - j0) * (D + C::PAD);
+            if constexpr (BF) {
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                to[16 * j + g] = o[j][x][k];
+                to[16 * j + 8 + g] = o[j][x][k + 2];
+              }
+            } else if constexpr (F8) {
+#pragma unroll
+              for (int j = 0; j < KS; ++j)
+                *reinterpret_cast<float2*>(to + 16 * j + 2 * g) = make_float2(o[j][x][k], o[j][x][k + 2]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < KS; j += 2)
+                *reinterpret_cast<float4*>(to + 16 * j + 4 * g) =
+                    make_float4(o[j][x][k], o[j][x][k + 2], o[j + 1][x][k], o[j + 1][x][k + 2]);
+            }
           }
-        } else if constexpr (F8) {
-#pragma unroll
-          for (int j = 0; j < KS; ++j)
-            *reinterpret_cast<float2*>(to + 16 * j + 2 * g) = make_float2(o[j][x][k], o[j][x][k + 2]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < KS; j += 2)
-            *reinterpret_cast<float4*>(to + 16 * j + 4 * g) =
-                make_float4(o[j][x][k], o[j][x][k + 2], o[j + 1][x][k], o[j + 1][x][k + 2]);
         }
+        __syncthreads();
+        const int left = rows - 8 * x - j0, some = left < C::JOIN ? left : C::JOIN;
+        for (int e = threadIdx.x; e < some * (D / 4); e += KA_THREADS) {
+          const int n = e / (D / 4), r = j0 + n, d = 4 * (e % (D / 4));
+          float top = KA_NONE, sum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < KA_WARPS; ++w) top = fmaxf(top, mls[(w * 8 + r) * 2]);
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < KA_WARPS; ++w) {
+            const float f = ex2(mls[(w * 8 + r) * 2] - top);
+            const float4 v = *reinterpret_cast<const float4*>(merge + (w * C::JOIN + n) * (D + C::PAD) + d);
+            sum = fmaf(f, mls[(w * 8 + r) * 2 + 1], sum);
+            y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
+          }
+          if (whole) {
+            ka_store(a, q0 + 8 * x + r, D, d, y, top, sum, vg);
+          } else {
+            __stcg(reinterpret_cast<float4*>(part + (8 * x + r) * D + d), y);
+            if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NT * D + 2 * (8 * x + r)), make_float2(top, sum));
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      const int some = rows - 8 * x < 8 ? rows - 8 * x : 8;
-      for (int e = threadIdx.x; e < some * (D / 4); e += KA_THREADS) {
-        const int r = e / (D / 4), d = 4 * (e % (D / 4));
-        float top = KA_NONE, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < KA_WARPS; ++w) top = fmaxf(top, mls[(w * 8 + r) * 2]);
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < KA_WARPS; ++w) {
-          const float f = ex2(mls[(w * 8 + r) * 2] - top);
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + r) * (D + C::PAD) + d);
-          sum = fmaf(f, mls[(w * 8 + r) * 2 + 1], sum);
-          y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
-        }
-        if (whole) {
-          ka_store(a, q0 + 8 * x + r, D, d, y, top, sum, vg);
-        } else {
-          __stcg(reinterpret_cast<float4*>(part + (8 * x + r) * D + d), y);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NT * D + 2 * (8 * x + r)), make_float2(top, sum));
-        }
-      }
-      __syncthreads();
     }
     if (whole) continue;
 
