@@ -407,7 +407,7 @@ typedef struct {
 
 /* Cached tokens back as contiguous bf16 rows (values as the cache holds them, rounded to nearest even).  Rows that no
  * sequence covers, and tokens whose page is past the table's row or the pools, are left unwritten; the latter, and a
- * sequence that ends past `total`, record HQ_ERR_INVALID_ARG.  One kernel. */
+ * sequence that ends past `total`, record HQ_ERR_INVALID_ARG.  With B or total 0 nothing is done.  One kernel. */
 HQ_API hq_status_t hq_kv_read(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_read_t* args,
                               void* workspace, size_t ws_bytes, hq_stream_t stream);
 

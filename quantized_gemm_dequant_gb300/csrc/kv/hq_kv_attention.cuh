@@ -353,7 +353,8 @@ __device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint3
       ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
     } else {  // (all (m, l) have been read, and o's dims are this thread's alone)
       __stcg(reinterpret_cast<float4*>(part_at(0) + e), y[i]);
-      if (d == 0) __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(tops[2 * r], tops[2 * r + 1]));
+      if (d == 0)
+        __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(tops[2 * r], tops[2 * r + 1]));
     }
   }
   __syncthreads();  // the next pair's join writes where this one's was read
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   // ---- the ring's front: this warp's chunks of the share, keys and values alternating
   KaWalk<TB, C::EXTRA> ahead = at;
   int next_tok = ahead.from() + 16 * TB * warp, next_end = ahead.to();
-  int place = -1;       // lane i: the place in the pools (in blocks) of the warp's i-th block from the last look at the table
+  int place = -1;       // lane i: the place in the pools (in blocks) of the warp's i-th block since the last table look
   int used = 32;        // blocks of it that are used up
   bool more = true;     // false: all of the share has been asked for
   int put = 0, get = 0;
@@ -1013,7 +1014,8 @@ cudaError_t launch_ka(const KvAttnArgs& a, int sms, int64_t tokens, uint8_t* wor
   // no more CTAs than the longest lengths make shares
   const int64_t per = (tokens + 16 * C::TB - 1) / (16 * C::TB);
   const int64_t pairs = a.B * a.kv.heads * ((a.group + KA_ROWS - 1) / KA_ROWS);
-  const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4), all = C::CTAS * sms < KA_MOST ? C::CTAS * sms : KA_MOST;
+  const int64_t want = (pairs * (C::EXTRA + (per > 0 ? per : 1)) + C::EXTRA + 3) / (C::EXTRA + 4);
+  const int64_t all = C::CTAS * sms < KA_MOST ? C::CTAS * sms : KA_MOST;
   return launch_kernel(kv_attention_kernel<KIND, D, NT>, dim3((unsigned)(want < all ? want : all)), dim3(KA_THREADS),
                        C::SMEM, stream, a, reinterpret_cast<float*>(workspace + KV_HEADER_BYTES),
                        reinterpret_cast<int*>(workspace + ka_group_counters_at(sms)),

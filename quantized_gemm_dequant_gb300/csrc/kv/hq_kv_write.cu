@@ -344,8 +344,8 @@ cudaError_t launch_steps(const KvWriteArgs& a, cudaStream_t stream) {
     n = (per > 0 ? per : 1) * (sms > 0 ? sms : 1);
     resident.store(n, std::memory_order_relaxed);
   }
-  return launch_kernel(kv_write_kernel<KIND, D, MODE, STEPS, MORE>, dim3((unsigned)(a.T < n ? a.T : n)), dim3(KW_THREADS), 0, stream,
-                       a);
+  return launch_kernel(kv_write_kernel<KIND, D, MODE, STEPS, MORE>, dim3((unsigned)(a.T < n ? a.T : n)),
+                       dim3(KW_THREADS), 0, stream, a);
 }
 
 template <int KIND, int D, int MODE>
