@@ -2,7 +2,8 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin),   then one rounding:
 //   bf16; e4m3 of y / s with s = absmax / 448; or e2m1 of y / d with d = e4m3(absmax_16 / (6 g)) * g.
-// All steps are fp32; the divisions that decide a code are IEEE divisions.
+// All steps are fp32; the divisions that decide a code give what IEEE divisions give, overflow included: most are products
+// with a reciprocal and their correction.
 //
 // Memory-bound: every element is read once and written once, and the instructions per element decide whether that is
 // reached.  A CTA takes one token; its four warps take every fourth step of 256 / D heads of one kind (query, key or
@@ -33,14 +34,17 @@ constexpr int KW_THREADS = 128;
 
 // x / y rounded to nearest even from yi = RN(1 / y): RN(x yi) is faithful, its residual is exact with one FMA, and one
 // more FMA gives the correctly rounded quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  Valid while the residual stays a normal number: callers take
-// it for y >= 2^-100, where a quotient that can round to a nonzero code has |x| >= 2^-110, and divide otherwise.
+// System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  quick() says for which y callers take it, and they divide
+// otherwise: 1 / y is a normal number there, and the residual, a multiple of ulp(quotient) * ulp(y), is one of 2^-149
+// for every quotient from 2^-10 on; smaller ones become zero codes however they are rounded.  (A row's largest magnitude
+// over 448, kept in all its bits, has a residual of multiples of 2^-140.)  The quotient must be finite: of an infinite
+// one the residual would make a NaN, where a division's saturates.
 __device__ __forceinline__ float quotient(float x, float y, float yi) {
   const float q = __fmul_rn(x, yi);
   return __fmaf_rn(__fmaf_rn(-q, y, x), yi, q);
 }
-constexpr float KW_FAST = 7.8886091e-31f;  // 2^-100
-__device__ __forceinline__ bool quick(float y) { return y == 0.0f || (y >= KW_FAST && y < INFINITY); }
+constexpr float KW_LEAST = 1.0097420e-28f, KW_MOST = 4.2535296e+37f;  // 2^-93, 2^125
+__device__ __forceinline__ bool quick(float y) { return y == 0.0f || (y >= KW_LEAST && y <= KW_MOST); }
 
 // A head's row in its lanes: dims lo .. lo + 3 and hi .. hi + 3 of each lane.
 struct Row {
@@ -114,25 +118,28 @@ __device__ __forceinline__ void norm_rotate(float (&x)[8], bool on, const float 
 // NVFP4's global scale of one side and what block scales are divided by
 struct Global {
   float g, six, inverse;  // g, 6 g, 1 / (6 g)
-  bool quick;             // quotient() may divide by 6 g
+  float most;             // largest magnitudes below it are taken by quotient(): 1024 * 6 g, far into saturation; 0: none is
   __device__ __forceinline__ explicit Global(float x) : g(x) {
     six = __fmul_rn(6.0f, x);
     inverse = __frcp_rn(six);
-    quick = six >= KW_FAST && six < INFINITY;
+    most = six >= KW_LEAST && six <= KW_MOST ? six * 1024.0f : 0.0f;
   }
 };
 
 // The scale that a lane's eight dims are divided by: e4m3's of the row, NVFP4's of the block of 16 dims (two lanes) with
 // its byte.  0 where all codes are zero.  A NaN is a code of its own in e4m3 and does not count for the scale; e2m1 has
-// none, so it makes its block's scale NaN.
+// none, so it makes its block's scale NaN.  fits: no dim's quotient by the scale passes fp32's range (e4m3: it is 449 at
+// most, or quick() refuses the scale; NVFP4: a scale is 2^-9 g at least, so it is below 2^22).
 template <int KIND, int D>
-__device__ __forceinline__ float scale_of(const float (&x)[8], const Global& g, uint32_t& byte) {
+__device__ __forceinline__ float scale_of(const float (&x)[8], const Global& g, uint32_t& byte, bool& fits) {
   if constexpr (KIND == HQ_KV_E4M3) {
     const float m = lanes_largest<D / 8, false>(x);
-    return m >= KW_FAST && m < INFINITY ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
+    fits = true;
+    return m >= KW_LEAST && m < INFINITY ? quotient(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
   } else {
     const float m = lanes_largest<2, true>(x);
-    const float y = g.quick && m < INFINITY ? quotient(m, g.six, g.inverse) : __fdiv_rn(m, g.six);
+    fits = m < g.most;
+    const float y = fits ? quotient(m, g.six, g.inverse) : __fdiv_rn(m, g.six);
     byte = g.g > 0.0f ? pack_e4m3x2(y, 0.0f) & 0xFFu : 0u;
     return __fmul_rn(f16x2_to_f32x2(e4m3x2_to_f16x2(byte)).x, g.g);
   }
@@ -176,7 +183,7 @@ struct Token {
 constexpr int KW_STEPS = 4;  // query steps of a warp that are kept in registers, at most
 
 // STEPS: query steps of a warp that are kept in registers, 1, 2 or KW_STEPS.  A step without heads costs its instructions
-// all the same (with KW_STEPS alone: 16 / 4 heads of 128 dims, 9029 tokens NVFP4 35.1 us, so 27.5; 8 / 1 heads, 20000
+// all the same (with KW_STEPS alone: 16 / 4 heads of 128 dims, 9029 tokens NVFP4 35.1 us, so 27.5, with the check of its range 28.9; 8 / 1 heads, 20000
 // tokens e4m3 63 and 41).  Five CTAs per SM where one step leaves the registers are no faster.
 // MORE: a warp has at least two query steps beyond those that its registers hold; they are loaded as many at a time (56
 // heads of 256 dims: 243 us one by one, 194 so).  With one beyond them it is loaded on its own: the batch's registers
@@ -311,9 +318,10 @@ __global__ void __launch_bounds__(KW_THREADS, 4) kv_write_kernel(const KvWriteAr
         }
       } else {
         uint32_t kb = 0, vb = 0;
-        const float ks = scale_of<KIND, D>(f, kg, kb), vs = scale_of<KIND, D>(g, vg, vb);
+        bool kfit, vfit;
+        const float ks = scale_of<KIND, D>(f, kg, kb, kfit), vs = scale_of<KIND, D>(g, vg, vb, vfit);
         const float kd = divisor<KIND>(ks), vd = divisor<KIND>(vs);
-        if (__all_sync(0xffffffffu, quick(kd) && quick(vd))) {
+        if (__all_sync(0xffffffffu, kfit && vfit && quick(kd) && quick(vd))) {
           const float ki = __frcp_rn(kd), vi = __frcp_rn(vd);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], kd, ki), g[i] = quotient(g[i], vd, vi);
