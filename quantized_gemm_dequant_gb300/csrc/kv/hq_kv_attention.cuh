@@ -273,6 +273,16 @@ struct KaWalk {
   }
 };
 
+// s -> cap tanh(s / cap).  Near zero tanh's Taylor series up to t^9, so that a score far below the cap keeps its relative
+// error: 1 - 2 / (1 + e^2t) there is a difference of two numbers near 1, off by cap 2^-23 (a cap of 1e5: scores off by
+// 0.01).  The series' remainder is under 2^-26 of t where the two meet.
+__device__ __forceinline__ void ka_cap(float& s, float cap, float per_cap) {
+  const float t = s * per_cap, t2 = t * t, y = t * 2.8853900817779268f;  // 2 log2 e
+  const float p = fmaf(t2, fmaf(t2, fmaf(t2, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f);
+  const float far = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(y > 80.0f ? 80.0f : y)));
+  s = fabsf(t) < 0.25f ? fmaf(s * t2, p, s) : far;
+}
+
 // One row's result: 4 dims of o, and lse
 __device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, int d, float4 y, float top, float sum,
                                          float gain) {
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     kg = *a.kv.k_global;
     vg = *a.kv.v_global;
   }
-  const float cap = a.softcap * 1.4426950408889634f;
+  const float cap = a.softcap * 1.4426950408889634f, per_cap = fminf(1.0f / cap, 3.4e38f);  // (a subnormal cap's is infinite)
 
   // ---- one pair after another
   for (; !at.done(); at.next(a, hrs)) {
@@ -613,8 +623,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        qscale[x][k] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + k)) * kg * a.scale;
-        qscale[x][k] *= a.softcap > 0.0f ? 2.0f * 1.4426950408889634f / a.softcap : 1.4426950408889634f;
+        qscale[x][k] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + k)) * kg * a.scale * 1.4426950408889634f;
       }
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -750,12 +759,9 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             s[t][x][i] = (C::SUMS == 2 ? s2[0][x][i] + s2[C::SUMS - 1][x][i] : s2[0][x][i]) *
                          (F8 ? qscale[x][i & 1] * ks[i >> 1] : qscale[x][i & 1]);
       }
-      if (a.softcap > 0.0f) {  // cap * tanh(y) = cap * (1 - 2 / (1 + e^2y)); the scores hold 2 y log2 e
+      if (a.softcap > 0.0f) {
 #pragma unroll
-        for (int i = 0; i < TB * NT * 4; ++i) {
-          float& y = (&s[0][0][0])[i];
-          y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(y > 80.0f ? 80.0f : y)));
-        }
+        for (int i = 0; i < TB * NT * 4; ++i) ka_cap((&s[0][0][0])[i], cap, per_cap);
       }
       if (seen != FULL) {
 #pragma unroll

@@ -82,3 +82,53 @@ def test_nvfp4_globals_at_the_ends(lib, power):
         want, sb = _nvfp4(rows[:, at:at + H], getattr(c, side + "_global").cpu().numpy()[0])
         got, got_sb = _held_nvfp4(c, side, T)
         assert np.array_equal(got_sb, sb) and np.array_equal(got, want), side
+
+
+def _exact_cache(lib, kind, n, D, seed):
+    """One sequence of n tokens whose values (0, +-.5, .. +-2) every format holds exactly, and queries in eighths: with
+    64 dims all products and their sums are whole multiples of 1/16 below 2^11, exact in fp32."""
+    g = torch.Generator().manual_seed(seed)
+    page = 16
+    pages = -(-n // page)
+    c = lib.make_kv_cache(kind, pages, page, 1, D, k_amax=2688.0, v_amax=2688.0)
+    for side in ("k", "v"):
+        code = torch.randint(0, 5, (pages, 1, page, D), generator=g)
+        x = code * 0.5 * (1 - 2 * torch.randint(0, 2, code.shape, generator=g))
+        if kind == "bf16":
+            getattr(c, side).copy_(x)
+        elif kind == "e4m3":
+            getattr(c, side).copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
+            getattr(c, side + "_scale").fill_(1.0)
+        else:
+            e = (code + 8 * (x < 0)).to(torch.uint8)
+            getattr(c, side).copy_(e[..., 0::2] | (e[..., 1::2] << 4))
+            getattr(c, side + "_scale").fill_(0x38)
+    q = (torch.randint(-32, 33, (1, 2, D), generator=g) / 8).to(torch.bfloat16)
+    return c, q, torch.randperm(pages, generator=g).to(torch.int32)[None]
+
+
+@pytest.mark.parametrize("kind", K.KINDS)
+@pytest.mark.parametrize("softcap", [1e-39, 1e-3, 0.7, 30.0, 1e3, 1e5, 1e7, 1e30, 3.4e38])
+def test_caps_of_any_size(lib, kind, softcap):
+    """softcap * tanh(s / softcap) to a relative error: a cap far above the scores is no cap.
+
+    The dot products are exact here, so a score's error is that of the cap's evaluation, relative to the score.  Below
+    a quarter of the cap: a series whose remainder is under 2^-26, and at most eight roundings of 2^-24.  Above:
+    1 - 2 / (1 + e^2t) with exp2 within 2^-22 and its argument's rounding, |2t log2 e| 2^-24, times the derivative, the
+    approximate division within 2 ulp: under 2^-21 in all, of tanh t >= 0.2449.  So 2^-18 of the score is ample."""
+    n, D, scale = 300, 64, 0.125
+    c, q, table = _exact_cache(lib, kind, n, D, 21)
+    out, lse = lib.paged_attention(c, q.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(), scale=scale,
+                                   softcap=softcap)
+    torch.cuda.synchronize()
+    k, v = (K.rows_of(K.cache_values(c, side), table[0].numpy(), c.page_size, 0, n)[:, 0] for side in ("k", "v"))
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11
+    cap = float(np.float32(softcap))
+    for h in range(2):
+        s = cap * np.tanh((k @ K.f64(q)[0, h] * scale) / cap)
+        ds = np.abs(s).max() * (2.0 ** -18 + 2.0 ** -21)
+        e = np.exp(s - s.max())
+        want, wl = e @ v / e.sum(), s.max() + np.log(e.sum())
+        bound = 2.0 ** -8 * np.abs(want) + (u + 2 * ds + 2.0 ** -18) * (e @ np.abs(v)) / e.sum()
+        assert abs(float(lse[0, h]) - wl) <= ds + 2.0 ** -18 + abs(wl) * 2.0 ** -22
+        assert np.all(np.abs(K.f64(out)[0, h] - want) <= bound)
