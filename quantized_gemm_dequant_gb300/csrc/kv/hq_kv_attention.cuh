@@ -23,8 +23,10 @@
 //    fragments' dims are permuted so that a lane's bytes are its own: the dot product does not care about the order of
 //    dims if q follows it, and the output's order is undone when it is stored.
 //  - e4m3: a token's key scale multiplies its score.  Its value scale v multiplies its weight, and a weight must fit
-//    f16: the running maximum is taken over s_j + log2 v_j, so that the largest weight times its scale is about one
-//    whatever the scales' range, while l sums exp2(s_j - m) in fp32 beside it.
+//    f16: o's weights are exp2(s_j - m + log2 v_j - d) with a running d of their own, the largest of what stands before
+//    it, so that the largest weight times its scale is about one whatever the scales' range, while l sums exp2(s_j - m)
+//    in fp32.  (By one maximum for both, a value scale 2^126 times the others before it took their weights out of l.)
+//    A scale of zero has a weight of zero in o and its own in l; o / l is multiplied by 2^d at the end.
 //  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and to o.
 //  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
 //  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
@@ -71,7 +73,7 @@ __host__ __device__ constexpr int ka_ctas(int kind, int dim, int nt) {
 // pairs, then two counters per KA_GROUP CTAs, then one per (sequence, head, row tile).  The slots' room is that of the
 // largest format, so that the counters, which have to be zero between calls, are at one place whatever the calls' shapes
 // are.
-constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 2);  // o, then (m, l) of each row, of 16 heads of 256 dims
+constexpr size_t KA_SLOT_FLOATS = KA_ROWS * (256 + 3);  // o, then (m, l) and d of each row, of 16 heads of 256 dims
 constexpr int KA_MOST_CTAS = 2;                         // per SM, of that size
 constexpr size_t ka_group_counters_at(int sms) {
   return KV_HEADER_BYTES + 2 * (size_t)(KA_MOST_CTAS * sms) * KA_SLOT_FLOATS * sizeof(float);
@@ -97,7 +99,9 @@ struct KaCfg {
   static constexpr int PAIR_BYTES = KIND == HQ_KV_NVFP4 ? 49152 : 81920;
   static constexpr int EXTRA = PAIR_BYTES / (2 * SIDE) > 0 ? PAIR_BYTES / (2 * SIDE) : 1;
   static constexpr int CTAS = ka_ctas(KIND, D, NT);  // resident per SM
-  static constexpr size_t PART = 8 * NT * (D + 2);   // floats of a part: o, then (m, l) of each head
+  static constexpr bool OD = KIND == HQ_KV_E4M3;     // o has a running maximum of its own, d over m
+  static constexpr size_t PART = 8 * NT * (D + (OD ? 3 : 2));  // floats of a part: o, then (m, l), then d of each head
+  static constexpr int ML = OD ? 3 : 2;              // floats of a head in shared memory: m, l, d
   static_assert(CTAS * PART <= KA_MOST_CTAS * KA_SLOT_FLOATS, "workspace");
   static constexpr int PAD = 4;                      // floats: the lanes' stores of a head's dims meet no bank twice
   // heads of every warp that are joined at a time: with eight of 256 dims the ring of bf16 would have two steps instead
@@ -106,7 +110,7 @@ struct KaCfg {
   static constexpr int MERGE = KA_WARPS * JOIN * (D + PAD) * 4;
   static constexpr bool QS = D == 256 && NT == 2;    // q's fragments in shared memory instead of registers
   static constexpr int QBYTES = QS ? D / 16 * NT * 256 : 0;
-  static constexpr int FIXED = MERGE + QBYTES + 384;
+  static constexpr int FIXED = MERGE + QBYTES + 128 + KA_WARPS * 8 * ML * 4;
   static constexpr int LIMIT = (228 * 1024) / CTAS / 128 * 128 - 1024;  // shared memory of a CTA
   static constexpr int FIT = (LIMIT - FIXED) / (KA_WARPS * (STEP + 4));
   static constexpr int DEPTH = FIT < 2 ? 2 : (FIT > 12 ? 12 : FIT);  // ring steps
@@ -283,13 +287,18 @@ __device__ __forceinline__ void ka_cap(float& s, float cap, float per_cap) {
   s = fabsf(t) < 0.25f ? fmaf(s * t2, p, s) : far;
 }
 
-// One row's result: 4 dims of o, and lse
-__device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, int d, float4 y, float top, float sum,
-                                         float gain) {
+// One row's result: 4 dims of o (over: its maximum over m), and lse
+template <bool OD>
+__device__ __forceinline__ void ka_store(const KvAttnArgs& a, int64_t q, int D, int d, float4 y, float over, float m,
+                                         float sum, float gain) {
   const float inv = sum == 0.0f ? 0.0f : gain / sum;  // a NaN stays one
-  *reinterpret_cast<uint2*>(a.out + q * D + d) =
-      make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  if (d == 0 && a.lse) a.lse[q] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+  if constexpr (OD) {  // by 2^over in two steps: half of it is never out of range
+    const float h = ex2(0.5f * over);
+    y.x = y.x * h * h, y.y = y.y * h * h, y.z = y.z * h * h, y.w = y.w * h * h;
+  }
+  *reinterpret_cast<uint2*>(a.out + q * D + d) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  if (d == 0 && a.lse) a.lse[q] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Joins at most 32 parts of a split pair in order: slot `first`, then slots others + k apart.  The result goes to the
@@ -304,7 +313,7 @@ __device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint3
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto part_at = [&](int k) { return slots + (k ? others + k * apart : first) * C::PART; };
   float* factor = merge;  // [head][32]
-  float* tops = mls;      // [head][2]: top, sum
+  float* tops = mls;      // [head][ML]: top, sum, o's top over it
   float4 v[AHEAD][MINE], y[MINE];
   auto take = [&](int k0) {
 #pragma unroll
@@ -318,11 +327,13 @@ __device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint3
   };
   take(0);
   float2 ml[HEADS];
+  float over[HEADS];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int r = warp + i * KA_WARPS;
     ml[i] = lane < parts && r < rows ? __ldcg(reinterpret_cast<const float2*>(part_at(lane) + 8 * NT * D + 2 * r))
                                      : make_float2(KA_NONE, 0.0f);
+    over[i] = C::OD && lane < parts && r < rows ? __ldcg(part_at(lane) + 8 * NT * (D + 2) + r) : KA_NONE;
   }
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
@@ -330,12 +341,21 @@ __device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint3
     float top = ml[i].x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float f = ex2(ml[i].x - top);
-    float sum = f * ml[i].y;
+    float f = ex2(ml[i].x - top), sum = f * ml[i].y, otop = KA_NONE;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (C::OD) {
+      const float y = ml[i].x - top + over[i];
+      otop = fmaxf(otop, y);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) otop = fmaxf(otop, __shfl_xor_sync(0xffffffffu, otop, o));
+      f = ex2(y - otop);
+    }
     factor[r * 32 + lane] = f;
-    if (lane == 0) tops[2 * r] = top, tops[2 * r + 1] = sum;
+    if (lane == 0) {
+      tops[C::ML * r] = top, tops[C::ML * r + 1] = sum;
+      if constexpr (C::OD) tops[C::ML * r + 2] = otop;
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -359,12 +379,15 @@ __device__ __forceinline__ void ka_join(const KvAttnArgs& a, float* slots, uint3
   for (int i = 0; i < MINE; ++i) {
     const int e = 4 * (threadIdx.x + i * KA_THREADS), r = e / D, d = e % D;
     if (r >= rows) continue;
+    const float top = tops[C::ML * r], sum = tops[C::ML * r + 1], otop = C::OD ? tops[C::ML * r + 2] : 0.0f;
     if (!to_part) {
-      ka_store(a, q0 + r, D, d, y[i], tops[2 * r], tops[2 * r + 1], vg);
+      ka_store<C::OD>(a, q0 + r, D, d, y[i], otop, top, sum, vg);
     } else {  // (all (m, l) have been read, and o's dims are this thread's alone)
       __stcg(reinterpret_cast<float4*>(part_at(0) + e), y[i]);
-      if (d == 0)
-        __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(tops[2 * r], tops[2 * r + 1]));
+      if (d == 0) {
+        __stcg(reinterpret_cast<float2*>(part_at(0) + 8 * NT * D + 2 * r), make_float2(top, sum));
+        if constexpr (C::OD) __stcg(part_at(0) + 8 * NT * (D + 2) + r, otop);
+      }
     }
   }
   __syncthreads();  // the next pair's join writes where this one's was read
@@ -416,7 +439,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
   uint32_t* qsm = reinterpret_cast<uint32_t*>(smem + C::MERGE);
   int* found = reinterpret_cast<int*>(smem + C::MERGE + C::QBYTES);  // 2 words
   int* last_one = found + 2;
-  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 128);  // [warp][8 heads][2]
+  float* mls = reinterpret_cast<float*>(smem + C::MERGE + C::QBYTES + 128);  // [warp][8 heads][ML]
   int64_t* scan = reinterpret_cast<int64_t*>(mls);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + C::FIXED + warp * C::DEPTH * C::STEP;
@@ -652,9 +675,11 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][x][i] = 0.0f;
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], od[C::OD ? NT : 1][2];  // od: o's maximum over m
 #pragma unroll
     for (int x = 0; x < NT; ++x) m[x][0] = m[x][1] = KA_NONE, l[x][0] = l[x][1] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < (C::OD ? NT : 1); ++x) od[x][0] = od[x][1] = KA_NONE;
 
     const int end = at.to();
 #pragma unroll 1
@@ -787,12 +812,11 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
         vl[t][0] = vl[t][1] = 0.0f;
-        if constexpr (F8) {  // a scale under 2^-80 counts as that: its values are as good as zero, and l cannot overflow
+        if constexpr (F8) {  // (a scale under 2^-126 counts as zero)
           const uint8_t* vscale = vslot_p + t * C::BLOCK + 16 * C::RB;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float v = *reinterpret_cast<const float*>(vscale + 4 * g + 32 * i);
-            vl[t][i] = lg2(v < 8.2718061e-25f ? 8.2718061e-25f : v);
+            vl[t][i] = lg2(*reinterpret_cast<const float*>(vscale + 4 * g + 32 * i));
             if (seen != FULL && !((seen >> (16 * t + g + 8 * i)) & 1u)) vl[t][i] = 0.0f;  // whatever is there
           }
         }
@@ -807,34 +831,47 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           __syncwarp();
         }
       }
-      // ---- weights; the running maximum is of s, or of s + log2 of the value scale
+      // ---- weights: the running maximum of s, and of s - m + log2 of the value scale
+      auto largest = [&](int x, int k) {
+        float y = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < TB; ++t) y = fmaxf(y, fmaxf(s[t][x][k], s[t][x][k + 2]));
+        return y;
+      };
+      auto largest_scaled = [&](int x, int k) {
+        float y = KA_NONE;
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+          y = fmaxf(y, fmaxf(s[t][x][k] - m[x][k] + vl[t][0], s[t][x][k + 2] - m[x][k] + vl[t][1]));
+        return y;
+      };
+      auto all_largest = [&](float y) {
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, i));
+        return y;
+      };
       bool over = false;
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float y = -INFINITY;
-#pragma unroll
-          for (int t = 0; t < TB; ++t)
-            y = fmaxf(y, F8 ? fmaxf(s[t][x][k] + vl[t][0], s[t][x][k + 2] + vl[t][1])
-                            : fmaxf(s[t][x][k], s[t][x][k + 2]));
-          over |= y > m[x][k] + KA_LAZY;
+          over |= largest(x, k) > m[x][k] + KA_LAZY;
+          if constexpr (C::OD) over |= largest_scaled(x, k) > od[x][k] + KA_LAZY;
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float y = m[x][k];
-#pragma unroll
-            for (int t = 0; t < TB; ++t)
-              y = fmaxf(y, F8 ? fmaxf(s[t][x][k] + vl[t][0], s[t][x][k + 2] + vl[t][1])
-                              : fmaxf(s[t][x][k], s[t][x][k + 2]));
-#pragma unroll
-            for (int i = 4; i < 32; i <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, i));
-            const float f = ex2(m[x][k] - y);
+            const float y = all_largest(fmaxf(m[x][k], largest(x, k))), down = m[x][k] - y;
+            float f = ex2(down);
             m[x][k] = y;
             l[x][k] *= f;
+            if constexpr (C::OD) {  // (KA_NONE at least, so that differences stay numbers)
+              const float z = all_largest(fmaxf(od[x][k] + down, largest_scaled(x, k)));
+              f = ex2(od[x][k] - z + down);
+              od[x][k] = z;
+            }
 #pragma unroll
             for (int j = 0; j < KS; ++j) o[j][x][k] *= f, o[j][x][k + 2] *= f;
           }
@@ -851,7 +888,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             for (int k = 0; k < 2; ++k) {
               const float y = s[t][x][2 * i + k] - m[x][k], e = ex2(y);
               l[x][k] += e;
-              w[k] = F8 ? ex2(y + vl[t][i]) : e;
+              w[k] = C::OD ? ex2(y + (vl[t][i] - od[C::OD ? x : 0][k])) : e;
             }
             pb[t][x][i] = turn8x8(BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]));
           }
@@ -944,8 +981,10 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[x][k] += __shfl_xor_sync(0xffffffffu, l[x][k], i);
         if (g == 0) {
-          mls[(warp * 8 + 2 * c + k) * 2] = m[x][k];
-          mls[(warp * 8 + 2 * c + k) * 2 + 1] = l[x][k];
+          float* to = mls + (warp * 8 + 2 * c + k) * C::ML;
+          to[0] = m[x][k];
+          to[1] = l[x][k];
+          if constexpr (C::OD) to[2] = od[C::OD ? x : 0][k];
         }
       }
 #pragma unroll 1
@@ -976,22 +1015,32 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
         const int left = rows - 8 * x - j0, some = left < C::JOIN ? left : C::JOIN;
         for (int e = threadIdx.x; e < some * (D / 4); e += KA_THREADS) {
           const int n = e / (D / 4), r = j0 + n, d = 4 * (e % (D / 4));
-          float top = KA_NONE, sum = 0.0f;
+          const float* ml = mls + r * C::ML;  // the first warp's
+          constexpr int W = 8 * C::ML;
+          float top = KA_NONE, otop = KA_NONE, sum = 0.0f;
 #pragma unroll
-          for (int w = 0; w < KA_WARPS; ++w) top = fmaxf(top, mls[(w * 8 + r) * 2]);
+          for (int w = 0; w < KA_WARPS; ++w) top = fmaxf(top, ml[w * W]);
+          if constexpr (C::OD) {
+#pragma unroll
+            for (int w = 0; w < KA_WARPS; ++w) otop = fmaxf(otop, ml[w * W] - top + ml[w * W + C::ML - 1]);
+          }
           float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < KA_WARPS; ++w) {
-            const float f = ex2(mls[(w * 8 + r) * 2] - top);
+            float f = ex2(ml[w * W] - top);
             const float4 v = *reinterpret_cast<const float4*>(merge + (w * C::JOIN + n) * (D + C::PAD) + d);
-            sum = fmaf(f, mls[(w * 8 + r) * 2 + 1], sum);
+            sum = fmaf(f, ml[w * W + 1], sum);
+            if constexpr (C::OD) f = ex2(ml[w * W] - top + ml[w * W + C::ML - 1] - otop);
             y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
           }
           if (whole) {
-            ka_store(a, q0 + 8 * x + r, D, d, y, top, sum, vg);
+            ka_store<C::OD>(a, q0 + 8 * x + r, D, d, y, otop, top, sum, vg);
           } else {
             __stcg(reinterpret_cast<float4*>(part + (8 * x + r) * D + d), y);
-            if (d == 0) __stcg(reinterpret_cast<float2*>(part + 8 * NT * D + 2 * (8 * x + r)), make_float2(top, sum));
+            if (d == 0) {
+              __stcg(reinterpret_cast<float2*>(part + 8 * NT * D + 2 * (8 * x + r)), make_float2(top, sum));
+              if constexpr (C::OD) __stcg(part + 8 * NT * (D + 2) + 8 * x + r, otop);
+            }
           }
         }
         __syncthreads();

@@ -132,3 +132,28 @@ def test_caps_of_any_size(lib, kind, softcap):
         bound = 2.0 ** -8 * np.abs(want) + (u + 2 * ds + 2.0 ** -18) * (e @ np.abs(v)) / e.sum()
         assert abs(float(lse[0, h]) - wl) <= ds + 2.0 ** -18 + abs(wl) * 2.0 ** -22
         assert np.all(np.abs(K.f64(out)[0, h] - want) <= bound)
+
+
+@pytest.mark.parametrize("n,heads,group,D", [(33, 1, 1, 64), (70, 2, 4, 128), (5000, 1, 8, 256), (5000, 1, 16, 256),
+                                             (60001, 1, 4, 128)])
+@pytest.mark.parametrize("low,high", [(None, 50), (None, 100), (-60, 70), (-120, 100), (100, -120), (-100, -100)])
+def test_value_scales_rise_and_fall(lib, n, heads, group, D, low, high):
+    """e4m3: all of the first half's values have a scale of 2^low (None: 0, rows of zeros), the second half's 2^high,
+    or half of either where the other would be out of reach.  The scores are ordinary, so every token's weight counts
+    in the sum of weights whatever its values' scale is."""
+    table, pages = K.tables([n], 16, spare=0)
+    c = lib.make_kv_cache("e4m3", pages, 16, heads, D)
+    K.fill(c, 31)
+    half = n // 2 // 16
+    for j in range(table.shape[1]):
+        p = int(table[0, j])
+        if (low if j < half else high) is None:
+            c.v[p], c.v_scale[p] = 0, 0.0
+        else:
+            c.v_scale[p] = 2.0 ** (low if j < half else high)
+    q = torch.randn(1, heads * group, D, generator=torch.Generator().manual_seed(32)).to(torch.bfloat16)
+    out, lse = lib.paged_attention(c, q.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    want, wl, bo, bl = K.attention(c, q, table, [n], D ** -0.5)
+    assert np.all(np.abs(K.f64(lse) - wl) <= bl)
+    assert np.all(np.abs(K.f64(out) - want) <= bo)
