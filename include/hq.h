@@ -431,9 +431,10 @@ typedef struct {
  *   s_j = scale * (q . k_j), or softcap * tanh(scale * (q . k_j) / softcap) when softcap > 0
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
  * A sequence of length 0 gives out = 0 and lse = -inf.  Places that are not seen may hold anything.
- * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) are rounded to the
- * values' 16-bit type before they multiply them.  E4M3 scales are not negative; a value scale under 2^-126 counts as
- * zero.  A length outside its range is taken as the nearest end of it, and tokens on a page outside the pools are
+ * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) are rounded to a
+ * 16-bit type before they multiply the values: bf16, or for the 8- and 4-bit caches f16 (times the value scale for
+ * E4M3), where what is under 2^-21 of the largest loses bits and what is under 2^-32 counts as zero.  E4M3 scales are
+ * not negative; a value scale under 2^-126 counts as zero.  A length outside its range is taken as the nearest end of it, and tokens on a page outside the pools are
  * left out; both record HQ_ERR_INVALID_ARG, as do lengths that make more than 2^31 units of 16 tokens and heads (then
  * nothing is written).  Results do not depend on timing: the length is split by a fixed rule and the parts are joined
  * in order.  One kernel. */

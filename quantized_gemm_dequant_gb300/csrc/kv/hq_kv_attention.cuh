@@ -30,7 +30,9 @@
 //  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and to o.
 //  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
 //  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
-//    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.
+//    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.  f16's are 2^7 times
+//    that (what stands for the maximum is 7 less): they keep their bits down to 2^-21 of the largest and vanish under
+//    2^-32 of it, beside a token that holds nearly all of the weight (l has them in fp32).
 //
 // Measured on a GB300 (6.69 TB/s measured copy), 8 query heads of 128 dims per key-value head unless said: bf16, 24
 // sequences of up to 5000 tokens, 4 query heads: 43.1 us, 88% of copy; e4m3, 64 of up to 16384: 93.5 us, 89%; e4m3, one
@@ -54,6 +56,7 @@ constexpr int KA_WARPS = 4;
 constexpr int KA_THREADS = 32 * KA_WARPS;
 constexpr int KA_ROWS = 16;          // query heads of one row tile, at most
 constexpr float KA_LAZY = 8.0f;      // the running maximum lags by at most this (log2)
+constexpr float KA_LEAD = 7.0f;      // f16 weights are 2^7 times what they would be: 2^15 at most
 constexpr int KA_GROUP = 16;         // CTAs whose parts of a pair with many are joined first, to one part
 constexpr int KA_MANY = 24;          // parts from more than which that is done
 constexpr int KA_MOST = 32 * KA_GROUP;  // CTAs, so that a join has 32 parts at most
@@ -101,6 +104,7 @@ struct KaCfg {
   static constexpr int CTAS = ka_ctas(KIND, D, NT);  // resident per SM
   static constexpr bool OD = KIND == HQ_KV_E4M3;     // o has a running maximum of its own, d over m
   static constexpr size_t PART = 8 * NT * (D + (OD ? 3 : 2));  // floats of a part: o, then (m, l), then d of each head
+  static constexpr float LEAD = KIND == HQ_KV_NVFP4 ? KA_LEAD : 0.0f;  // m is the maximum less this; d: less KA_LEAD
   static constexpr int ML = OD ? 3 : 2;              // floats of a head in shared memory: m, l, d
   static_assert(CTAS * PART <= KA_MOST_CTAS * KA_SLOT_FLOATS, "workspace");
   static constexpr int PAD = 4;                      // floats: the lanes' stores of a head's dims meet no bank twice
@@ -855,20 +859,20 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          over |= largest(x, k) > m[x][k] + KA_LAZY;
-          if constexpr (C::OD) over |= largest_scaled(x, k) > od[x][k] + KA_LAZY;
+          over |= largest(x, k) > m[x][k] + (KA_LAZY + C::LEAD);
+          if constexpr (C::OD) over |= largest_scaled(x, k) > od[x][k] + (KA_LAZY + KA_LEAD);
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float y = all_largest(fmaxf(m[x][k], largest(x, k))), down = m[x][k] - y;
+            const float y = all_largest(fmaxf(m[x][k], largest(x, k) - C::LEAD)), down = m[x][k] - y;
             float f = ex2(down);
             m[x][k] = y;
             l[x][k] *= f;
             if constexpr (C::OD) {  // (KA_NONE at least, so that differences stay numbers)
-              const float z = all_largest(fmaxf(od[x][k] + down, largest_scaled(x, k)));
+              const float z = all_largest(fmaxf(od[x][k] + down, largest_scaled(x, k) - KA_LEAD));
               f = ex2(od[x][k] - z + down);
               od[x][k] = z;
             }

@@ -157,3 +157,35 @@ def test_value_scales_rise_and_fall(lib, n, heads, group, D, low, high):
     want, wl, bo, bl = K.attention(c, q, table, [n], D ** -0.5)
     assert np.all(np.abs(K.f64(lse) - wl) <= bl)
     assert np.all(np.abs(K.f64(out) - want) <= bo)
+
+
+@pytest.mark.parametrize("kind", K.KINDS)
+@pytest.mark.parametrize("above", [12.0, 16.0, 17.0, 18.0, 19.0])
+@pytest.mark.parametrize("at", [0, 500])
+def test_a_sink_without_values(lib, kind, above, at):
+    """One token holds nearly all of the weight, `above` nats over the others, and has values of zero: the output is
+    what the others bring.  Their weights are rounded to the 16-bit type: bf16 to 2^-9 of each; f16 to 2^-12 of each,
+    or, scaled so that the largest is 2^7 at least, to 2^-25 - 7 of the largest where that is more."""
+    n, D, page = 512, 64, 16
+    c = lib.make_kv_cache(kind, n // page, page, 1, D, k_amax=2688.0, v_amax=2688.0)
+    x = torch.zeros(n, 3, D)
+    x[at, 1] = 6.0  # (the formats hold these exactly, e4m3 to its scale's rounding)
+    x[:, 2] = 6.0
+    x[at, 2] = 0.0
+    if kind == "e4m3":
+        x[at, 2, 1] = 6.0  # the row's scale is as the others': its zeros are codes
+    lib.kv_write(c, x.to(torch.bfloat16).reshape(n, -1).cuda(), torch.arange(n).cuda(), 1)
+    q = torch.full((1, 1, D), 1.0, dtype=torch.bfloat16)
+    out, lse = lib.paged_attention(c, q.cuda(), torch.arange(n // page, dtype=torch.int32)[None].cuda(),
+                                   torch.tensor([n], dtype=torch.int32).cuda(), scale=above / (6 * D))
+    torch.cuda.synchronize()
+    w = np.exp(-float(np.float32(above / (6 * D))) * 6 * D)
+    z = 1.0 + (n - 1) * w
+    want = np.full(D, 6 * (n - 1) * w / z)
+    if kind == "e4m3":
+        want[1] = 6.0
+    u, sub = (2.0 ** -9, 0.0) if kind == "bf16" else (2.0 ** -12, 2.0 ** -32)
+    # the scores' error: above 2^-21 from the product with log2 e and exp2's argument; exp2 and sums 2^-18
+    bound = 2.0 ** -8 * want + (u + 2 * above * 2.0 ** -21 + 2.0 ** -18) * want + sub * 6 * (n - 1) / z
+    assert np.all(np.abs(K.f64(out)[0, 0] - want) <= bound)
+    assert abs(float(lse[0, 0]) - (above + np.log(z))) <= above * 2.0 ** -21 + 2.0 ** -18
