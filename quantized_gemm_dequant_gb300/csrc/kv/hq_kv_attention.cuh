@@ -28,7 +28,8 @@
 //    in fp32.  (By one maximum for both, a value scale 2^126 times the others before it took their weights out of l.)
 //    A scale of zero has a weight of zero in o and its own in l; o / l is multiplied by 2^d at the end.
 //  - nvfp4: code * block scale is exact in f16 (2 + 4 significant bits); the global scales go to q's scale and to o.
-//  - Queries of the f16 kinds are scaled by a power of two per row, so that no bf16 query leaves f16's range.
+//  - Queries of the f16 kinds are scaled by a power of two per row that takes the largest element to [2^14, 2^15): a bf16
+//    element keeps its bits down to 2^-31 of that one, loses them one by one below and is zero under 2^-39 of it.
 //  - The running maximum only moves when a score exceeds it by 8 (powers of two): a vote finds that out, so that the
 //    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.  f16's are 2^7 times
 //    that (what stands for the maximum is 7 less): they keep their bits down to 2^-21 of the largest and vanish under
@@ -639,8 +640,8 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
           for (int i = 0; i < 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest magnitude goes to [1, 2)
-        e = top == 0.0f ? 0 : (e < -120 ? -120 : (e > 120 ? 120 : e));  // (both powers are normal numbers)
+        int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;  // the largest magnitude goes to [2^14, 2^15)
+        e = top == 0.0f ? 0 : (e < -126 ? -126 : (e > 113 ? 113 : e));  // (both powers are normal numbers; 128: infinite)
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
         back = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll

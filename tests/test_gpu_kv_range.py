@@ -189,3 +189,31 @@ def test_a_sink_without_values(lib, kind, above, at):
     bound = 2.0 ** -8 * want + (u + 2 * above * 2.0 ** -21 + 2.0 ** -18) * want + sub * 6 * (n - 1) / z
     assert np.all(np.abs(K.f64(out)[0, 0] - want) <= bound)
     assert abs(float(lse[0, 0]) - (above + np.log(z))) <= above * 2.0 ** -21 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("kind", K.KINDS)
+@pytest.mark.parametrize("power", [10, 18, 24, 28])
+def test_queries_with_one_huge_element(lib, kind, power):
+    """One dim of the queries is 2^power, the keys hold zeros there: the scores come from the other dims, in full.  The
+    others are multiples of 2^-8, so that none needs more than f16's bits at the row's scale; the matrix unit aligns the products of a step to the largest exponent,
+    where a zero key may count as f16's smallest normal: 2^-23 of that for each of the dims."""
+    lens, D = [300, 33], 64
+    table, pages = K.tables(lens, 16)
+    c = lib.make_kv_cache(kind, pages, 16, 2, D, k_amax=168.0, v_amax=168.0)
+    K.fill(c, 41)
+    if kind == "nvfp4":
+        c.k[..., 8] &= 0xF0  # dim 16
+    else:
+        c.k[..., 16] = 0
+    q = torch.randn(2, 8, D, generator=torch.Generator().manual_seed(42)).mul(256).round().div(256).to(torch.bfloat16)
+    q[..., 16] = 2.0 ** power
+    out, lse = lib.paged_attention(c, q.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    want, wl, bo, bl = K.attention(c, q, table, lens, D ** -0.5)
+    ds = 0.0
+    if kind != "bf16":
+        top = c.k_scale.max().item() if kind == "e4m3" else float(c.k_global)
+        ds = D * 2.0 ** -23 * 2.0 ** (power - 14) * top * D ** -0.5
+    v = np.abs(K.cache_values(c, "v")).max()
+    assert np.all(np.abs(K.f64(lse) - wl) <= bl + ds)
+    assert np.all(np.abs(K.f64(out) - want) <= bo + 2 * ds * v)
