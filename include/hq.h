@@ -435,8 +435,12 @@ typedef struct {
  * 16-bit type before they multiply the values: bf16, or for the 8- and 4-bit caches f16 (times the value scale for
  * E4M3), where what is under 2^-21 of the largest loses bits and what is under 2^-32 counts as zero.  E4M3 scales are
  * not negative; a value scale under 2^-126 counts as zero.  A length outside its range is taken as the nearest end of it, and tokens on a page outside the pools are
- * left out; both record HQ_ERR_INVALID_ARG, as do lengths that make more than 2^31 units of 16 tokens and heads (then
- * nothing is written).  Results do not depend on timing: the length is split by a fixed rule and the parts are joined
+ * left out; both record HQ_ERR_INVALID_ARG.
+ * The work is counted in units of 16 tokens (32 for NVFP4 heads of 64 and 128 dims and E4M3 heads of 64) of one sequence,
+ * key-value head and up to 16 of its query heads (of a larger group the cache is read once for every 16), and each of
+ * those counts up to 21 units for itself.  2^31 units or more are not done: a batch that reaches them with one token per
+ * sequence is refused (HQ_ERR_INVALID_ARG; hq_kv_workspace_bytes returns 0), lengths that reach them record
+ * HQ_ERR_INVALID_ARG and nothing is written.  Results do not depend on timing: the length is split by a fixed rule and the parts are joined
  * in order.  One kernel. */
 HQ_API hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache,
                                       const hq_kv_attention_t* args, void* workspace, size_t ws_bytes,

@@ -48,6 +48,12 @@ int64_t pairs(const hq_kv_format_t* f, int64_t batch, int32_t num_q_heads) {
   return batch * f->num_heads * ((num_q_heads / f->num_heads + KA_ROWS - 1) / KA_ROWS);
 }
 
+// The attention counts its work in 31 bits, and a triple as one unit at least beside its own: a batch past that is refused
+// here, lengths that are past it by the kernel.
+bool countable(const hq_kv_format_t* f, int64_t batch, int32_t num_q_heads) {
+  return pairs(f, batch, num_q_heads) <= INT32_MAX / (ka_extra(f->kind, f->head_dim) + 1);
+}
+
 hq_status_t check_workspace(const hq_kv_format_t* f, int64_t batch, int32_t num_q_heads, const void* ws,
                             size_t ws_bytes) {
   if (!ws || ws_bytes < hq_kv_workspace_bytes(f, batch, num_q_heads)) return HQ_ERR_WORKSPACE;
@@ -91,7 +97,8 @@ extern "C" {
 size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, int32_t num_q_heads) {
   if (check_format(fmt) != HQ_OK || batch < 0 || batch > kMaxRows) return 0;
   if (batch == 0) return KV_HEADER_BYTES;
-  if (check_q_heads(fmt, num_q_heads) != HQ_OK || batch * num_q_heads > kMaxRows) return 0;
+  if (check_q_heads(fmt, num_q_heads) != HQ_OK || batch * num_q_heads > kMaxRows || !countable(fmt, batch, num_q_heads))
+    return 0;
   return ka_counters_at(num_sms()) + sizeof(int) * (size_t)pairs(fmt, batch, num_q_heads);
 }
 
@@ -169,8 +176,9 @@ hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* c
   if (st != HQ_OK) return st;
   if (!x) return HQ_ERR_INVALID_ARG;
   if ((st = check_q_heads(fmt, x->num_q_heads)) != HQ_OK) return st;
-  if (x->B < 0 || x->B > kMaxRows || x->B * x->num_q_heads > kMaxRows || x->table_stride < 0 ||
-      x->table_stride > kMaxRows || x->window < 0 || !isfinite(x->scale) || !(x->softcap >= 0.0f) || isinf(x->softcap))
+  if (x->B < 0 || x->B > kMaxRows || x->B * x->num_q_heads > kMaxRows || !countable(fmt, x->B, x->num_q_heads) ||
+      x->table_stride < 0 || x->table_stride > kMaxRows || x->window < 0 || !isfinite(x->scale) || !(x->softcap >= 0.0f) ||
+      isinf(x->softcap))
     return HQ_ERR_INVALID_ARG;
   if (x->B == 0) return HQ_OK;
   if ((st = check_cache(fmt, cache)) != HQ_OK) return st;

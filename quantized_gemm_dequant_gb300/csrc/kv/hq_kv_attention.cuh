@@ -73,6 +73,14 @@ __host__ __device__ constexpr int ka_ctas(int kind, int dim, int nt) {
   return dim == 256 ? 2 : (nt == 2 ? 2 : 3);
 }
 
+// Beginning and ending a pair costs a CTA about as long as streaming so many bytes (3 to 4 us): so many units of the list
+// are the pair's own.  Without them the CTAs with more pairs were up to a fifth later than the others (a batch of 64 e4m3
+// sequences: 99 us, with them 94 to 96).
+__host__ __device__ constexpr int ka_extra(int kind, int dim) {
+  return (kind == HQ_KV_NVFP4 ? 49152 : 81920) /
+         (2 * ka_blocks(kind, dim) * KV_BLOCK * (kv_row_bytes(kind, dim) + kv_scale_bytes(kind, dim)));
+}
+
 // Workspace of a call, for the host (sizes) and the device: the status, then two slots per CTA for the parts of split
 // pairs, then two counters per KA_GROUP CTAs, then one per (sequence, head, row tile).  The slots' room is that of the
 // largest format, so that the counters, which have to be zero between calls, are at one place whatever the calls' shapes
@@ -97,11 +105,7 @@ struct KaCfg {
   static constexpr bool PAIR = KIND != HQ_KV_BF16;
   static constexpr int STEP = PAIR ? 2 * SIDE : SIDE;
   static constexpr int SUMS = KIND == HQ_KV_BF16 ? 2 : 1;  // of a score: every other 16 dims of bf16 apart, a shorter chain
-  // Beginning and ending a pair costs a CTA about as long as streaming so many bytes (3 to 4 us): so many units of the
-  // list are the pair's own.  Without them the CTAs with more pairs were up to a fifth later than the others (a batch
-  // of 64 e4m3 sequences: 99 us, with them 94 to 96).
-  static constexpr int PAIR_BYTES = KIND == HQ_KV_NVFP4 ? 49152 : 81920;
-  static constexpr int EXTRA = PAIR_BYTES / (2 * SIDE) > 0 ? PAIR_BYTES / (2 * SIDE) : 1;
+  static constexpr int EXTRA = ka_extra(KIND, D);
   static constexpr int CTAS = ka_ctas(KIND, D, NT);  // resident per SM
   static constexpr bool OD = KIND == HQ_KV_E4M3;     // o has a running maximum of its own, d over m
   static constexpr size_t PART = 8 * NT * (D + (OD ? 3 : 2));  // floats of a part: o, then (m, l), then d of each head
