@@ -627,6 +627,19 @@ def _kv_right(t, dtype, elements, dev):
                          and t.numel() >= elements and t.is_contiguous())
 
 
+def _kv_space(t, dev):
+    """Whether an optional workspace, of any dtype, is right; the library checks its size."""
+    return t is None or (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous())
+
+
+def _kv_pack(w, layout, *values):
+    """A call's argument struct; a number that its field cannot hold is refused."""
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise HQArgError(w, f"an argument is no number of its field's type or range: {e}") from None
+
+
 def _kv_table(w, page_table, batch):
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise HQArgError(w, f"page_table must be a 2-D [{batch}, pages] tensor")
@@ -665,7 +678,7 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
             and _kv_right(slots, _i64t, T, dev) and slots is not None and _kv_right(q_norm, _bf16, D, dev)
             and _kv_right(k_norm, _bf16, D, dev) and _kv_right(cos_sin, _f32, 0, dev)
             and (R == 0 or _kv_right(positions, _i32t, T, dev)) and _kv_right(q_out, _bf16, T * Hq * D, dev)
-            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+            and _kv_space(workspace, dev)):
         px, psl = x.data_ptr(), slots.data_ptr()
         pqn, pkn = 0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr()
         pcs, pps = (cos_sin.data_ptr(), positions.data_ptr()) if R else (0, 0)
@@ -680,7 +693,8 @@ def kv_write(cache, qkv, slots, num_q_heads, q_norm=None, k_norm=None, eps=1e-6,
                  _on(stream, torch.empty, (T, Hq, D), dtype=_bf16, device=c.device))
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-    r = _KV_ROWS.pack(px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl, q_out.data_ptr())
+    r = _kv_pack(w, _KV_ROWS, px, stride, T, Hq, R, 1 if interleaved else 0, eps, pqn, pkn, pcs, P, pps, psl,
+                 q_out.data_ptr())
     st = _lib.hq_kv_write(*c._at, r, workspace.data_ptr(), workspace.nbytes,
                           _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
@@ -697,12 +711,14 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
         raise HQArgError(w, "starts must be a 1-D [B + 1] tensor")
     B, total = starts.shape[0] - 1, int(total)
+    if total < 0:
+        raise HQArgError(w, "total must not be negative")
     size = total * c.num_heads * c.head_dim
     ko, vo = (None, None) if out is None else out
     cols, dev = _kv_table(w, page_table, B), c._index
     if (_kv_right(page_table, _i32t, 0, dev) and _kv_right(starts, _i64t, 0, dev) and _kv_right(first, _i32t, B, dev)
             and _kv_right(ko, _bf16, size, dev) and _kv_right(vo, _bf16, size, dev) and _device() == dev
-            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+            and _kv_space(workspace, dev)):
         pt, pst, pf = page_table.data_ptr(), starts.data_ptr(), 0 if first is None else first.data_ptr()
     else:
         pt, pst, pf, _, _, _ = (p or 0 for p in _kv_ptrs(w, c, (
@@ -718,7 +734,7 @@ def kv_read(cache, page_table, starts, total, first=None, out=None, workspace=No
             vo = _on(stream, torch.empty_like, ko)
     if workspace is None:
         workspace = make_kv_workspace(c, stream=stream)
-    x = _KV_READ.pack(pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr())
+    x = _kv_pack(w, _KV_READ, pt, cols, pst, pf, B, total, ko.data_ptr(), vo.data_ptr())
     st = _lib.hq_kv_read(*c._at, x, workspace.data_ptr(), workspace.nbytes,
                          _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
@@ -742,7 +758,7 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
             and page_table.dtype is _i32t and page_table.get_device() == dev and page_table.is_contiguous()
             and lens is not None and _kv_right(lens, _i32t, B, dev) and _kv_right(out, _bf16, B * Hq * D, dev)
             and _kv_right(lse, _f32, B * Hq, dev)
-            and (workspace is None or _kv_right(workspace, workspace.dtype, 0, dev))):
+            and _kv_space(workspace, dev)):
         pq, pt, pn = q.data_ptr(), page_table.data_ptr(), lens.data_ptr()
     else:
         pq, pt, pn, _, _, _ = (p or 0 for p in _kv_ptrs(w, c, (
@@ -755,8 +771,8 @@ def paged_attention(cache, q, page_table, lens, scale=None, window=0, softcap=0.
                _on(stream, torch.empty, (B, Hq), dtype=_f32, device=c.device))
     if workspace is None:
         workspace = make_kv_workspace(c, B, Hq, stream=stream)
-    x = _KV_ATTENTION.pack(pq, pt, cols, pn, B, window, Hq, D ** -0.5 if scale is None else scale, softcap,
-                           out.data_ptr(), lse.data_ptr())
+    x = _kv_pack(w, _KV_ATTENTION, pq, pt, cols, pn, B, window, Hq, D ** -0.5 if scale is None else scale,
+                 softcap, out.data_ptr(), lse.data_ptr())
     st = _lib.hq_paged_attention(*c._at, x, workspace.data_ptr(), workspace.nbytes,
                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
