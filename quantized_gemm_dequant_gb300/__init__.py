@@ -81,9 +81,13 @@ class KVRead(ctypes.Structure):
                 ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
 
 
-# KVRows, KVRead and KVAttention, packed in one step
-_KV_ROWS, _KV_READ = struct.Struct("@PqqiiifPPPqPPP"), struct.Struct("@PqPPqqPP")
-_KV_ATTENTION = struct.Struct("@PPqPqqiffPP")
+def _layout(s):
+    """The fields of a structure, which a call packs in one step instead of setting them one by one."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    return struct.Struct("@" + "".join(code[t] for _, t in s._fields_))
+
+
+_KV_ROWS, _KV_READ, _KV_ATTENTION = _layout(KVRows), _layout(KVRead), _layout(KVAttention)
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t

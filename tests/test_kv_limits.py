@@ -26,3 +26,12 @@ def test_a_batch_past_the_count_of_work_is_refused(kind, dim, extra, heads, q_he
         assert call(most + 1) == hq.HQ_ERR_INVALID_ARG
     else:
         assert hq._lib.hq_kv_workspace_bytes(f, rows, q_heads) > 0 and call(rows) == hq.HQ_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("name,layout", [("KVRows", "_KV_ROWS"), ("KVRead", "_KV_READ"), ("KVAttention", "_KV_ATTENTION")])
+def test_packed_arguments_are_the_structures(name, layout):
+    """What a call packs is, byte for byte, the structure with the same fields."""
+    import quantized_gemm_dequant_gb300 as hq
+    s, layout = getattr(hq, name), getattr(hq, layout)
+    values = [0.5 + i if t is ctypes.c_float else 1000 + i for i, (_, t) in enumerate(s._fields_)]
+    assert layout.size == ctypes.sizeof(s) and layout.pack(*values) == bytes(s(*values))
