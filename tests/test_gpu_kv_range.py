@@ -164,8 +164,8 @@ def test_value_scales_rise_and_fall(lib, n, heads, group, D, low, high):
 @pytest.mark.parametrize("at", [0, 500])
 def test_a_sink_without_values(lib, kind, above, at):
     """One token holds nearly all of the weight, `above` nats over the others, and has values of zero: the output is
-    what the others bring.  Their weights are rounded to the 16-bit type: bf16 to 2^-9 of each; f16 to 2^-12 of each,
-    or, scaled so that the largest is 2^7 at least, to 2^-25 - 7 of the largest where that is more."""
+    what the others bring.  Their weights are rounded to the 16-bit type: bf16 (in two parts) to 2^-16 of each; f16 to
+    2^-11 of each, or, scaled so that the largest is 2^7 at least, to 2^-32 of the largest where that is more."""
     n, D, page = 512, 64, 16
     c = lib.make_kv_cache(kind, n // page, page, 1, D, k_amax=2688.0, v_amax=2688.0)
     x = torch.zeros(n, 3, D)
@@ -184,7 +184,7 @@ def test_a_sink_without_values(lib, kind, above, at):
     want = np.full(D, 6 * (n - 1) * w / z)
     if kind == "e4m3":
         want[1] = 6.0
-    u, sub = (2.0 ** -9, 0.0) if kind == "bf16" else (2.0 ** -12, 2.0 ** -32)
+    u, sub = (2.0 ** -16, 0.0) if kind == "bf16" else (2.0 ** -11, 2.0 ** -32)
     # the scores' error: above 2^-21 from the product with log2 e and exp2's argument; exp2 and sums 2^-18
     bound = 2.0 ** -8 * want + (u + 2 * above * 2.0 ** -21 + 2.0 ** -18) * want + sub * 6 * (n - 1) / z
     assert np.all(np.abs(K.f64(out)[0, 0] - want) <= bound)
@@ -217,3 +217,28 @@ def test_queries_with_one_huge_element(lib, kind, power):
     v = np.abs(K.cache_values(c, "v")).max()
     assert np.all(np.abs(K.f64(lse) - wl) <= bl + ds)
     assert np.all(np.abs(K.f64(out) - want) <= bo + 2 * ds * v)
+
+
+@pytest.mark.parametrize("D,heads,group", [(64, 2, 4), (128, 1, 16), (128, 2, 3), (256, 1, 8), (256, 1, 12)])
+def test_bf16_weights_keep_16_bits(lib, D, heads, group):
+    """The weights enter a bf16 cache's products as two bf16 numbers, within 2^-16 of themselves: where values cancel in
+    the output, nothing else is left to err than the scores, exp2 and the sums."""
+    lens, page = [64, 300, 2000], 16
+    table, pages = K.tables(lens, page)
+    c = lib.make_kv_cache("bf16", pages, page, heads, D)
+    K.fill(c, 51)
+    q = torch.randn(len(lens), heads * group, D, generator=torch.Generator().manual_seed(52)).to(torch.bfloat16)
+    out, _ = lib.paged_attention(c, q.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    keys, values = K.cache_values(c, "k"), K.cache_values(c, "v")
+    for b, n in enumerate(lens):
+        k, v = (K.rows_of(x, table[b].clamp(min=0).numpy(), page, 0, n) for x in (keys, values))
+        for h in range(heads * group):
+            kk, vv, qq = k[:, h // group], v[:, h // group], K.f64(q)[b, h]
+            s = kk @ qq * D ** -0.5
+            # sums of D products in fp32, the matrix unit's truncated ones twice that; log2 e and exp2's argument
+            ds = 2 * D * 2.0 ** -24 * np.max(np.abs(kk) @ np.abs(qq)) * D ** -0.5 + np.abs(s).max() * 2.0 ** -21
+            e = np.exp(s - s.max())
+            want = e @ vv / e.sum()
+            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * ds + 2.0 ** -18) * (e @ np.abs(vv)) / e.sum()
+            assert np.all(np.abs(K.f64(out)[b, h] - want) <= bound)
