@@ -388,8 +388,10 @@ HQ_API size_t hq_kv_workspace_bytes(const hq_kv_format_t* fmt, int64_t batch, in
  *   (a, b) -> (a cos - b sin, b cos + a sin)       for the rotated pairs, angles of the row's position
  * query heads are rounded once to bf16 into q_out; key heads, and value heads as they are, go to the row's slot,
  * rounded once to the cache's format (nearest even, saturating; a scale of zero gives zero codes, and an e2m1 zero has
- * no sign).  A NaN stays one: as its bf16 value, its e4m3 code, or its NVFP4 block's scale.  A row whose position is outside [0, num_positions) is skipped whole, a row whose slot is past the pools
- * is not cached; both record HQ_ERR_INVALID_ARG.  Two rows of one call must not name one slot.  One kernel. */
+ * no sign).  A NaN stays one: as its bf16 value, its e4m3 code, or its NVFP4 block's scale.  An infinity saturates like
+ * any large value in NVFP4; in e4m3 it makes its row's scale infinite and itself a NaN.  A row whose position is outside
+ * [0, num_positions) is skipped whole, a row whose slot is past the pools is not cached; both record
+ * HQ_ERR_INVALID_ARG.  Two rows of one call must not name one slot.  One kernel. */
 HQ_API hq_status_t hq_kv_write(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache, const hq_kv_rows_t* rows,
                                void* workspace, size_t ws_bytes, hq_stream_t stream);
 
@@ -434,14 +436,14 @@ typedef struct {
  * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) multiply a bf16
  * cache's values as the sum of two bf16 numbers (16 bits), those of the 8- and 4-bit caches (times the value scale for
  * E4M3) rounded to f16, where what is under 2^-21 of the largest loses bits and what is under 2^-32 counts as zero.
- * E4M3 scales are not negative; a value scale under 2^-126 counts as zero.  A length outside its range is taken as the nearest end of it, and tokens on a page outside the pools are
- * left out; both record HQ_ERR_INVALID_ARG.
+ * E4M3 scales are not negative; a value scale under 2^-126 counts as zero.  A length outside its range is taken as the
+ * nearest end of it, and tokens on a page outside the pools are left out; both record HQ_ERR_INVALID_ARG.
  * The work is counted in units of 16 tokens (32 for NVFP4 heads of 64 and 128 dims and E4M3 heads of 64) of one sequence,
  * key-value head and up to 16 of its query heads (of a larger group the cache is read once for every 16), and each of
  * those counts up to 21 units for itself.  2^31 units or more are not done: a batch that reaches them with one token per
  * sequence is refused (HQ_ERR_INVALID_ARG; hq_kv_workspace_bytes returns 0), lengths that reach them record
- * HQ_ERR_INVALID_ARG and nothing is written.  Results do not depend on timing: the length is split by a fixed rule and the parts are joined
- * in order.  One kernel. */
+ * HQ_ERR_INVALID_ARG and nothing is written.  Results do not depend on timing: the length is split by a fixed rule and
+ * the parts are joined in order.  One kernel. */
 HQ_API hq_status_t hq_paged_attention(const hq_kv_format_t* fmt, const hq_kv_cache_t* cache,
                                       const hq_kv_attention_t* args, void* workspace, size_t ws_bytes,
                                       hq_stream_t stream);

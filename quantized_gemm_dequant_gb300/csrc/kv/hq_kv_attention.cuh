@@ -7,7 +7,9 @@
 // (scores are multiplied by log2 e once), in fp32.
 //
 // What bounds it: the cache is read once and 4 G operations are done per key-value pair of elements for the G query
-// heads that share a head, so up to G = 16 the kernel is bound by memory.  The work is laid out for that:
+// heads that share a head.  bf16 and e4m3 caches are bound by memory up to G = 8 (with 12 and 16, on one or two CTAs per
+// SM less, they reach 71% and 59% of the copy's rate), NVFP4 by the instructions that decode it.  The work is laid out to
+// read the cache once:
 //  - The tokens of all (sequence, head) pairs form one list of small units, cut into equal shares for a fixed number of
 //    CTAs, whatever the lengths are.  A pair inside one share is finished there; one that crosses shares leaves fp32
 //    partial results in the workspace, and the last CTA to arrive joins them in order.  The lengths are read on the
@@ -39,9 +41,10 @@
 //    off is an eighth of the output's own rounding.
 //
 // Measured on a GB300 (6.69 TB/s measured copy), 8 query heads of 128 dims per key-value head unless said: bf16, 24
-// sequences of up to 5000 tokens, 4 query heads: 43.1 us, 88% of copy; e4m3, 64 of up to 16384: 93.5 us, 89%; e4m3, one
-// of 131072, 4 query heads: 52.2 us, 79%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 27.4 us, 72%; NVFP4,
-// 128 of up to 8192: 133 us, 69% (bound by the instructions of decoding: 2.2 a cycle, half on the integer pipe).
+// sequences of up to 5000 tokens, 4 query heads: 43.3 us, 88% of copy; e4m3, 64 of up to 16384: 93.9 us, 88%; e4m3, one
+// of 131072, 4 query heads: 52.9 us, 78%; bf16, 33 with a window of 1024, 2 query heads of 256 dims: 27.4 us, 72%; NVFP4,
+// 128 of up to 8192: 133 us, 69% (710 instructions per 32 tokens and warp, 2.1 issued a cycle, the integer pipe busy half
+// of the time).  NVFP4 otherwise: heads of 64 dims 46%, 16 query heads 46 to 49%, 256 sequences of up to 600 tokens 35%.
 #pragma once
 #include <cuda_runtime.h>
 #include <math.h>
@@ -67,8 +70,9 @@ constexpr int KA_MOST = 32 * KA_GROUP;  // CTAs, so that a join has 32 parts at 
 constexpr float KA_NONE = -3.0e38f;  // the running maximum of no token
 
 // 16-token blocks per chunk and unit of the list: two where a chunk's ring steps leave room for three of them (NVFP4 with
-// one: 205 us instead of 187, the copies' bookkeeping); resident CTAs per SM: what the registers allow without spills to
-// speak of (NVFP4 with two 207, four 206, three 192; bf16 58, 53, 47).
+// one: 154 us instead of 133, the copies' bookkeeping); resident CTAs per SM: what the registers allow without spills
+// (the batches above with two, three and four, which spill: NVFP4 147, 133, 155 us; bf16 45.4, 43.4, 49.9; e4m3 93.6,
+// 94.0, 97.7).
 __host__ __device__ constexpr int ka_blocks(int kind, int dim) {
   return kind == HQ_KV_NVFP4 ? (dim == 256 ? 1 : 2) : (kind == HQ_KV_E4M3 && dim == 64 ? 2 : 1);
 }
@@ -617,7 +621,8 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
     kg = *a.kv.k_global;
     vg = *a.kv.v_global;
   }
-  const float cap = a.softcap * 1.4426950408889634f, per_cap = fminf(1.0f / cap, 3.4e38f);  // (a subnormal cap's is infinite)
+  const float cap = a.softcap * 1.4426950408889634f;
+  const float per_cap = fminf(1.0f / cap, 3.4e38f);  // (a subnormal cap's is infinite)
 
   // ---- one pair after another
   for (; !at.done(); at.next(a, hrs)) {

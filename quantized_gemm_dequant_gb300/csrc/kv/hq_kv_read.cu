@@ -4,7 +4,10 @@
 // of all heads: the rows are one contiguous stretch of the output, and in the cache each head's rows are contiguous
 // as far as the tokens share a page.  16 threads first find their row's sequence (binary search in `starts`) and its
 // place in the pools; then every thread converts 8 dims at a time.  Measured on a GB300: e4m3, 9 sequences of up to 16000
-// tokens, 8 heads of 128 dims: 78.2 us, 90% of the measured copy bandwidth; NVFP4, one of 50001: 44.3 us, 88%.
+// tokens, 8 heads of 128 dims: 78.5 us, 90% of the measured copy bandwidth; NVFP4, one of 50001: 44.5 us, 88%.  With few
+// heads a CTA has little to load behind its chain of lookups (one head of 64 dims: 128 pieces for 256 threads): 16 of up
+// to 16384 tokens, one head of 64 dims bf16 14.8 us, 75%, e4m3 18.7, 45%, NVFP4 16.3, 43%; one of 128 dims 96%, 69%,
+// 63%; two of 128 dims 93%, 80%, 80%.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -2,8 +2,8 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin),   then one rounding:
 //   bf16; e4m3 of y / s with s = absmax / 448; or e2m1 of y / d with d = e4m3(absmax_16 / (6 g)) * g.
-// All steps are fp32; the divisions that decide a code give what IEEE divisions give, overflow included: most are products
-// with a reciprocal and their correction.
+// All steps are fp32; the divisions that decide a code give what IEEE divisions give, overflow included: most are
+// products with a reciprocal and their correction.
 //
 // Memory-bound: every element is read once and written once, and the instructions per element decide whether that is
 // reached.  A CTA takes one token; its four warps take every fourth step of 256 / D heads of one kind (query, key or
@@ -13,8 +13,11 @@
 // row.  For a rotation by halves a lane holds four dims of the first half and their four partners, so that the rotation
 // needs no exchange between lanes and a lane's four angles serve both; otherwise it holds eight neighbouring dims.  Sums
 // of squares and largest magnitudes are shuffles inside the head's lanes.
-// Measured on a GB300, 8192 tokens of 32 query and 8 key-value heads of 128 dims into e4m3: 38.0 us, 74% of the measured
-// copy bandwidth (a warp per token and two heads: 160; without the next token on its way: 47).
+// Measured on a GB300, 8192 tokens of 32 query and 8 key-value heads of 128 dims into e4m3: 38.4 us, 73% of the measured
+// copy bandwidth (a warp per token and two heads: 160; without the next token on its way: 47); bf16 36.7, 83%; NVFP4 41,
+// 66%.  Fewer heads leave it further off: 16 / 4 of 128 dims, 9029 tokens NVFP4 29.2 us, 51%; 14 / 2 of 64, 20000 tokens
+// bf16 33, 44%; 8 / 1 of 128, 20000 tokens e4m3 41, 39%.  The four CTAs of an SM have one more token each on its way:
+// 48, 24, 9 and 10 KB for 32 / 8, 16 / 4, 14 / 2 and 8 / 1 heads, where 44 GB/s an SM over about 1 us of latency take 44.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -183,8 +186,8 @@ struct Token {
 constexpr int KW_STEPS = 4;  // query steps of a warp that are kept in registers, at most
 
 // STEPS: query steps of a warp that are kept in registers, 1, 2 or KW_STEPS.  A step without heads costs its instructions
-// all the same (with KW_STEPS alone: 16 / 4 heads of 128 dims, 9029 tokens NVFP4 35.1 us, so 27.5, with the check of its range 28.9; 8 / 1 heads, 20000
-// tokens e4m3 63 and 41).  Five CTAs per SM where one step leaves the registers are no faster.
+// all the same (with KW_STEPS alone: 16 / 4 heads of 128 dims, 9029 tokens NVFP4 35.1 us, where this was 27.5; 8 / 1 heads,
+// 20000 tokens e4m3 63 and 41).  Five CTAs per SM where one step leaves the registers are no faster.
 // MORE: a warp has at least two query steps beyond those that its registers hold; they are loaded as many at a time (56
 // heads of 256 dims: 243 us one by one, 194 so).  With one beyond them it is loaded on its own: the batch's registers
 // cost 32 heads of 128 dims 38.4 us -> 40.2.

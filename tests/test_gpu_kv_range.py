@@ -195,8 +195,8 @@ def test_a_sink_without_values(lib, kind, above, at):
 @pytest.mark.parametrize("power", [10, 18, 24, 28])
 def test_queries_with_one_huge_element(lib, kind, power):
     """One dim of the queries is 2^power, the keys hold zeros there: the scores come from the other dims, in full.  The
-    others are multiples of 2^-8, so that none needs more than f16's bits at the row's scale; the matrix unit aligns the products of a step to the largest exponent,
-    where a zero key may count as f16's smallest normal: 2^-23 of that for each of the dims."""
+    others are multiples of 2^-8, so that none needs more than f16's bits at the row's scale; the matrix unit aligns a step's products to the largest exponent, where
+    a zero key may count as f16's smallest normal: 2^-23 of that for each of the dims."""
     lens, D = [300, 33], 64
     table, pages = K.tables(lens, 16)
     c = lib.make_kv_cache(kind, pages, 16, 2, D, k_amax=168.0, v_amax=168.0)
