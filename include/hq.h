@@ -434,7 +434,7 @@ typedef struct {
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
  * A sequence of length 0 gives out = 0 and lse = -inf.  Places that are not seen may hold anything.
  * Scores, their running maximum and sum, and the weighted sums are fp32; the weights exp(s_j - max) multiply a bf16
- * cache's values as the sum of two bf16 numbers (16 bits), those of the 8- and 4-bit caches (times the value scale for
+ * cache's values as the sum of two bf16 numbers (15 bits), those of the 8- and 4-bit caches (times the value scale for
  * E4M3) rounded to f16, where what is under 2^-21 of the largest loses bits and what is under 2^-32 counts as zero.
  * E4M3 scales are not negative; a value scale under 2^-126 counts as zero.  A length outside its range is taken as the
  * nearest end of it, and tokens on a page outside the pools are left out; both record HQ_ERR_INVALID_ARG.

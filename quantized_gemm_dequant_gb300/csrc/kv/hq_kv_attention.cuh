@@ -36,9 +36,9 @@
 //    steady state has no shuffles and o is seldom rescaled; weights up to 2^8 fit the 16-bit types.  f16's are 2^7 times
 //    that (what stands for the maximum is 7 less): they keep their bits down to 2^-21 of the largest and vanish under
 //    2^-32 of it, beside a token that holds nearly all of the weight (l has them in fp32).  bf16 has 8 bits: a weight
-//    is two of them, its rounding and the rest, and the values are multiplied by both, which costs a kernel that waits
-//    for memory nothing (24 ragged sequences: 43.1 us with one, 43.0 with two).  f16's 11 bits are one: what they round
-//    off is an eighth of the output's own rounding.
+//    is the sum of two of them, 15 bits, and the values are multiplied by both, which costs a kernel that waits for
+//    memory nothing (24 ragged sequences: 43.1 us with one, 43.0 with two).  f16's 11 bits are one: what they round off
+//    is an eighth of the output's own rounding.
 //
 // Measured on a GB300 (6.69 TB/s measured copy), 8 query heads of 128 dims per key-value head unless said: bf16, 24
 // sequences of up to 5000 tokens, 4 query heads: 43.3 us, 88% of copy; e4m3, 64 of up to 16384: 93.9 us, 88%; e4m3, one
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
             for (int j = 0; j < KS; ++j) o[j][x][k] *= f, o[j][x][k + 2] *= f;
           }
       }
-      uint32_t pb[TB][NT][2], pr[BF ? TB : 1][BF ? NT : 1][2];  // pr: what bf16 rounds off
+      uint32_t pb[TB][NT][2], pr[BF ? TB : 1][BF ? NT : 1][2];  // pr: the weights' second part
 #pragma unroll
       for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -907,7 +907,9 @@ __global__ void __launch_bounds__(KA_THREADS, KaCfg<KIND, D, NT>::CTAS)
               l[x][k] += e;
               w[k] = C::OD ? ex2(y + (vl[t][i] - od[C::OD ? x : 0][k])) : e;
             }
-            const uint32_t p = BF ? pack_bf16x2(w[0], w[1]) : pack_f16x2(w[0], w[1]);
+            // bf16's first part is of a weight 2^-8 smaller, and so below it: the rest is positive, between 2^-16 and
+            // 2^-7 of the weight, and an infinite value stays that
+            const uint32_t p = BF ? pack_bf16x2(w[0] * 0.99609375f, w[1] * 0.99609375f) : pack_f16x2(w[0], w[1]);
             pb[t][x][i] = turn8x8(p);
             if constexpr (BF) pr[t][x][i] = turn8x8(pack_bf16x2(w[0] - bf16_lo(p), w[1] - bf16_hi(p)));
           }

@@ -164,7 +164,7 @@ def test_value_scales_rise_and_fall(lib, n, heads, group, D, low, high):
 @pytest.mark.parametrize("at", [0, 500])
 def test_a_sink_without_values(lib, kind, above, at):
     """One token holds nearly all of the weight, `above` nats over the others, and has values of zero: the output is
-    what the others bring.  Their weights are rounded to the 16-bit type: bf16 (in two parts) to 2^-16 of each; f16 to
+    what the others bring.  Their weights are rounded to the 16-bit type: bf16 (in two parts) to 2^-15 of each; f16 to
     2^-11 of each, or, scaled so that the largest is 2^7 at least, to 2^-32 of the largest where that is more."""
     n, D, page = 512, 64, 16
     c = lib.make_kv_cache(kind, n // page, page, 1, D, k_amax=2688.0, v_amax=2688.0)
@@ -184,7 +184,7 @@ def test_a_sink_without_values(lib, kind, above, at):
     want = np.full(D, 6 * (n - 1) * w / z)
     if kind == "e4m3":
         want[1] = 6.0
-    u, sub = (2.0 ** -16, 0.0) if kind == "bf16" else (2.0 ** -11, 2.0 ** -32)
+    u, sub = (2.0 ** -15, 0.0) if kind == "bf16" else (2.0 ** -11, 2.0 ** -32)
     # the scores' error: above 2^-21 from the product with log2 e and exp2's argument; exp2 and sums 2^-18
     bound = 2.0 ** -8 * want + (u + 2 * above * 2.0 ** -21 + 2.0 ** -18) * want + sub * 6 * (n - 1) / z
     assert np.all(np.abs(K.f64(out)[0, 0] - want) <= bound)
@@ -220,9 +220,9 @@ def test_queries_with_one_huge_element(lib, kind, power):
 
 
 @pytest.mark.parametrize("D,heads,group", [(64, 2, 4), (128, 1, 16), (128, 2, 3), (256, 1, 8), (256, 1, 12)])
-def test_bf16_weights_keep_16_bits(lib, D, heads, group):
-    """The weights enter a bf16 cache's products as two bf16 numbers, within 2^-16 of themselves: where values cancel in
-    the output, nothing else is left to err than the scores, exp2 and the sums."""
+def test_bf16_weights_keep_15_bits(lib, D, heads, group):
+    """The weights enter a bf16 cache's products as two bf16 numbers, within 2^-15 of themselves (the second is 2^-7 of a
+    weight at most): where values cancel in the output, nothing else is left to err than the scores, exp2 and the sums."""
     lens, page = [64, 300, 2000], 16
     table, pages = K.tables(lens, page)
     c = lib.make_kv_cache("bf16", pages, page, heads, D)
@@ -240,5 +240,30 @@ def test_bf16_weights_keep_16_bits(lib, D, heads, group):
             ds = 2 * D * 2.0 ** -24 * np.max(np.abs(kk) @ np.abs(qq)) * D ** -0.5 + np.abs(s).max() * 2.0 ** -21
             e = np.exp(s - s.max())
             want = e @ vv / e.sum()
-            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * ds + 2.0 ** -18) * (e @ np.abs(vv)) / e.sum()
+            bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -15 + 2 * ds + 2.0 ** -18) * (e @ np.abs(vv)) / e.sum()
             assert np.all(np.abs(K.f64(out)[b, h] - want) <= bound)
+
+
+@pytest.mark.parametrize("D,group,n", [(64, 4, 40), (128, 16, 300), (256, 8, 20000)])
+def test_infinite_bf16_values_stay_infinite(lib, D, group, n):
+    """An infinite value in a seen place makes its dim of its heads' outputs infinite with its sign; opposite ones in one
+    dim make it NaN.  The other dims and the other head are as without them."""
+    heads, page = 2, 16
+    table, pages = K.tables([n], page)
+    c = lib.make_kv_cache("bf16", pages, page, heads, D)
+    K.fill(c, 61)
+    q = (0.1 * torch.randn(1, heads * group, D, generator=torch.Generator().manual_seed(62))).to(torch.bfloat16)
+    at = lambda j: (int(table[0, j // page]), 0, j % page)  # noqa: E731
+    args = (q.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda())
+    was, _ = lib.paged_attention(c, *args)
+    inf = float("inf")
+    for j, dim, x in ((3, 5, inf), (n - 1, 6, -inf), (n // 2, 7, inf), (n // 2 + 1, 7, inf), (1, 9, inf), (n - 2, 9, -inf)):
+        c.v[(*at(j), dim)] = x
+    out, lse = lib.paged_attention(c, *args)
+    torch.cuda.synchronize()
+    got, want = out.cpu()[0], was.cpu()[0].clone()
+    want[:group, 5] = want[:group, 7] = inf
+    want[:group, 6] = -inf
+    want[:group, 9] = float("nan")
+    assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)) and torch.equal(got.isnan(), want.isnan())
+    assert torch.isfinite(lse).all()
