@@ -82,14 +82,15 @@ enum {
   HQ_W_UINT3_ZP = 10 /* q, z in [0, 7], value (q - z) * s, a 3-bit bit string, bf16 scale and zero per group */
 };
 /* Scale data types. */
-enum { HQ_S_BF16 = 1, HQ_S_UE4M3 = 2, HQ_S_UE8M0 = 3 };
+enum { HQ_S_BF16 = 1, HQ_S_UE4M3 = 2, HQ_S_UE8M0 = 3, HQ_S_F32 = 4 /* one per 128 x 128 block of the weights */ };
 /* Activation formats. */
 enum {
   HQ_A_BF16 = 1,       /* bf16 [M, K] */
   HQ_A_E4M3_TOKEN = 2, /* e4m3 [M, K] bytes + fp32 scale per row (token) */
   HQ_A_NVFP4 = 3,      /* e2m1 [M, K/2] packed + ue4m3 [M, K/16] + fp32 global scale [1] */
   HQ_A_MXFP8 = 4,      /* e4m3 [M, K] bytes + e8m0 [M, K/32] block scales (OCP Microscaling MXFP8) */
-  HQ_A_MXFP4 = 5       /* e2m1 [M, K/2] packed (low nibble = even k) + e8m0 [M, K/32] (OCP Microscaling MXFP4) */
+  HQ_A_MXFP4 = 5,      /* e2m1 [M, K/2] packed (low nibble = even k) + e8m0 [M, K/32] (OCP Microscaling MXFP4) */
+  HQ_A_E4M3_BLOCK = 6  /* e4m3 [M, K] bytes + fp32 scales [M, K/128], one per 128 elements of a row */
 };
 
 /* The unified quantization description ("standard format").  Supported
@@ -104,12 +105,15 @@ enum {
  *   E4M3,     group 128, BF16 scales,  no zero, no global, act BF16
  *   UINT1_ZP, group 128, BF16 scales,  zero,    no global, act BF16
  *   UINT3_ZP, group 128, BF16 scales,  zero,    no global, act BF16
- * The last six are the other WnA16 widths and formats of "Results: kernel
+ *   E4M3,     group 128, F32 scales,   no zero, no global, act E4M3_BLOCK, one expert (hq_gemm only: no MoE form)
+ * The six before the last are the other WnA16 widths and formats of "Results: kernel
  * microbenchmarks" (INT1, INT2, INT3 as GPTQ-style unsigned codes with integer
  * zero points, INT8 as the zero-exponent e0m7 of "Results: quantization
  * support", MXINT4, FP8); MXFP8 and MXFP4 activations are the microscaled
  * W4A8 and W4A4 variants of "W8A8 / W4A8 / W4A4" (both need K a multiple
- * of 512).  Anything else returns HQ_ERR_UNSUPPORTED. */
+ * of 512).  The last is the W8A8 product with one fp32 scale per 128 x 128
+ * block of the weights and per 128 elements of an activation row.  Anything
+ * else returns HQ_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t weight_type;      /* HQ_W_* */
   int32_t group_size;       /* K elements per scale */
@@ -123,8 +127,8 @@ typedef struct {
 } hq_format_t;
 
 /* Activation operand.  data: see HQ_A_*; scale: fp32 [M] for E4M3_TOKEN,
- * ue4m3 [M, K/16] for NVFP4, e8m0 [M, K/32] for MXFP8 and MXFP4, NULL for
- * BF16; global_scale: fp32 [1] for NVFP4. */
+ * ue4m3 [M, K/16] for NVFP4, e8m0 [M, K/32] for MXFP8 and MXFP4, fp32
+ * [M, K/128] for E4M3_BLOCK, NULL for BF16; global_scale: fp32 [1] for NVFP4. */
 typedef struct {
   const void* data;
   const void* scale;
@@ -145,7 +149,8 @@ HQ_API size_t hq_packed_bytes(const hq_format_t* fmt);
  *                hold its k = 4b + i) or [E][N][K*b/8] (UINT1_ZP b = 1, UINT3_ZP b = 3:
  *                a little-endian bit string, bit j of code k at bit position k*b + j
  *                of the row, position p being bit p % 8 of byte p / 8)
- *   scales       [E][N][K/group] of scale_type (bf16 as 16-bit patterns, ue4m3/e8m0 bytes)
+ *   scales       [E][N][K/group] of scale_type (bf16 as 16-bit patterns, ue4m3/e8m0 bytes); F32: fp32
+ *                [ceil(N/128)][K/128], one per 128 x 128 block
  *   zeros        uint8 [E][N][K/group], values 0..2^b - 1 for the b-bit zero-point formats
  *                (UINT4_ZP, UINT3_ZP, UINT2_ZP, UINT1_ZP), else NULL
  *   global_scale fp32 [E] (NVFP4), else NULL
@@ -197,7 +202,10 @@ HQ_API hq_status_t hq_workspace_init(void* workspace, size_t bytes, hq_stream_t 
  *   bias    bf16 [N] or NULL
  * Output scaling: NVFP4 multiplies by A.global_scale * W global scale,
  * E4M3_TOKEN by the row's token scale.  M may be 0 (no work).  Accumulation is
- * fp32; C is rounded to nearest-even bf16. */
+ * fp32; C is rounded to nearest-even bf16.
+ * E4M3 weights with F32 scales: C[m, n] = bias[n] + sum_b s(A)[m, b] * s(W)[n / 128, b] * sum_{k in block b} A[m, k] *
+ * W[n, k]; every 128-K block is summed by itself and added, times its scale, in fp32, in an order that does not depend
+ * on timing.  The workspace holds the status header alone; A's scales and C are 16-byte aligned. */
 HQ_API hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packedW, const void* bias, void* C,
                     int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes, hq_stream_t stream);
 
@@ -245,6 +253,42 @@ HQ_API hq_status_t hq_moe_gemm_combine(const hq_format_t* fmt, const hq_act_t* A
  * a multiple of 8 (HQ_ERR_ALIGNMENT); pointers 16-byte aligned. One kernel. */
 HQ_API hq_status_t hq_swiglu(const void* x, int64_t R, int64_t I, void* out, hq_stream_t stream);
 
+/* The same between a dense layer's two products, or an expert's, with an 8-bit output: y[r, c] = silu(x[r, c]) *
+ * x[r, I + c] in fp32, not rounded on the way, then scale = absmax / 448 of each row (HQ_A_E4M3_TOKEN: out_scale fp32
+ * [R]) or of each 128 of its elements (HQ_A_E4M3_BLOCK: out_scale fp32 [R, I/128]) and out_data = e4m3(y / scale),
+ * nearest even, [R, I].  A scale of zero has zero codes; a NaN or an infinity makes its scale NaN or infinite.
+ * I is a multiple of 16 and at most 32768 (TOKEN; HQ_ERR_UNSUPPORTED above) or a multiple of 128 (BLOCK); pointers
+ * 16-byte aligned.  R = 0 does nothing.  One kernel. */
+HQ_API hq_status_t hq_swiglu_quantize(int32_t act_type, const void* x, int64_t R, int64_t I, void* out_data,
+                                      void* out_scale, hq_stream_t stream);
+
+/* One hq_add_rms_norm call. */
+typedef struct {
+  int32_t act_type;  /* HQ_A_BF16, HQ_A_E4M3_TOKEN or HQ_A_E4M3_BLOCK: what out_data and out_scale hold */
+  float eps;         /* >= 0 */
+  int64_t T;         /* rows, >= 0 */
+  int64_t K;         /* elements of a row, at most 32768; a multiple of 8 (BF16), 16 (TOKEN) or 128 (BLOCK) */
+  const void* x;     /* bf16 [T] rows of K */
+  int64_t x_stride;  /* elements from one row to the next, a multiple of 8, at least K */
+  const void* residual; /* bf16 [T] rows of K, or NULL: no addition */
+  int64_t residual_stride;
+  const void* weight;   /* bf16 [K] */
+  void* residual_out;   /* bf16 [T] rows of K; NULL exactly when residual is.  May be residual or x itself (same stride) */
+  int64_t residual_out_stride;
+  void* out_data;    /* bf16 [T][K], or e4m3 [T][K] */
+  void* out_scale;   /* fp32 [T] (TOKEN) or [T][K/128] (BLOCK); not used for BF16 */
+} hq_norm_t;
+
+/* What stands before a layer's projections: a sublayer's output added to the residual stream, the sum's RMS norm, and
+ * its quantisation as the next product's activations.  Per row, in fp32:
+ *   r = x + residual,  residual_out = bf16(r),  y = r / sqrt(mean(r^2) + eps) * weight
+ * y takes the sum as it is, before its rounding to bf16, and is rounded once: to bf16, or to e4m3 codes whose scale is
+ * absmax / 448 of the row or of each 128 elements, as hq_quantize_act makes them from bf16 rows.  Sums of squares that
+ * leave fp32's range are taken again with the row scaled.  A NaN or an infinity in r makes the row's values NaN.
+ * The strides of residual and residual_out are read only where residual is given.  Pointers 16-byte aligned; outputs
+ * must not overlap anything else that the call reads.  One kernel, no workspace. */
+HQ_API hq_status_t hq_add_rms_norm(const hq_norm_t* args, hq_stream_t stream);
+
 /* Copy the device status word out of `workspace` (synchronizes `stream`) and
  * clear it.  *status_out receives HQ_OK or the first device-detected error
  * (HQ_ERR_TIMEOUT, HQ_ERR_BAD_ROUTING); the return value reports only whether
@@ -289,7 +333,7 @@ HQ_API hq_status_t hq_gemm_static_scratch(const hq_format_t* fmt, const hq_act_t
                                           const void* bias, void* C, int64_t M, int64_t N, int64_t K,
                                           hq_stream_t stream);
 
-/* Activation quantization: bf16 activations -> the E4M3_TOKEN or NVFP4 operand
+/* Activation quantization: bf16 activations -> the E4M3_TOKEN, E4M3_BLOCK or NVFP4 operand
  * of hq_gemm / hq_moe_gemm.  The deployment picks a layer's activation type
  * ("Selecting activation types"): token-wise FP8 for W4A8 ("End-to-end
  * inference performance"), NVFP4 for W4A4 ("W8A8 / W4A8 / W4A4").  Scales map
@@ -298,18 +342,19 @@ HQ_API hq_status_t hq_gemm_static_scratch(const hq_format_t* fmt, const hq_act_t
  * even, saturating:
  *   E4M3_TOKEN  s[m] = absmax(x[m, :]) / 448, data = e4m3(x / s[m]); a zero
  *               row gets s = 0 and zero codes.  An e4m3 zero keeps its sign.
+ *   E4M3_BLOCK  the same for each 128 elements of a row: s[m, b], b = k / 128
  *   NVFP4       g = amax / (6 * 448), amax = the tensor's largest magnitude or
  *               the calibrated *global_amax; per 16 elements of a row
  *               sb = e4m3(amax_b / (6 * g)), d = value(sb) * g,
  *               code = e2m1(x / d) (+0 for a zero result; d = 0: zero codes).
  * Arguments (device pointers, 16-byte aligned, caller-owned):
- *   act_type     HQ_A_E4M3_TOKEN or HQ_A_NVFP4 (else HQ_ERR_UNSUPPORTED)
- *   x            bf16 [M, K] row-major; K a multiple of 16 (else HQ_ERR_ALIGNMENT), M >= 0
+ *   act_type     HQ_A_E4M3_TOKEN, HQ_A_E4M3_BLOCK or HQ_A_NVFP4 (else HQ_ERR_UNSUPPORTED)
+ *   x            bf16 [M, K] row-major; K a multiple of 16, E4M3_BLOCK 128 (else HQ_ERR_ALIGNMENT), M >= 0
  *   global_amax  NVFP4: fp32 [1] calibrated largest magnitude, or NULL to take
- *                the tensor's own (one more kernel reads x first); ignored for E4M3_TOKEN
- *   out_data     E4M3_TOKEN: e4m3 [M, K]; NVFP4: e2m1 [M, K/2], low nibble = even k
- *   out_scale    E4M3_TOKEN: fp32 [M]; NVFP4: ue4m3 [M, K/16]
- *   out_global   NVFP4: fp32 [1] receives g; may be NULL for E4M3_TOKEN
+ *                the tensor's own (one more kernel reads x first); ignored for E4M3_TOKEN and E4M3_BLOCK
+ *   out_data     E4M3_TOKEN, E4M3_BLOCK: e4m3 [M, K]; NVFP4: e2m1 [M, K/2], low nibble = even k
+ *   out_scale    E4M3_TOKEN: fp32 [M]; E4M3_BLOCK: fp32 [M, K/128]; NVFP4: ue4m3 [M, K/16]
+ *   out_global   NVFP4: fp32 [1] receives g; may be NULL for E4M3_TOKEN and E4M3_BLOCK
  *   workspace    NVFP4 without global_amax: hq_quantize_act_workspace_bytes()
  *                bytes (HQ_ERR_WORKSPACE if smaller), no initialisation
  *                needed; otherwise may be NULL

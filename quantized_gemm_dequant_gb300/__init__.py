@@ -29,15 +29,16 @@ HQ_OK, HQ_ERR_INVALID_ARG, HQ_ERR_UNSUPPORTED, HQ_ERR_ALIGNMENT, HQ_ERR_CUDA, HQ
     HQ_ERR_BAD_ROUTING, HQ_ERR_WORKSPACE, HQ_ERR_BOUNDS = range(9)
 HQ_W_INT4_SYM, HQ_W_UINT4_ZP, HQ_W_NVFP4, HQ_W_MXFP4 = 1, 2, 3, 4
 HQ_W_INT8_SYM, HQ_W_UINT2_ZP, HQ_W_MXINT4, HQ_W_E4M3, HQ_W_UINT1_ZP, HQ_W_UINT3_ZP = 5, 6, 7, 8, 9, 10
-HQ_S_BF16, HQ_S_UE4M3, HQ_S_UE8M0 = 1, 2, 3
-HQ_A_BF16, HQ_A_E4M3_TOKEN, HQ_A_NVFP4, HQ_A_MXFP8, HQ_A_MXFP4 = 1, 2, 3, 4, 5
+HQ_S_BF16, HQ_S_UE4M3, HQ_S_UE8M0, HQ_S_F32 = 1, 2, 3, 4
+HQ_A_BF16, HQ_A_E4M3_TOKEN, HQ_A_NVFP4, HQ_A_MXFP8, HQ_A_MXFP4, HQ_A_E4M3_BLOCK = 1, 2, 3, 4, 5, 6
 HQ_KV_BF16, HQ_KV_E4M3, HQ_KV_NVFP4 = 1, 2, 3
 
 EXPORTS = ["hq_packed_bytes", "hq_pack_weights", "hq_unpack_weights", "hq_workspace_bytes", "hq_workspace_init",
            "hq_gemm", "hq_moe_gemm", "hq_last_device_status", "hq_status_string", "hq_gemm_static_scratch",
            "hq_kernels_per_call", "hq_launch_plan", "hq_quantize_act_workspace_bytes", "hq_quantize_act",
            "hq_moe_combine_workspace_bytes", "hq_moe_gemm_combine", "hq_swiglu", "hq_set_wait_limit_ns",
-           "hq_kv_workspace_bytes", "hq_kv_write", "hq_kv_read", "hq_paged_attention"]
+           "hq_kv_workspace_bytes", "hq_kv_write", "hq_kv_read", "hq_paged_attention",
+           "hq_swiglu_quantize", "hq_add_rms_norm"]
 
 
 class Format(ctypes.Structure):
@@ -81,6 +82,13 @@ class KVRead(ctypes.Structure):
                 ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
 
 
+class Norm(ctypes.Structure):
+    _fields_ = [("act_type", ctypes.c_int32), ("eps", ctypes.c_float), ("T", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_int64), ("out_data", ctypes.c_void_p), ("out_scale", ctypes.c_void_p)]
+
+
 def _layout(s):
     """The fields of a structure, which a call packs in one step instead of setting them one by one."""
     code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
@@ -88,6 +96,7 @@ def _layout(s):
 
 
 _KV_ROWS, _KV_READ, _KV_ATTENTION = _layout(KVRows), _layout(KVRead), _layout(KVAttention)
+_NORM = _layout(Norm)
 
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -136,6 +145,10 @@ _lib.hq_kv_read.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_kv_read.restype = ctypes.c_int
 _lib.hq_paged_attention.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
 _lib.hq_paged_attention.restype = ctypes.c_int
+_lib.hq_swiglu_quantize.argtypes = [_i32, _vp, _i64, _i64, _vp, _vp, _vp]
+_lib.hq_swiglu_quantize.restype = ctypes.c_int
+_lib.hq_add_rms_norm.argtypes = [_vp, _vp]
+_lib.hq_add_rms_norm.restype = ctypes.c_int
 _lib.hq_status_string.argtypes = [ctypes.c_int]
 _lib.hq_status_string.restype = ctypes.c_char_p
 
@@ -147,10 +160,11 @@ _WEIGHT = {"int4_sym": (HQ_W_INT4_SYM, 128, HQ_S_BF16, 0, 0, HQ_A_BF16),
            "uint2_zp": (HQ_W_UINT2_ZP, 128, HQ_S_BF16, 1, 0, HQ_A_BF16),
            "mxint4": (HQ_W_MXINT4, 32, HQ_S_UE8M0, 0, 0, HQ_A_BF16),
            "e4m3": (HQ_W_E4M3, 128, HQ_S_BF16, 0, 0, HQ_A_BF16),
+           "e4m3_block": (HQ_W_E4M3, 128, HQ_S_F32, 0, 0, HQ_A_E4M3_BLOCK),
            "uint1_zp": (HQ_W_UINT1_ZP, 128, HQ_S_BF16, 1, 0, HQ_A_BF16),
            "uint3_zp": (HQ_W_UINT3_ZP, 128, HQ_S_BF16, 1, 0, HQ_A_BF16)}
 _ACT_FMT = {"bf16": HQ_A_BF16, "e4m3_tok": HQ_A_E4M3_TOKEN, "nvfp4": HQ_A_NVFP4, "mxfp8": HQ_A_MXFP8,
-            "mxfp4": HQ_A_MXFP4}
+            "mxfp4": HQ_A_MXFP4, "e4m3_block": HQ_A_E4M3_BLOCK}
 
 
 class HQError(RuntimeError):
@@ -181,7 +195,7 @@ def _check(code, where):
 # bits of one weight code and bytes of one scale, per format code (the layouts of hq_pack_weights' inputs)
 _CODE_BITS = {HQ_W_INT4_SYM: 4, HQ_W_UINT4_ZP: 4, HQ_W_NVFP4: 4, HQ_W_MXFP4: 4, HQ_W_INT8_SYM: 8, HQ_W_UINT2_ZP: 2,
               HQ_W_MXINT4: 4, HQ_W_E4M3: 8, HQ_W_UINT1_ZP: 1, HQ_W_UINT3_ZP: 3}
-_SCALE_BYTES = {HQ_S_BF16: 2, HQ_S_UE4M3: 1, HQ_S_UE8M0: 1}
+_SCALE_BYTES = {HQ_S_BF16: 2, HQ_S_UE4M3: 1, HQ_S_UE8M0: 1, HQ_S_F32: 4}
 _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
@@ -217,13 +231,16 @@ class _Args:
         """The activation operand of `rows` rows of K in fmt.act_type: data, per-row or block scales, NVFP4 global
         scale, each against the bytes the call reads."""
         K, at = fmt.K, fmt.act_type
-        row = {HQ_A_BF16: 2 * K, HQ_A_E4M3_TOKEN: K, HQ_A_MXFP8: K, HQ_A_NVFP4: K // 2, HQ_A_MXFP4: K // 2}.get(at, 0)
-        srow = {HQ_A_E4M3_TOKEN: 4, HQ_A_NVFP4: K // 16, HQ_A_MXFP8: K // 32, HQ_A_MXFP4: K // 32}.get(at, 0)
+        row = {HQ_A_BF16: 2 * K, HQ_A_E4M3_TOKEN: K, HQ_A_MXFP8: K, HQ_A_NVFP4: K // 2, HQ_A_MXFP4: K // 2,
+               HQ_A_E4M3_BLOCK: K}.get(at, 0)
+        srow = {HQ_A_E4M3_TOKEN: 4, HQ_A_NVFP4: K // 16, HQ_A_MXFP8: K // 32, HQ_A_MXFP4: K // 32,
+                HQ_A_E4M3_BLOCK: 4 * (K // 128)}.get(at, 0)
         if not isinstance(a, dict) or "data" not in a:
             raise HQArgError(self.where, "act must be a dict with 'data' (and 'scale', 'gscale' where the format "
                                          "has them)")
         self.add(a["data"], "act['data']", rows * row, _BF16 if at == HQ_A_BF16 else None)
-        self.add(a.get("scale"), "act['scale']", rows * srow, _F32 if at == HQ_A_E4M3_TOKEN else None)
+        self.add(a.get("scale"), "act['scale']", rows * srow,
+                 _F32 if at in (HQ_A_E4M3_TOKEN, HQ_A_E4M3_BLOCK) else None)
         return self.add(a.get("gscale"), "act['gscale']", 4 if at == HQ_A_NVFP4 else 0, _F32)
 
     def ptrs(self):
@@ -300,7 +317,10 @@ def _standard(fmt, codes, scales, zeros, global_scale, where, args=None):
     rows = fmt.num_experts * fmt.N
     groups = fmt.K // fmt.group_size if fmt.group_size > 0 else 0
     args.add(codes, "codes", rows * (fmt.K * _CODE_BITS.get(fmt.weight_type, 0) // 8))
-    args.add(scales, "scales", rows * groups * _SCALE_BYTES.get(fmt.scale_type, 0))
+    if fmt.scale_type == HQ_S_F32:  # one per 128 x 128 block
+        args.add(scales, "scales", 4 * fmt.num_experts * -(-fmt.N // 128) * groups, _F32)
+    else:
+        args.add(scales, "scales", rows * groups * _SCALE_BYTES.get(fmt.scale_type, 0))
     args.add(zeros, "zeros", rows * groups if fmt.has_zero else 0)
     return args.add(global_scale, "global_scale", 4 * fmt.num_experts if fmt.has_global_scale else 0, _F32)
 
@@ -468,7 +488,7 @@ def pack_inputs(inputs, device="cuda", stream=None):
     return fmt, packed
 
 
-_ACT_TYPE = {"e4m3_tok": HQ_A_E4M3_TOKEN, "nvfp4": HQ_A_NVFP4}
+_ACT_TYPE = {"e4m3_tok": HQ_A_E4M3_TOKEN, "nvfp4": HQ_A_NVFP4, "e4m3_block": HQ_A_E4M3_BLOCK}
 
 
 def quantize_act_workspace_bytes(afmt, M, K):
@@ -477,7 +497,8 @@ def quantize_act_workspace_bytes(afmt, M, K):
 
 def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=None):
     """bf16 activations x [M, K] (cuda) -> the activation operand dict of `gemm` / `moe_gemm`:
-    'e4m3_tok': {data e4m3 bytes [M, K], scale fp32 [M]}; 'nvfp4': {data packed e2m1 [M, K/2], scale ue4m3 [M, K/16],
+    'e4m3_tok': {data e4m3 bytes [M, K], scale fp32 [M]}; 'e4m3_block': {data e4m3 bytes [M, K], scale fp32 [M, K/128]};
+    'nvfp4': {data packed e2m1 [M, K/2], scale ue4m3 [M, K/16],
     gscale fp32 [1]}.  `global_amax` (NVFP4): fp32 tensor [1] with a calibrated largest magnitude, else the tensor's
     own.  `out` (same dict layout) receives the result when given."""
     w = "hq_quantize_act"
@@ -489,13 +510,16 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
     args = _Args(w).add(x, "x", 2 * M * K, _BF16).add(global_amax, "global_amax", 4, _F32)
     if out is not None:
         args.add(out["data"], "out['data']", M * (K // 2) if nvfp4 else M * K)
-        args.add(out["scale"], "out['scale']", M * (K // 16) if nvfp4 else 4 * M, None if nvfp4 else _F32)
+        per = K // 128 if at == HQ_A_E4M3_BLOCK else 1
+        args.add(out["scale"], "out['scale']", M * (K // 16) if nvfp4 else 4 * M * per, None if nvfp4 else _F32)
         args.add(out.get("gscale"), "out['gscale']", 4 if nvfp4 else 0, _F32)
     args.add(workspace, "workspace")
     p = args.ptrs()
     dev = x.device
     if out is None:
-        if afmt == "e4m3_tok":
+        if afmt == "e4m3_block":
+            out = _new_act(at, M, K, dev, stream)
+        elif afmt == "e4m3_tok":
             out = dict(data=torch.empty((M, K), dtype=torch.uint8, device=dev),
                        scale=torch.empty((M,), dtype=torch.float32, device=dev))
         else:
@@ -513,6 +537,121 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     _check(_lib.hq_quantize_act(at, p[0], M, K, p[1], pd, ps, pg, pws, ws_bytes, _stream(stream)), w)
     return out
+
+
+def _new_act(at, rows, width, device, stream=None):
+    """An activation operand that a call fills: bf16 rows, or e4m3 codes with a scale per row or per 128 elements."""
+    if at == HQ_A_BF16:
+        return dict(data=_on(stream, torch.empty, (rows, width), dtype=torch.bfloat16, device=device))
+    shape = (rows, width // 128) if at == HQ_A_E4M3_BLOCK else (rows,)
+    return dict(data=_on(stream, torch.empty, (rows, width), dtype=torch.uint8, device=device),
+                scale=_on(stream, torch.empty, shape, dtype=torch.float32, device=device))
+
+
+def _act_items(w, at, out, rows, width):
+    """The tensors of an activation operand that a call writes, for _right_or_raise."""
+    if out is None:
+        return ()
+    if not isinstance(out, dict) or "data" not in out or (at != HQ_A_BF16 and out.get("scale") is None):
+        raise HQArgError(w, "out must be a dict with 'data' and, in 8 bits, 'scale'")
+    n = rows * width
+    if at == HQ_A_BF16:
+        return ((out["data"], "out['data']", n, _bf16),)
+    if isinstance(out["data"], torch.Tensor) and out["data"].element_size() != 1:
+        raise HQArgError(w, f"out['data'] has dtype {out['data'].dtype}; expected one byte per element")
+    return ((out["data"], "out['data']", n, None),
+            (out["scale"], "out['scale']", n // 128 if at == HQ_A_E4M3_BLOCK else rows, _f32))
+
+
+def _right_or_raise(w, items, dev):
+    """Checks the tensors of a call, items (tensor or None, name, elements, dtype or None for bytes): one look at each
+    right one; at the first that is not, all are judged and HQArgError is raised."""
+    for t, name, n, dt in items:
+        if t is not None and not (isinstance(t, torch.Tensor) and (dt is None or t.dtype is dt)
+                                  and t.get_device() == dev and t.is_contiguous() and t.numel() >= n):
+            args = _Args(w)
+            for t, name, n, dt in items:
+                args.add(t, name, n * (dt.itemsize if dt else 1), (dt,) if dt else None)
+            args.ptrs()
+            raise HQArgError(w, "the tensors are on different devices")
+
+
+def swiglu_quantize(afmt, x, out=None, stream=None):
+    """x bf16 [R, 2I] = [gate | up] -> silu(gate) * up as the activation operand of `gemm` / `moe_gemm`: 'e4m3_tok'
+    {data e4m3 bytes [R, I], scale fp32 [R]} (I up to 32768) or 'e4m3_block' {data, scale fp32 [R, I/128]}."""
+    w = "hq_swiglu_quantize"
+    at = _ACT_FMT.get(afmt)
+    if at not in (HQ_A_E4M3_TOKEN, HQ_A_E4M3_BLOCK):
+        raise HQArgError(w, f"afmt must be 'e4m3_tok' or 'e4m3_block', not {afmt!r}")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] % 2:
+        raise HQArgError(w, "x must be a 2-D [R, 2I] tensor")
+    R, I = x.shape[0], x.shape[1] // 2
+    dev = _device() if x.is_cuda else None  # (no tensor is on device None: host tensors are refused)
+    _right_or_raise(w, ((x, "x", 2 * R * I, _bf16), *_act_items(w, at, out, R, I)), dev)
+    if out is None:
+        out = _new_act(at, R, I, x.device, stream)
+    st = _lib.hq_swiglu_quantize(at, x.data_ptr(), R, I, out["data"].data_ptr(), out["scale"].data_ptr(),
+                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
+    return out
+
+
+def _rows_of(w, t, name, K):
+    """Row stride of a 2-D [T, K] tensor whose rows are contiguous and do not overlap, and a tensor to check in its
+    place (itself, or its first row where rows lie apart)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != K:
+        raise HQArgError(w, f"{name} must be a 2-D [T, {K}] tensor")
+    if t.shape[0] <= 1 or t.stride(0) == K:
+        return K, t
+    if t.stride(0) < K or (K > 1 and t.stride(1) != 1):
+        raise HQArgError(w, f"{name}'s rows must be contiguous and must not overlap")
+    return t.stride(0), t[0]
+
+
+def add_rms_norm(afmt, x, weight, residual=None, eps=1e-6, residual_out=None, out=None, stream=None):
+    """r = x + residual (fp32), y = r / sqrt(mean(r^2) + eps) * weight as the activation operand of `gemm` /
+    `moe_gemm`: 'bf16' {data bf16 [T, K]}, 'e4m3_tok' {data e4m3 bytes [T, K], scale fp32 [T]} or 'e4m3_block' {data,
+    scale fp32 [T, K/128]}.  x and residual are bf16 [T, K] whose rows may be strided, weight bf16 [K]; K at most 32768.
+    Returns (operand, residual_out), residual_out = bf16(r) [T, K]: a new tensor, or the one given, which may be
+    `residual` or x itself; None without a residual."""
+    w = "hq_add_rms_norm"
+    at = _ACT_FMT.get(afmt)
+    if at not in (HQ_A_BF16, HQ_A_E4M3_TOKEN, HQ_A_E4M3_BLOCK):
+        raise HQArgError(w, f"afmt must be 'bf16', 'e4m3_tok' or 'e4m3_block', not {afmt!r}")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise HQArgError(w, "x must be a 2-D [T, K] tensor")
+    T, K = x.shape
+    if weight is None:
+        raise HQArgError(w, "weight is required")
+    sx, x1 = _rows_of(w, x, "x", K)
+    items = [(x1, "x", x1.numel(), _bf16), (weight, "weight", K, _bf16)]
+    sr = so = K
+    if residual is None:
+        if residual_out is not None:
+            raise HQArgError(w, "residual_out needs a residual")
+    else:
+        sr, r1 = _rows_of(w, residual, "residual", K)
+        items.append((r1, "residual", r1.numel(), _bf16))
+        if residual_out is not None:
+            so, o1 = _rows_of(w, residual_out, "residual_out", K)
+            items.append((o1, "residual_out", o1.numel(), _bf16))
+        for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+            if t is not None and t.shape[0] != T:
+                raise HQArgError(w, f"{name} has {t.shape[0]} rows, x has {T}")
+    dev = _device() if x.is_cuda else None  # (no tensor is on device None: host tensors are refused)
+    _right_or_raise(w, (*items, *_act_items(w, at, out, T, K)), dev)
+    if out is None:
+        out = _new_act(at, T, K, x.device, stream)
+    if residual is not None and residual_out is None:
+        residual_out = _on(stream, torch.empty, (T, K), dtype=_bf16, device=x.device)
+    a = _kv_pack(w, _NORM, at, eps, T, K, x.data_ptr(), sx, 0 if residual is None else residual.data_ptr(), sr,
+                 weight.data_ptr(), 0 if residual is None else residual_out.data_ptr(), so, out["data"].data_ptr(),
+                 0 if at == HQ_A_BF16 else out["scale"].data_ptr())
+    st = _lib.hq_add_rms_norm(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
+    return out, residual_out
 
 
 # ----------------------------------------------------------------- paged key-value cache

@@ -22,28 +22,13 @@
 #include "hq_act_quant.h"
 #include "hq_launch.h"
 #include "hq_ptx.cuh"
+#include "hq_quant.cuh"
 
 namespace hq {
 
 namespace {
 
 constexpr int AQ_THREADS = 256;
-
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// two floats -> two e4m3 bytes (lo = a), round to nearest even, saturating
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
-  return d;
-}
 
 // eight floats -> one word of eight e2m1 codes (code i in nibble i), round to nearest even, saturating; the sign
 // of a zero code is kept here (see e2m1x8_clear_neg_zero)
@@ -72,32 +57,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
   uint32_t h;
   asm("{\n\t.reg .b16 t;\n\tmov.b16 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "h"((uint16_t)b));
   return __half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu)));
-}
-
-// x / y rounded to nearest even (IEEE binary32) from yi = RN(1 / y): q = RN(x * yi) is faithful, the residual
-// x - q * y is exact with one FMA, and RN(q + residual * yi) is the correctly rounded quotient (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  Valid
-// while the residual stays a normal number: the callers use it only when the scale is at least 2^-100 (every quotient
-// that can round to a nonzero code then has |x| >= 2^-110), and take the plain division otherwise.
-__device__ __forceinline__ float div_by(float x, float y, float yi) {
-  const float q = __fmul_rn(x, yi);
-  const float r = __fmaf_rn(-q, y, x);
-  return __fmaf_rn(r, yi, q);
-}
-constexpr float kDivMinScale = 7.8886091e-31f;  // 2^-100
-
-// largest bf16 magnitude of 8 values (4 words), as the 16-bit pattern: finite non-negative bf16 values order like
-// their bit patterns, so a SIMD unsigned max of the sign-cleared halves suffices
-__device__ __forceinline__ uint32_t bf16x8_absmax_bits(const uint4& v, uint32_t m) {
-  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
-  m = __vmaxu2(m, v.w & 0x7FFF7FFFu);
-  return m;
-}
-__device__ __forceinline__ float absmax_bits_to_f32(uint32_t m) {
-  const uint32_t h = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
-  return __uint_as_float(h << 16);
 }
 
 __device__ __forceinline__ float block_max(float v, float* red) {

@@ -12,6 +12,7 @@
 #include "hq_act_quant.h"
 #include "hq_gemm_kernel.cuh"
 #include "hq_layout.h"
+#include "hq_row_ops.h"
 #include "hq_tune.h"
 
 namespace hq {
@@ -26,6 +27,7 @@ cudaError_t launch_gemm_mxfp4a(const GemmArgs& a, int bt, int grid, cudaStream_t
 cudaError_t launch_gemm_mxfp4x(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_small(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_small_fmt(int dec, const GemmArgs& a, int bt, int grid, cudaStream_t stream);
+cudaError_t launch_gemm_block(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_splitk_reduce(int path, const GemmArgs& a, int bt, int gemm_grid, int grid, cudaStream_t stream);
 cudaError_t launch_combine_round(const float* acc, int64_t n, uint16_t* c, cudaStream_t stream);
 cudaError_t launch_swiglu(const void* x, int64_t R, int64_t I, void* out, cudaStream_t stream);
@@ -77,8 +79,16 @@ hq_status_t check_format(const hq_format_t* f) {
       // multiples
       if ((f->act_type == HQ_A_MXFP8 || f->act_type == HQ_A_MXFP4) && f->K % 512) return HQ_ERR_ALIGNMENT;
       break;
-    case HQ_W_INT8_SYM:
     case HQ_W_E4M3:
+      if (f->scale_type == HQ_S_F32 || f->act_type == HQ_A_E4M3_BLOCK) {  // scales per block of 128 on both operands
+        if (f->group_size != 128 || f->scale_type != HQ_S_F32 || f->has_zero || f->has_global_scale ||
+            f->act_type != HQ_A_E4M3_BLOCK || f->num_experts != 1)
+          return HQ_ERR_UNSUPPORTED;
+        if (f->K % 128) return HQ_ERR_ALIGNMENT;
+        break;
+      }
+      [[fallthrough]];
+    case HQ_W_INT8_SYM:
       if (f->group_size != 128 || f->scale_type != HQ_S_BF16 || f->has_zero || f->has_global_scale ||
           f->act_type != HQ_A_BF16)
         return HQ_ERR_UNSUPPORTED;
@@ -109,9 +119,14 @@ hq_status_t check_format(const hq_format_t* f) {
   return HQ_OK;
 }
 
+// E4M3 weights with fp32 scales per 128 x 128 block (validated descriptors only).
+bool block_scaled(const hq_format_t* f) { return f->act_type == HQ_A_E4M3_BLOCK; }
+
 // Packed layout of a descriptor: MXFP4 weights meant for MXFP4 activations are packed like NVFP4 (packed e2m1 in
-// the MMA, scales as tensor-memory words), every other format by its weight type.
+// the MMA, scales as tensor-memory words), E4M3 weights with block scales as the MMA reads them, every other format by
+// its weight type.
 int pack_kind(const hq_format_t* f) {
+  if (block_scaled(f)) return (int)WK_E4M3_BLOCK;
   return (f->weight_type == HQ_W_MXFP4 && f->act_type == HQ_A_MXFP4) ? (int)WK_MXFP4_X : f->weight_type;
 }
 
@@ -210,6 +225,18 @@ void plan_tiles(Plan& p, int64_t M_or_T, int32_t topk, bool moe, int64_t E, int6
   }
 }
 
+// Block-scaled e4m3 products: token tile and CTAs per tile (a cluster that splits K), no workspace past the header.
+void plan_block(Plan& p, int64_t M, int sms) {
+  p.bt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  p.m_tiles = (M + p.bt - 1) / p.bt;
+  p.max_tiles = p.m_tiles * p.n_tiles;
+  const int64_t room = (int64_t)sms * (p.bt <= 64 ? 2 : 1);
+  p.sk = 1;
+  while (p.sk < 8 && p.max_tiles * p.sk * 2 <= room && p.kst >= 4 * p.sk) p.sk *= 2;
+  p.grid = (int)(p.max_tiles * p.sk);
+  p.ws_bytes = kHeaderBytes;
+}
+
 // The built-in rule, then the tuned table's row for (format class, size bucket), then HQ_TUNE; every choice is
 // checked against what the kernels support before it is taken.
 // kind: 0 dense (hq_gemm), 1 MoE (hq_moe_gemm), 2 MoE with the top-k combine (hq_moe_gemm_combine)
@@ -221,6 +248,10 @@ Plan make_plan(const hq_format_t* f, int64_t M_or_T, int32_t topk, int kind, int
   p.n_tiles = g.n_tiles;
   p.kst = g.k_stages;
   if (sms < 1) sms = 1;
+  if (p.path == PATH_E4M3B) {
+    plan_block(p, M_or_T, sms);
+    return p;
+  }
   size_t off = kHeaderBytes;  // status word, epoch, exit count
   const int64_t E = f->num_experts;
   const int64_t rows = M_or_T * (moe ? topk : 1);
@@ -327,6 +358,7 @@ void dbg_extents(GemmArgs& a, const Plan& p, int64_t c_rows, int64_t comb_rows) 
 
 cudaError_t launch_path(const Plan& p, const GemmArgs& a, cudaStream_t s) {
   cudaError_t e;
+  if (p.path == PATH_E4M3B) return launch_gemm_block(a, p.bt, p.grid, s);
   if (p.path == PATH_INT4)
     e = !p.small ? launch_gemm_int4(a, p.bt, p.grid, s)
                  : (p.dec == DEC_INT4 ? launch_gemm_small(a, p.bt, p.grid, s)
@@ -380,7 +412,7 @@ bool act_maps(GemmArgs& a, const hq_format_t* f, const hq_act_t* A, int64_t rows
   const uint32_t box_rows = moe ? 1u : (uint32_t)bt;
   const uint64_t K = (uint64_t)f->K;
   if (f->act_type == HQ_A_BF16) return encode_2d(&a.tmap_a, A->data, true, K, rows, 64, box_rows, true);
-  if (f->act_type == HQ_A_E4M3_TOKEN) return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true);
+  if (f->act_type == HQ_A_E4M3_TOKEN || f->act_type == HQ_A_E4M3_BLOCK) return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true);
   if (f->act_type == HQ_A_MXFP8)
     return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true) &&
            encode_2d(&a.tmap_sf, A->scale, false, K / 32, rows, 16, box_rows, false);
@@ -428,6 +460,7 @@ hq_status_t hq_unpack_weights(const hq_format_t* fmt, const void* packed, uint8_
 
 size_t hq_workspace_bytes(const hq_format_t* fmt, int64_t M_or_T, int32_t topk) {
   if (check_format(fmt) != HQ_OK || M_or_T < 0 || topk < 1) return 0;
+  if (block_scaled(fmt)) return topk == 1 ? kHeaderBytes : 0;  // no MoE form
   const int sms = num_sms();
   if (fmt->num_experts > 1 || topk > 1) return make_plan(fmt, M_or_T, topk, 1, sms).ws_bytes;
   // one expert with top-1 serves both hq_gemm and hq_moe_gemm: cover both plans
@@ -438,6 +471,7 @@ size_t hq_workspace_bytes(const hq_format_t* fmt, int64_t M_or_T, int32_t topk) 
 
 int32_t hq_kernels_per_call(const hq_format_t* fmt, int64_t M_or_T, int32_t topk, int32_t moe) {
   if (check_format(fmt) != HQ_OK || M_or_T < 1 || topk < 1 || moe < 0 || moe > 2) return 0;
+  if (block_scaled(fmt)) return moe ? 0 : 1;
   const Plan p = make_plan(fmt, M_or_T, topk, moe, num_sms());
   int32_t n = 1 + (p.sk && !p.small ? 1 : 0);  // GEMM (+ split-K reduction of the UMMA kernel)
   if (moe) n += (p.fused ? 0 : 1) + (p.grouped ? 1 : 0);  // routing (+ row permutation), unless fused
@@ -447,11 +481,12 @@ int32_t hq_kernels_per_call(const hq_format_t* fmt, int64_t M_or_T, int32_t topk
 
 hq_status_t hq_launch_plan(const hq_format_t* fmt, int64_t M_or_T, int32_t topk, int32_t moe, int32_t* plan_out) {
   if (check_format(fmt) != HQ_OK || M_or_T < 1 || topk < 1 || moe < 0 || moe > 2 || !plan_out) return HQ_ERR_INVALID_ARG;
+  if (block_scaled(fmt) && moe) return HQ_ERR_UNSUPPORTED;
   const Plan p = make_plan(fmt, M_or_T, topk, moe, num_sms());
   plan_out[0] = p.small;
   plan_out[1] = p.small ? p.dec : p.path;
   plan_out[2] = p.bt;
-  plan_out[3] = p.sk;
+  plan_out[3] = p.path == PATH_E4M3B ? p.sk > 1 : p.sk;
   plan_out[4] = p.grid;
   plan_out[5] = p.grouped;
   return HQ_OK;
@@ -472,6 +507,10 @@ hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packe
   if (fmt->act_type == HQ_A_E4M3_TOKEN && !A->scale) return HQ_ERR_INVALID_ARG;
   if (fmt->act_type == HQ_A_NVFP4 && (!A->scale || !A->global_scale)) return HQ_ERR_INVALID_ARG;
   if ((fmt->act_type == HQ_A_MXFP8 || fmt->act_type == HQ_A_MXFP4) && !A->scale) return HQ_ERR_INVALID_ARG;
+  if (block_scaled(fmt)) {
+    if (!A->scale) return HQ_ERR_INVALID_ARG;
+    if (!aligned16(A->scale) || !aligned16(C)) return HQ_ERR_ALIGNMENT;
+  }
   if (!aligned16(A->data) || !aligned16(packedW) || (A->scale && act_scale_row_bytes(fmt) > 0 && !aligned16(A->scale)))
     return HQ_ERR_ALIGNMENT;
   const int sms = num_sms();
@@ -485,10 +524,12 @@ hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packe
   a.w_expert_bytes = g.expert_bytes;
   a.w_blk = g.blk_bytes;
   a.w_gscale = g.gscale_off >= 0 ? reinterpret_cast<const float*>(a.w + g.gscale_off) : nullptr;
+  if (g.bscale_off >= 0) a.w_gscale = reinterpret_cast<const float*>(a.w + g.bscale_off);
   if (!act_maps(a, fmt, A, M, p.bt, false)) return HQ_ERR_INVALID_ARG;
   a.a_scale = fmt->act_type == HQ_A_NVFP4 ? A->global_scale
-                                            : (fmt->act_type == HQ_A_E4M3_TOKEN ? static_cast<const float*>(A->scale)
-                                                                                 : nullptr);
+                                            : (fmt->act_type == HQ_A_E4M3_TOKEN || block_scaled(fmt)
+                                                   ? static_cast<const float*>(A->scale)
+                                                   : nullptr);
   a.bias = static_cast<const uint16_t*>(bias);
   a.c = static_cast<uint16_t*>(C);
   a.M = (int)M;
@@ -528,6 +569,7 @@ hq_status_t moe_call(const hq_format_t* fmt, const hq_act_t* A, const void* pack
                      hq_stream_t stream, bool combine) {
   hq_status_t st = check_format(fmt);
   if (st != HQ_OK) return st;
+  if (block_scaled(fmt)) return HQ_ERR_UNSUPPORTED;
   if (T < 0 || topk < 1 || T * topk > kMaxRows) return HQ_ERR_INVALID_ARG;
   if (T == 0) return HQ_OK;
   if (!A || !A->data || !packedW || !C || !topk_ids) return HQ_ERR_INVALID_ARG;
@@ -635,7 +677,7 @@ hq_status_t hq_moe_gemm_combine(const hq_format_t* fmt, const hq_act_t* A, const
 }
 
 size_t hq_moe_combine_workspace_bytes(const hq_format_t* fmt, int64_t T, int32_t topk) {
-  if (check_format(fmt) != HQ_OK || T < 0 || topk < 1) return 0;
+  if (check_format(fmt) != HQ_OK || T < 0 || topk < 1 || block_scaled(fmt)) return 0;
   const Plan p = make_plan(fmt, T, topk, 2, num_sms());
   return comb_offset(p) + sizeof(float) * (size_t)(T * fmt->N);
 }
@@ -649,9 +691,70 @@ hq_status_t hq_swiglu(const void* x, int64_t R, int64_t I, void* out, hq_stream_
   return cuda_status(launch_swiglu(x, R, I, out, (cudaStream_t)stream));
 }
 
+hq_status_t hq_swiglu_quantize(int32_t act_type, const void* x, int64_t R, int64_t I, void* out_data, void* out_scale,
+                               hq_stream_t stream) {
+  if (act_type != HQ_A_E4M3_TOKEN && act_type != HQ_A_E4M3_BLOCK) return HQ_ERR_UNSUPPORTED;
+  if (R < 0 || R > kMaxRows || I < 16 || I > kMaxRows) return HQ_ERR_INVALID_ARG;
+  if (I % (act_type == HQ_A_E4M3_BLOCK ? 128 : 16)) return HQ_ERR_ALIGNMENT;
+  if (act_type == HQ_A_E4M3_TOKEN && I > ROW_MAX) return HQ_ERR_UNSUPPORTED;
+  if (R == 0) return HQ_OK;
+  if (!x || !out_data || !out_scale) return HQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(out_data) || !aligned16(out_scale)) return HQ_ERR_ALIGNMENT;
+  if (act_type == HQ_A_E4M3_BLOCK)
+    return cuda_status(launch_block_quant(true, x, R, I, out_data, out_scale, (cudaStream_t)stream));
+  RowArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_stride = 2 * I;
+  a.out = out_data;
+  a.scale = static_cast<float*>(out_scale);
+  a.rows = R;
+  a.width = (int)I;
+  return cuda_status(launch_swiglu_token(a, (cudaStream_t)stream));
+}
+
+hq_status_t hq_add_rms_norm(const hq_norm_t* n, hq_stream_t stream) {
+  if (!n) return HQ_ERR_INVALID_ARG;
+  RowOut out;
+  int64_t unit;
+  switch (n->act_type) {
+    case HQ_A_BF16: out = ROW_BF16, unit = 8; break;
+    case HQ_A_E4M3_TOKEN: out = ROW_TOKEN, unit = 16; break;
+    case HQ_A_E4M3_BLOCK: out = ROW_BLOCK, unit = 128; break;
+    default: return HQ_ERR_UNSUPPORTED;
+  }
+  if (n->T < 0 || n->T > kMaxRows || n->K < unit || n->K > kMaxRows || !(n->eps >= 0.0f)) return HQ_ERR_INVALID_ARG;
+  if (n->K % unit) return HQ_ERR_ALIGNMENT;
+  if (n->K > ROW_MAX) return HQ_ERR_UNSUPPORTED;
+  if ((n->residual != nullptr) != (n->residual_out != nullptr)) return HQ_ERR_INVALID_ARG;
+  const int64_t strides[3] = {n->x_stride, n->residual ? n->residual_stride : n->K,
+                              n->residual ? n->residual_out_stride : n->K};
+  for (int64_t s : strides) {
+    if (s < n->K || s > ((int64_t)1 << 40)) return HQ_ERR_INVALID_ARG;
+    if (s % 8) return HQ_ERR_ALIGNMENT;
+  }
+  if (n->T == 0) return HQ_OK;
+  if (!n->x || !n->weight || !n->out_data || (out != ROW_BF16 && !n->out_scale)) return HQ_ERR_INVALID_ARG;
+  const void* all[6] = {n->x, n->residual, n->weight, n->residual_out, n->out_data, n->out_scale};
+  for (const void* p : all)
+    if (!aligned16(p)) return HQ_ERR_ALIGNMENT;
+  RowArgs a{};
+  a.x = static_cast<const uint16_t*>(n->x);
+  a.x_stride = n->x_stride;
+  a.residual = static_cast<const uint16_t*>(n->residual);
+  a.residual_stride = n->residual_stride;
+  a.weight = static_cast<const uint16_t*>(n->weight);
+  a.residual_out = static_cast<uint16_t*>(n->residual_out);
+  a.residual_out_stride = n->residual_out_stride;
+  a.out = n->out_data;
+  a.scale = static_cast<float*>(n->out_scale);
+  a.rows = n->T;
+  a.width = (int)n->K;
+  a.eps = n->eps;
+  return cuda_status(launch_add_rms_norm(out, a, (cudaStream_t)stream));
+}
 
 size_t hq_quantize_act_workspace_bytes(int32_t act_type, int64_t M, int64_t K) {
-  if (act_type != HQ_A_E4M3_TOKEN && act_type != HQ_A_NVFP4) return 0;
+  if (act_type != HQ_A_E4M3_TOKEN && act_type != HQ_A_NVFP4 && act_type != HQ_A_E4M3_BLOCK) return 0;
   if (M < 0 || M > kMaxRows || K < 16 || K > kMaxRows || K % 16) return 0;
   return act_type == HQ_A_NVFP4 ? sizeof(float) * (size_t)hq::ACT_AMAX_MAX_PARTS : 0;
 }
@@ -659,10 +762,10 @@ size_t hq_quantize_act_workspace_bytes(int32_t act_type, int64_t M, int64_t K) {
 hq_status_t hq_quantize_act(int32_t act_type, const void* x, int64_t M, int64_t K, const float* global_amax,
                             void* out_data, void* out_scale, float* out_global, void* workspace, size_t ws_bytes,
                             hq_stream_t stream) {
-  if (act_type != HQ_A_E4M3_TOKEN && act_type != HQ_A_NVFP4) return HQ_ERR_UNSUPPORTED;
+  if (act_type != HQ_A_E4M3_TOKEN && act_type != HQ_A_NVFP4 && act_type != HQ_A_E4M3_BLOCK) return HQ_ERR_UNSUPPORTED;
   if (M < 0 || M > kMaxRows || K < 16 || K > kMaxRows) return HQ_ERR_INVALID_ARG;
-  if (K % 16) return HQ_ERR_ALIGNMENT;
-  const bool fp8 = act_type == HQ_A_E4M3_TOKEN;
+  if (K % (act_type == HQ_A_E4M3_BLOCK ? 128 : 16)) return HQ_ERR_ALIGNMENT;
+  const bool fp8 = act_type != HQ_A_NVFP4;
   if (!fp8 && !out_global) return HQ_ERR_INVALID_ARG;
   if (M > 0 && (!x || !out_data || !out_scale)) return HQ_ERR_INVALID_ARG;
   if (M > 0 && (!aligned16(x) || !aligned16(out_data) || !aligned16(out_scale))) return HQ_ERR_ALIGNMENT;
@@ -671,6 +774,8 @@ hq_status_t hq_quantize_act(int32_t act_type, const void* x, int64_t M, int64_t 
     if (!aligned16(workspace)) return HQ_ERR_ALIGNMENT;
   }
   if (fp8 && M == 0) return HQ_OK;
+  if (act_type == HQ_A_E4M3_BLOCK)
+    return cuda_status(launch_block_quant(false, x, M, K, out_data, out_scale, (cudaStream_t)stream));
   return cuda_status(hq::launch_act_quant(fp8 ? 1 : 0, x, M, K, global_amax, out_data, out_scale, out_global,
                                           workspace, (cudaStream_t)stream));
 }

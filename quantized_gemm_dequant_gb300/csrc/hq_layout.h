@@ -65,6 +65,10 @@
 //    [16384, 18432) e8m0 block-32 scales as tensor-memory words in the NVFP4 word
 //                   order: word (l*16 + t*4 + c) holds the two scales of MMA step t
 //                   (64 K) of row 32c + l as bytes (s0, s1, s0, s1)
+//  E4M3 with block scales (WK_E4M3_BLOCK), K stage = 128:
+//    [0, 16384)     e4m3 codes as the shared-memory image of a 128-row x 128-byte K-major tile with the 128-byte
+//                   swizzle (as NVFP4's codes)
+//    block scales: fp32 [E][N tile][K stage] after the last expert's blocks
 //  MXFP4, K stage = 128:
 //    [0, 8192)      e2m1 codes, 8 bytes (16 K) per piece, piece p = r*8 + c lands in
 //                   the low half of swizzled 16-byte chunk c of row r
@@ -86,7 +90,8 @@ enum WeightKind {
   WK_E4M3 = 8,
   WK_UINT1_ZP = 9,
   WK_UINT3_ZP = 10,
-  WK_MXFP4_X = 11  // MXFP4 weights packed for MXFP4 activations (not an API format: chosen by the activation type)
+  WK_MXFP4_X = 11,  // MXFP4 weights packed for MXFP4 activations (not an API format: chosen by the activation type)
+  WK_E4M3_BLOCK = 12  // E4M3 weights with a scale per 128 x 128 block (not an API format: chosen by the scale type)
 };
 // Decode variants of the register-decode kernel, one per integer / e4m3 weight layout
 enum DecodeKind { DEC_INT4 = 0, DEC_MXINT4 = 1, DEC_INT8 = 2, DEC_E4M3 = 3, DEC_UINT2 = 4, DEC_UINT1 = 5, DEC_UINT3 = 6 };
@@ -105,7 +110,8 @@ inline int decode_kind(int weight_type) {
 inline bool register_decode_only(int weight_type) { return weight_type >= WK_INT8_SYM; }
 // tcgen05 kernel variants; PATH_MXFP4A: MXFP4 weights with MXFP8 activations (e8m0 block scales on both operands)
 // PATH_MXFP4X: MXFP4 weights with MXFP4 activations (e8m0 block scales on both operands, packed e2m1 in the MMA)
-enum KernelPath { PATH_INT4 = 0, PATH_NVFP4 = 1, PATH_MXFP4 = 2, PATH_MXFP4A = 3, PATH_MXFP4X = 4 };
+// PATH_E4M3B: e4m3 weights and activations with fp32 scales per block of 128 (kernels of their own, hq_gemm_block.cuh)
+enum KernelPath { PATH_INT4 = 0, PATH_NVFP4 = 1, PATH_MXFP4 = 2, PATH_MXFP4A = 3, PATH_MXFP4X = 4, PATH_E4M3B = 5 };
 
 constexpr int TILE_N = 128;  // weight rows per tile (the UMMA M dimension)
 
@@ -118,6 +124,7 @@ struct PackGeom {
   int64_t expert_bytes;
   int64_t total_bytes;  // all experts (+ NVFP4 global scales)
   int64_t gscale_off;   // NVFP4: byte offset of the fp32 [E] global scales, else -1
+  int64_t bscale_off;   // E4M3_BLOCK: byte offset of the fp32 [E][n_tiles][k_stages] block scales, else -1
 };
 
 inline PackGeom pack_geom(int weight_type, int64_t N, int64_t K, int64_t E) {
@@ -151,6 +158,10 @@ inline PackGeom pack_geom(int weight_type, int64_t N, int64_t K, int64_t E) {
     g.path = PATH_MXFP4X;
     g.kstage = 256;
     g.blk_bytes = 16384 + 2048;
+  } else if (weight_type == WK_E4M3_BLOCK) {
+    g.path = PATH_E4M3B;
+    g.kstage = 128;
+    g.blk_bytes = 16384;
   } else if (weight_type == WK_NVFP4) {
     g.path = PATH_NVFP4;
     g.kstage = 256;
@@ -167,6 +178,11 @@ inline PackGeom pack_geom(int weight_type, int64_t N, int64_t K, int64_t E) {
   if (weight_type == WK_NVFP4) {
     g.gscale_off = g.total_bytes;
     g.total_bytes += ((E * 4 + 255) / 256) * 256;
+  }
+  g.bscale_off = -1;
+  if (weight_type == WK_E4M3_BLOCK) {
+    g.bscale_off = g.total_bytes;
+    g.total_bytes += ((E * g.n_tiles * g.k_stages * 4 + 255) / 256) * 256;
   }
   return g;
 }

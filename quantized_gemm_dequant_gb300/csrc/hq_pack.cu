@@ -16,6 +16,7 @@ struct PackArgs {
   int64_t n_tiles, k_stages;
   int blk_bytes;
   int64_t gscale_off;
+  int64_t bscale_off;
 };
 
 // INT8 / E4M3 layout: K offset, within a 16-K row chunk, of byte b of word w (see hq_layout.h).
@@ -166,6 +167,32 @@ __global__ void pack_kernel(PackArgs p, uint8_t* codes, uint8_t* scales, uint8_t
         if (DIR == 0) *zdst = valid ? (uint8_t)(*zsrc & 0x3) : (uint8_t)0;
         else if (valid) *zsrc = *zdst;
       }
+    } else if (p.wt == WK_E4M3_BLOCK) {
+      uint8_t* row = codes + (e * p.N + n) * p.K + ks * 128;
+      const bool wide = (reinterpret_cast<uintptr_t>(codes) & 15) == 0;  // K % 128 == 0: then every row's chunks are
+      for (int c = 0; c < 8; ++c) {
+        uint8_t* d = blk + (r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4);
+        if (DIR == 0) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (valid && wide) v = *reinterpret_cast<const uint4*>(row + 16 * c);
+          *reinterpret_cast<uint4*>(d) = v;
+          if (valid && !wide)
+            for (int b = 0; b < 16; ++b) d[b] = row[16 * c + b];
+        } else if (valid && wide) {
+          *reinterpret_cast<uint4*>(row + 16 * c) = *reinterpret_cast<const uint4*>(d);
+        } else if (valid) {
+          for (int b = 0; b < 16; ++b) row[16 * c + b] = d[b];
+        }
+      }
+      if (r == 0) {
+        const int64_t at = (e * p.n_tiles + nt) * p.k_stages + ks;
+        float* s = reinterpret_cast<float*>(packed + p.bscale_off) + at;
+        float* given = reinterpret_cast<float*>(scales) + at;
+        if (DIR == 0) *s = *given;
+        else *given = *s;
+        if (DIR == 0 && at + 1 == p.E * p.n_tiles * p.k_stages)  // the last scale's thread clears what pads the buffer
+          for (++s; (reinterpret_cast<uintptr_t>(s) - reinterpret_cast<uintptr_t>(packed)) & 255; ++s) *s = 0.0f;
+      }
     } else if (p.wt == WK_INT4_SYM || p.wt == WK_UINT4_ZP || p.wt == WK_MXINT4) {
       const int G = 128;
       const int64_t ng = p.K / G;
@@ -269,7 +296,7 @@ __global__ void pack_kernel(PackArgs p, uint8_t* codes, uint8_t* scales, uint8_t
 cudaError_t launch_pack(int dir, int wt, int64_t N, int64_t K, int64_t E, const void* codes, const void* scales,
                         const void* zeros, const float* gscale, void* packed, cudaStream_t stream) {
   const PackGeom g = pack_geom(wt, N, K, E);
-  PackArgs p{wt, N, K, E, g.n_tiles, g.k_stages, g.blk_bytes, g.gscale_off};
+  PackArgs p{wt, N, K, E, g.n_tiles, g.k_stages, g.blk_bytes, g.gscale_off, g.bscale_off};
   const int64_t total = E * g.n_tiles * g.k_stages * TILE_N;
   const int threads = 256;
   int64_t blocks = (total + threads - 1) / threads;

@@ -1,0 +1,291 @@
+// A layer's rows made into the activations of its next product, in one pass over memory:
+//   add_rms_norm   r = x + residual, residual_out = bf16(r), y = r / sqrt(mean(r^2) + eps) * w
+//   swiglu         y = silu(gate) * up of the rows [gate | up]
+//   (rows as they are, for hq_quantize_act's block scales)
+// with y out as bf16, as e4m3 with one fp32 scale per row, or as e4m3 with one per 128 elements (scale = absmax / 448).
+// y is never rounded on the way: fp32 until its code.
+//
+// All of them are bound by memory: a row is read once and stays in registers between its statistics and its codes.
+#include <cuda_runtime.h>
+#include <float.h>
+#include <stdint.h>
+
+#include "hq_launch.h"
+#include "hq_ptx.cuh"
+#include "hq_quant.cuh"
+#include "hq_row_ops.h"
+
+namespace hq {
+
+namespace {
+
+enum RowSrc { SRC_NORM = 0, SRC_ADD_NORM = 1, SRC_SWIGLU = 2 };
+
+// silu(g) * u = g * u / (1 + exp(-g)).  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's fp32 rounding
+// error, found by an FMA, together with the part of log2(e) below fp32, corrects the power to first order
+// (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to |t| 2^-24.  The reciprocal gets one Newton
+// step.  Past 2^+-127 the quotient is 0 or 1, as it is when the power over- or underflows (infinite gates among them).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float t = g * -1.44269504f;
+  const float d = fmaf(g, -1.44269504f, -t) + g * -1.925963033e-8f;
+  float p, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(fminf(t, 127.0f)));
+  const float q = 1.0f + fmaf(p, d * 0.693147181f, p);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(q));
+  r = fmaf(r, fmaf(-q, r, 1.0f), r);
+  if (fabsf(t) > 127.0f) r = t > 0.0f ? 0.0f : 1.0f;
+  return g * r * u;
+}
+
+// Reductions over a row's threads: a warp, or the CTA (every thread calls them; `turn` alternates between the two
+// buffers, so that one barrier per reduction is enough).
+template <bool WARP, typename T, typename F>
+__device__ __forceinline__ T row_reduce(T v, T zero, T (*red)[32], int& turn, F&& f) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (WARP) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[turn][warp] = v;
+  __syncthreads();
+  v = lane < (int)(blockDim.x >> 5) ? red[turn][lane] : zero;
+  turn ^= 1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// One row per CTA, or per warp (WARP, eight rows a CTA), CH chunks of 8 elements per thread; the next row of the same
+// threads is loaded while the current one is reduced and written.
+template <int SRC, int OUT, int CH, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kernel(const RowArgs a) {
+  __shared__ float red_f[2][32];
+  __shared__ uint32_t red_u[2][32];
+  constexpr bool NORM = SRC != SRC_SWIGLU;
+  constexpr bool TWO = SRC != SRC_NORM;  // two operands a chunk: x and residual, or gate and up
+  constexpr bool AHEAD = CH <= 4;        // registers for the next row
+  int turn_f = 0, turn_u = 0;
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int n = WARP ? 32 : blockDim.x;
+  const int chunks = a.width >> 3;
+  const int64_t step = (int64_t)gridDim.x * (WARP ? 8 : 1);
+  int64_t row = (int64_t)blockIdx.x * (WARP ? 8 : 1) + (WARP ? (threadIdx.x >> 5) : 0);
+  pdl_trigger();
+  pdl_wait();
+  uint4 w[CH], va[CH], vb[CH];
+  auto load = [&](int64_t r) {
+    const uint4* pa = reinterpret_cast<const uint4*>(a.x + r * a.x_stride);
+    const uint4* pb = SRC == SRC_SWIGLU ? pa + chunks : reinterpret_cast<const uint4*>(a.residual + r * a.residual_stride);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = t + j * n;
+      va[j] = c < chunks ? pa[c] : make_uint4(0u, 0u, 0u, 0u);
+      if (TWO) vb[j] = c < chunks ? pb[c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (row < a.rows) load(row);
+  if (NORM) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = t + j * n;
+      w[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.weight) + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  for (; row < a.rows; row += step) {
+    float f[CH][8];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      bf16x8_to_f32(va[j], f[j]);
+      if (TWO) {
+        float g[8];
+        bf16x8_to_f32(vb[j], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = SRC == SRC_SWIGLU ? silu_mul(f[j][i], g[i]) : f[j][i] + g[i];
+      }
+    }
+    if (AHEAD && row + step < a.rows) load(row + step);
+    if (SRC == SRC_ADD_NORM) {
+      uint4* ro = reinterpret_cast<uint4*>(a.residual_out + row * a.residual_out_stride);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (t + j * n < chunks) ro[t + j * n] = bf16x8_of(f[j]);
+    }
+    if (NORM) {
+      auto add = [](float p, float q) { return p + q; };
+      auto squares = [&] {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i & 3] = fmaf(f[j][i], f[j][i], s[i & 3]);
+        return row_reduce<WARP>((s[0] + s[1]) + (s[2] + s[3]), 0.0f, red_f, turn_f, add);
+      };
+      const float ss = squares();
+      float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.width) + a.eps));
+      // A sum that overflowed, or one that lost small squares where eps does not cover them, is taken again with the
+      // row divided by a power of two near its largest magnitude.
+      if (!(ss <= FLT_MAX) || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) m = max(m, absmax_bits(f[j]));
+        m = row_reduce<WARP>(m, 0u, red_u, turn_u, [](uint32_t p, uint32_t q) { return max(p, q); });
+        if (m > 0u && m < 0x7F800000u) {
+          const int e = ilogbf(__uint_as_float(m));
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[j][i] = ldexpf(f[j][i], -e);
+          const double ms = (double)squares() / a.width + ldexp((double)a.eps, -2 * e);
+          rstd = (float)(1.0 / sqrt(ms));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        float g[8];
+        bf16x8_to_f32(w[j], g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * rstd * g[i];
+      }
+    }
+    if (OUT == ROW_BF16) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.width);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (t + j * n < chunks) o[t + j * n] = bf16x8_of(f[j]);
+    } else {
+      uint2* o = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.width);
+      if (OUT == ROW_TOKEN) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) m = max(m, absmax_bits(f[j]));
+        m = row_reduce<WARP>(m, 0u, red_u, turn_u, [](uint32_t p, uint32_t q) { return max(p, q); });
+        const E4m3Scale s(m);
+        if (t == 0) a.scale[row] = s.s;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          if (t + j * n < chunks) o[t + j * n] = s.codes(f[j]);
+      } else {
+        // the 16 chunks of a block are 16 neighbouring lanes (the row's threads are a multiple of 32)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          uint32_t m = absmax_bits(f[j]);
+#pragma unroll
+          for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+          const E4m3Scale s(m);
+          const int c = t + j * n;
+          if (c < chunks) {
+            o[c] = s.codes(f[j]);
+            if ((c & 15) == 0) a.scale[row * (a.width >> 7) + (c >> 4)] = s.s;
+          }
+        }
+      }
+    }
+    if (!AHEAD && row + step < a.rows) load(row + step);
+  }
+}
+
+// A scale per 128 outputs needs no statistics of the row: every thread takes UNROLL chunks of 8 outputs, all loads
+// first; 16 neighbouring lanes hold a block.
+constexpr int BQ_THREADS = 256;
+constexpr int BQ_UNROLL = 2;
+template <bool SWIGLU>
+__global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __restrict__ x, int64_t n8, uint32_t per_row,
+                                                                 uint2* __restrict__ q, float* __restrict__ s_out) {
+  pdl_trigger();
+  pdl_wait();
+  uint4 va[BQ_UNROLL], vb[BQ_UNROLL];
+  const int64_t base = (int64_t)blockIdx.x * (BQ_THREADS * BQ_UNROLL) + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < BQ_UNROLL; ++j) {
+    const int64_t i = base + j * BQ_THREADS;
+    va[j] = vb[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < n8) {
+      int64_t at = i;
+      if (SWIGLU) {  // [gate | up] rows; 32-bit division where it fits (the 64-bit one is a long software routine)
+        const int64_t r = n8 <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / per_row) : i / per_row;
+        at = i + r * per_row;
+        vb[j] = __ldg(x + at + per_row);
+      }
+      va[j] = __ldg(x + at);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < BQ_UNROLL; ++j) {
+    const int64_t i = base + j * BQ_THREADS;
+    float f[8];
+    bf16x8_to_f32(va[j], f);
+    if (SWIGLU) {
+      float u[8];
+      bf16x8_to_f32(vb[j], u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = silu_mul(f[k], u[k]);
+    }
+    uint32_t m = absmax_bits(f);
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const E4m3Scale s(m);
+    if (i < n8) {
+      q[i] = s.codes(f);
+      if ((threadIdx.x & 15) == 0) s_out[i >> 4] = s.s;
+    }
+  }
+}
+
+int sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    n = 1;
+  return n;
+}
+
+template <int SRC, int OUT, int CH, bool WARP>
+cudaError_t launch_row(const RowArgs& a, int threads, cudaStream_t stream) {
+  void (*k)(RowArgs) = row_kernel<SRC, OUT, CH, WARP>;
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+  const int64_t need = WARP ? (a.rows + 7) / 8 : a.rows;
+  const int64_t room = (int64_t)per_sm * sms();
+  return launch_kernel(k, dim3((unsigned)(need < room ? need : room)), dim3(threads), 0, stream, a);
+}
+
+template <int SRC, int OUT>
+cudaError_t launch_rows(const RowArgs& a, cudaStream_t stream) {
+  const int chunks = a.width / 8;
+  const auto threads = [&](int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; };
+  // Rows that a warp holds in four chunks a lane, and enough of them to fill the SMs' warps: no barriers.
+  if (chunks <= 128 && a.rows >= 2048) return launch_row<SRC, OUT, 4, true>(a, 256, stream);
+  // Few rows: as many threads as the row has chunks, for the shortest chain of work.
+  if (a.rows <= 2 * sms() && chunks <= 1024) return launch_row<SRC, OUT, 1, false>(a, threads(1), stream);
+  if (chunks <= 512) return launch_row<SRC, OUT, 2, false>(a, threads(2), stream);
+  if (chunks <= 2048) return launch_row<SRC, OUT, 4, false>(a, threads(4), stream);
+  return launch_row<SRC, OUT, 8, false>(a, threads(8), stream);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rms_norm(RowOut out, const RowArgs& a, cudaStream_t stream) {
+  if (a.residual) {
+    if (out == ROW_BF16) return launch_rows<SRC_ADD_NORM, ROW_BF16>(a, stream);
+    if (out == ROW_TOKEN) return launch_rows<SRC_ADD_NORM, ROW_TOKEN>(a, stream);
+    return launch_rows<SRC_ADD_NORM, ROW_BLOCK>(a, stream);
+  }
+  if (out == ROW_BF16) return launch_rows<SRC_NORM, ROW_BF16>(a, stream);
+  if (out == ROW_TOKEN) return launch_rows<SRC_NORM, ROW_TOKEN>(a, stream);
+  return launch_rows<SRC_NORM, ROW_BLOCK>(a, stream);
+}
+
+cudaError_t launch_swiglu_token(const RowArgs& a, cudaStream_t stream) {
+  return launch_rows<SRC_SWIGLU, ROW_TOKEN>(a, stream);
+}
+
+cudaError_t launch_block_quant(bool swiglu, const void* x, int64_t rows, int64_t width, void* data, void* scale,
+                               cudaStream_t stream) {
+  const int64_t n8 = rows * (width >> 3), per_cta = BQ_THREADS * BQ_UNROLL;
+  const int64_t grid = (n8 + per_cta - 1) / per_cta;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch_kernel(swiglu ? block_quant_kernel<true> : block_quant_kernel<false>, dim3((unsigned)grid),
+                       dim3(BQ_THREADS), 0, stream, static_cast<const uint4*>(x), n8, (uint32_t)(width >> 3),
+                       static_cast<uint2*>(data), static_cast<float*>(scale));
+}
+
+}  // namespace hq
