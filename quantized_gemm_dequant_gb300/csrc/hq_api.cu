@@ -28,6 +28,7 @@ cudaError_t launch_gemm_mxfp4x(const GemmArgs& a, int bt, int grid, cudaStream_t
 cudaError_t launch_gemm_small(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_small_fmt(int dec, const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_block(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
+cudaError_t launch_gemm_block_pair(const GemmArgs& a, int bn, int grid, cudaStream_t stream);
 cudaError_t launch_splitk_reduce(int path, const GemmArgs& a, int bt, int gemm_grid, int grid, cudaStream_t stream);
 cudaError_t launch_combine_round(const float* acc, int64_t n, uint16_t* c, cudaStream_t stream);
 cudaError_t launch_swiglu(const void* x, int64_t R, int64_t I, void* out, cudaStream_t stream);
@@ -144,6 +145,7 @@ struct Plan {
   int path = 0;
   int small = 0;  // integer / FP8 weights with at most 32 tokens per tile: register-decode mma.sync kernel
   int dec = 0;    // its decode variant
+  int pair = 0;     // block-scaled e4m3: features per tile of the CTA-pair kernel, 0 = the kernel for few tokens
   int grouped = 0;  // MoE: routed rows copied into expert-contiguous order first (2-D TMA boxes)
   int fused = 0;    // MoE: the register-decode kernel routes the rows itself (no routing kernel)
   int bt = 16;
@@ -225,16 +227,35 @@ void plan_tiles(Plan& p, int64_t M_or_T, int32_t topk, bool moe, int64_t E, int6
   }
 }
 
-// Block-scaled e4m3 products: token tile and CTAs per tile (a cluster that splits K), no workspace past the header.
+// Block-scaled e4m3 products, no workspace past the header: the CTA-pair kernel (256 tokens by 128 or 256 features), or
+// the kernel for few tokens (a token tile, and CTAs per tile: a cluster that splits K).  HQ_TUNE: kernel 0 / 1, bt the
+// pair's features or the token tile, sk the CTAs per tile.
 void plan_block(Plan& p, int64_t M, int sms) {
+  TuneChoice tc;
+  tune_env_override(tc);
+  // the pair kernel reads the packed weights as rows of 128 bytes, whose index is an int
+  const bool may_pair = p.n_tiles * p.kst < ((int64_t)1 << 24);
+  p.ws_bytes = kHeaderBytes;
+  bool pair = M > 256;
+  if (tc.kernel >= 0) pair = tc.kernel == 0;
+  if (pair && may_pair) {
+    p.pair = tc.bt == 128 || tc.bt == 256 ? tc.bt : 256;
+    p.bt = 256;
+    p.m_tiles = (M + 255) / 256;
+    p.max_tiles = p.m_tiles * (p.pair == 256 ? (p.n_tiles + 1) / 2 : p.n_tiles);
+    const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
+    p.grid = (int)(2 * (p.max_tiles < pairs ? p.max_tiles : pairs));
+    return;
+  }
   p.bt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  if (tc.bt == 16 || tc.bt == 32 || tc.bt == 64 || tc.bt == 128) p.bt = tc.bt;
   p.m_tiles = (M + p.bt - 1) / p.bt;
   p.max_tiles = p.m_tiles * p.n_tiles;
   const int64_t room = (int64_t)sms * (p.bt <= 64 ? 2 : 1);
   p.sk = 1;
   while (p.sk < 8 && p.max_tiles * p.sk * 2 <= room && p.kst >= 4 * p.sk) p.sk *= 2;
+  if (tc.sk >= 1 && tc.sk <= 8 && tc.sk <= p.kst) p.sk = tc.sk;
   p.grid = (int)(p.max_tiles * p.sk);
-  p.ws_bytes = kHeaderBytes;
 }
 
 // The built-in rule, then the tuned table's row for (format class, size bucket), then HQ_TUNE; every choice is
@@ -358,7 +379,8 @@ void dbg_extents(GemmArgs& a, const Plan& p, int64_t c_rows, int64_t comb_rows) 
 
 cudaError_t launch_path(const Plan& p, const GemmArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (p.path == PATH_E4M3B) return launch_gemm_block(a, p.bt, p.grid, s);
+  if (p.path == PATH_E4M3B)
+    return p.pair ? launch_gemm_block_pair(a, p.pair, p.grid, s) : launch_gemm_block(a, p.bt, p.grid, s);
   if (p.path == PATH_INT4)
     e = !p.small ? launch_gemm_int4(a, p.bt, p.grid, s)
                  : (p.dec == DEC_INT4 ? launch_gemm_small(a, p.bt, p.grid, s)
@@ -525,7 +547,10 @@ hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packe
   a.w_blk = g.blk_bytes;
   a.w_gscale = g.gscale_off >= 0 ? reinterpret_cast<const float*>(a.w + g.gscale_off) : nullptr;
   if (g.bscale_off >= 0) a.w_gscale = reinterpret_cast<const float*>(a.w + g.bscale_off);
-  if (!act_maps(a, fmt, A, M, p.bt, false)) return HQ_ERR_INVALID_ARG;
+  if (!act_maps(a, fmt, A, M, p.pair ? 128 : p.bt, false)) return HQ_ERR_INVALID_ARG;
+  if (p.pair && !encode_2d(&a.tmap_sf, a.w, false, 128, (uint64_t)(g.n_tiles * g.k_stages * 128), 128,
+                           (uint32_t)p.pair / 2, false))
+    return HQ_ERR_INVALID_ARG;
   a.a_scale = fmt->act_type == HQ_A_NVFP4 ? A->global_scale
                                             : (fmt->act_type == HQ_A_E4M3_TOKEN || block_scaled(fmt)
                                                    ? static_cast<const float*>(A->scale)

@@ -24,7 +24,21 @@ cudaError_t launch_bt(const GemmArgs& a, int grid, cudaStream_t stream) {
   return launch_cluster_kernel(gemm_block_kernel<BT>, grid, a.sk, BLK_THREADS, BlkCfg<BT>::SMEM, stream, a);
 }
 
+template <int BN>
+cudaError_t launch_pair(const GemmArgs& a, int grid, cudaStream_t stream) {
+  static int done[64] = {0};
+  const cudaError_t e = allow_smem(gemm_block_pair_kernel<BN>, PairCfg<BN>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(gemm_block_pair_kernel<BN>, dim3((unsigned)grid), dim3(PAIR_THREADS), PairCfg<BN>::SMEM, stream,
+                       a);
+}
+
 }  // namespace
+
+// bn features by 256 tokens a pair of CTAs
+cudaError_t launch_gemm_block_pair(const GemmArgs& a, int bn, int grid, cudaStream_t stream) {
+  return bn == 256 ? launch_pair<256>(a, grid, stream) : launch_pair<128>(a, grid, stream);
+}
 
 // bt tokens a tile, grid = tiles * a.sk CTAs
 cudaError_t launch_gemm_block(const GemmArgs& a, int bt, int grid, cudaStream_t stream) {

@@ -298,6 +298,360 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   }
 }
 
+// ------------------------------------------------------------------ many tokens
+// Two CTAs of a cluster share one MMA (cta_group::2): a tile is 256 tokens, the MMA's A operand, by BN features, its B
+// operand.  Each CTA loads its own 128 tokens and half of the tile's weight rows, so that both operands are read from
+// L2 and written to shared memory once per pair, and holds its tokens' sums: a token is a tensor-memory lane, so a
+// thread's sums share one token scale and (128 columns) one weight scale, and a K block costs a thread one scale and
+// an FMA per sum.  Two FMAs go in one instruction.
+//
+// Bound by the MMA: a K block of a 256 x 256 tile takes it 512 cycles, and the promotion of its 128 x 256 sums per CTA
+// by eight warps takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.
+template <int BN>
+struct PairCfg {
+  static constexpr int BROWS = BN / 2;  // weight rows a CTA loads
+  static constexpr int STAGE = 16384 + BROWS * 128;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int SLOTS = 512 / BN;
+  static constexpr int HC = BN / 2;  // columns of a promoting warp
+  static constexpr int SMEM = STAGES * STAGE + 1024 /*align*/ + 512 /*barriers*/;
+};
+constexpr int PAIR_THREADS = 384;  // warps 0-7 promote, 8 loads, 9 issues the MMAs (of the cluster's first CTA)
+// registers: 168 x 384 at launch; the promoting warps raise theirs to 224, the others go down to 56 (2 x 224 + 56 = 3 x 168)
+constexpr int PAIR_TOKENS = 256;
+constexpr int PAIR_GROUP = 8;  // token tiles per round of feature tiles: the tiles in flight share operands in L2
+
+template <int BN>
+struct PairSmem {
+  using C = PairCfg<BN>;
+  uint64_t full[C::STAGES], empty[C::STAGES], dfull[C::SLOTS], dempty[C::SLOTS], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Token tile and feature tile of a tile index: groups of PAIR_GROUP token tiles, feature tiles inside, token tiles
+// innermost.
+__host__ __device__ inline void pair_tile(int t, int m_tiles, int n_tiles, int& mt, int& nt) {
+  const int per = PAIR_GROUP * n_tiles, g = t / per, in = t - g * per;
+  const int left = m_tiles - g * PAIR_GROUP, rows = left < PAIR_GROUP ? left : PAIR_GROUP;
+  nt = in / rows;
+  mt = g * PAIR_GROUP + in - nt * rows;
+}
+
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on the barrier at this address in both CTAs once every tcgen05 operation issued so far completes
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// 2-D tensor load into this CTA whose bytes are counted on a barrier of the pair (a shared::cluster address)
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait with cluster scope: what the peer CTA did before its arrival is visible afterwards
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit_ns) {
+  const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;
+  const uint32_t hint = limit_ns < 1000000ull ? (uint32_t)limit_ns : 1000000u;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
+        : "memory");
+    if (ok) return true;
+    if (*abort || clock64() - c0 >= lim) return false;
+  }
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// (a0, a1) += (v0, v1) * (s, s), one instruction
+__device__ __forceinline__ void fma2(uint64_t& a, uint32_t v0, uint32_t v1, uint64_t s2) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(s2));
+}
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
+    gemm_block_pair_kernel(const __grid_constant__ GemmArgs args) {
+  using C = PairCfg<BN>;
+  static_assert(sizeof(PairSmem<BN>) <= 512, "shared state");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+  const int kst = args.kst;
+  const int f_tiles = BN == 256 ? (args.n_tiles + 1) / 2 : args.n_tiles;  // tiles of BN features
+  const int tiles = args.m_tiles * f_tiles;
+  volatile int* abort_flag = &sh.abort_flag;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 8 * 32) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int d = 0; d < C::SLOTS; ++d) {
+      mbar_init(&sh.dfull[d], 1);
+      mbar_init(&sh.dempty[d], 16);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&args.tmap_a);
+    prefetch_tmap(&args.tmap_sf);
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers stand before either is signalled
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  bool ok = true;
+  auto fail = [&] {
+    *abort_flag = 1;
+    atomicCAS(args.status, 0, ERR_TIMEOUT);
+    ok = false;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8 && lane == 0) {
+      // ------------------------------------------------ loads: this CTA's tokens and its half of the weight rows
+      int s = 0;
+      uint32_t ph = 0;
+      int64_t n = 0;
+      bool waited = false;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        int mt, ft;
+        pair_tile(t, args.m_tiles, f_tiles, mt, ft);
+        const int m0 = mt * PAIR_TOKENS + rank * 128;
+        // first row of this CTA's weights in the packed buffer, taken as rows of 128 bytes (a feature tile past the
+        // last one is loaded from the last: its columns are not stored)
+        int nt = BN == 256 ? 2 * ft + rank : ft;
+        nt = nt < args.n_tiles ? nt : args.n_tiles - 1;
+        const int w0 = nt * kst * 128 + (BN == 256 ? 0 : rank * C::BROWS);
+        for (int b = 0; b < kst; ++b) {
+          if (!mbar_wait(&sh.empty[s], ph ^ 1, abort_flag, args.wait_ns)) {
+            fail();
+            break;
+          }
+          const uint32_t bar = cluster_addr(smem_u32(&sh.full[s]), 0);
+          uint8_t* dst = smem + s * C::STAGE;
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE);
+          tma_load_2d_pair(dst + 16384, &args.tmap_sf, 0, w0 + b * 128, bar);
+          if (!waited) {  // packed weights may be read before the grid dependency wait, activations not
+            pdl_wait();
+            waited = true;
+          }
+          tma_load_2d_pair(dst, &args.tmap_a, b * 128, m0, bar);
+          ++n;
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // every copy lands before shared memory is released; the first CTA's barriers count both CTAs' bytes, and the
+      // second leaves after the first
+      int never = 0;
+      if (rank == 0)
+        for (int k = 0; k < C::STAGES; ++k)
+          if (n > k) mbar_wait(&sh.full[k], (uint32_t)(((n - 1 - k) / C::STAGES) & 1), &never, DRAIN_WAIT_NS);
+      if (!ok)
+        for (const long long c0 = clock64(); clock64() - c0 < 10000000ll;) {}  // copies that no barrier counts any more
+    } else if (warp == 9 && lane == 0 && rank == 0) {
+      // ------------------------------------------------ MMAs of the pair
+      int s = 0, d = 0;
+      uint32_t ph = 0, dph = 0;
+      auto waitf = [&](uint64_t* bar, uint32_t par) {
+        if (ok && !mbar_wait_cluster(bar, par, abort_flag, args.wait_ns)) fail();
+        return ok;
+      };
+      for (int t = pair; t < tiles && ok; t += pairs)
+        for (int b = 0; b < kst; ++b) {
+          if (!waitf(&sh.dempty[d], dph ^ 1) || !waitf(&sh.full[s], ph)) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + s * C::STAGE), w = a + 16384;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_e4m3_pair(tmem + d * BN, smem_desc(a + 32 * k, 16, 1024, 2), smem_desc(w + 32 * k, 16, 1024, 2),
+                           idesc_e4m3(256, BN), k > 0);
+          umma_commit_pair(&sh.empty[s]);
+          umma_commit_pair(&sh.dfull[d]);
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++d == C::SLOTS) {
+            d = 0;
+            dph ^= 1;
+          }
+        }
+      int never = 0;  // every MMA completes before tensor memory is released
+      umma_commit_pair(&sh.drain);
+      mbar_wait(&sh.drain, 0, &never, DRAIN_WAIT_NS);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ------------------------------------------------ promotion: warp -> 32 tokens warp % 4, column half warp / 4
+    pdl_wait();
+    const int h = warp >> 2;
+    const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * C::HC;
+    int d = 0;
+    uint32_t dph = 0;
+    const bool quad = (kst & 3) == 0;
+    uint32_t dempty[C::SLOTS];
+#pragma unroll
+    for (int i = 0; i < C::SLOTS; ++i) dempty[i] = cluster_addr(smem_u32(&sh.dempty[i]), 0);
+    for (int t = pair; t < tiles; t += pairs) {
+      int mt, ft;
+      pair_tile(t, args.m_tiles, f_tiles, mt, ft);
+      const int m = mt * PAIR_TOKENS + rank * 128 + (warp & 3) * 32 + lane;
+      const int nt = BN == 256 ? 2 * ft + h : ft;
+      const bool live = m < args.M && nt < args.n_tiles;
+      const float* sa = args.a_scale + (int64_t)(m < args.M ? m : 0) * kst;
+      const float* sw = args.w_gscale + (int64_t)(nt < args.n_tiles ? nt : 0) * kst;
+      // scales of four K blocks, loaded four ahead
+      float sc[4], next[4];
+      auto load_scales = [&](int b) {
+        if (!live || b >= kst) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = 0.0f;
+        } else if (quad) {
+          const float4 x = *reinterpret_cast<const float4*>(sa + b), y = *reinterpret_cast<const float4*>(sw + b);
+          next[0] = x.x * y.x;
+          next[1] = x.y * y.y;
+          next[2] = x.z * y.z;
+          next[3] = x.w * y.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next[i] = b + i < kst ? sa[b + i] * sw[b + i] : 0.0f;
+        }
+      };
+      uint64_t acc[C::HC / 2];
+#pragma unroll
+      for (int j = 0; j < C::HC / 2; ++j) acc[j] = 0;
+      load_scales(0);
+      for (int b0 = 0; b0 < kst && ok; b0 += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = next[i];
+        load_scales(b0 + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (b0 + i >= kst) break;
+          if (!mbar_wait(&sh.dfull[d], dph, abort_flag, args.wait_ns)) {
+            fail();
+            break;
+          }
+          tc_fence_after();
+          uint64_t s2;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(sc[i]));
+          uint32_t v[2][32];
+          tmem_ld32(src + d * BN, v[0]);
+#pragma unroll
+          for (int c = 0; c < C::HC / 32; ++c) {
+            tmem_wait_ld();
+            if (c + 1 < C::HC / 32) {
+              tmem_ld32(src + d * BN + 32 * (c + 1), v[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(dempty[d]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s2);
+          }
+          if (++d == C::SLOTS) {
+            d = 0;
+            dph ^= 1;
+          }
+        }
+      }
+      if (!ok) break;
+      // ------------------------------------------------ output: a thread's row, HC columns of it
+      int row = live ? m : -1;
+#if HQ_DEBUG_BOUNDS
+      if (row >= 0) row = dbg_row(row, args.dbg_c_rows, args.status);
+#endif
+      if (row >= 0) {
+        const int n0 = BN == 256 ? nt * 128 : nt * 128 + h * C::HC;
+        uint16_t* o = args.c + (int64_t)row * args.N + n0;
+        const bool wide = (args.N & 15) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 31) == 0;
+#pragma unroll
+        for (int j = 0; j < C::HC; j += 16) {
+          if (n0 + j >= args.N) break;
+          float y[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(y[2 * k]), "=f"(y[2 * k + 1]) : "l"(acc[j / 2 + k]));
+          if (args.bias) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (n0 + j + k < args.N) y[k] += bf16_to_f32(args.bias[n0 + j + k]);
+          }
+          uint32_t p[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p[k] = pack_bf16x2(y[2 * k], y[2 * k + 1]);
+          if (wide) {
+            st_global_32b(o + j, p);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (n0 + j + k < args.N) o[j + k] = (uint16_t)(p[k / 2] >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other's MMAs, copies or arrivals may still reach it
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
 // `cluster` CTAs of consecutive index form a cluster.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster_kernel(void (*kernel)(KArgs...), int grid, int cluster, int threads, int smem,

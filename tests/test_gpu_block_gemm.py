@@ -48,6 +48,15 @@ def test_large(lib, M, N, K):
     _check(lib, M, N, K, bias=True)
 
 
+# every kernel and every way of splitting a tile, at sizes that the planner would give to another
+@pytest.mark.parametrize("choice", ["kernel=0,bt=128", "kernel=0,bt=256", "kernel=1,bt=16", "kernel=1,bt=32,sk=1",
+                                    "kernel=1,bt=64,sk=8", "kernel=1,bt=128,sk=4", "kernel=1,bt=16,sk=2"])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (3, 130, 1024), (129, 257, 1152), (257, 1001, 1280), (1030, 700, 2048)])
+def test_choices(lib, monkeypatch, choice, M, N, K):
+    monkeypatch.setenv("HQ_TUNE", choice)
+    _check(lib, M, N, K, bias=True, seed=N)
+
+
 def test_pack_is_inverted(lib):
     for N, K in ((1, 128), (130, 256), (384, 1152)):
         _, _, w, sw, _ = B.operands(3, 1, N, K)
