@@ -548,8 +548,7 @@ hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packe
   a.w_gscale = g.gscale_off >= 0 ? reinterpret_cast<const float*>(a.w + g.gscale_off) : nullptr;
   if (g.bscale_off >= 0) a.w_gscale = reinterpret_cast<const float*>(a.w + g.bscale_off);
   if (!act_maps(a, fmt, A, M, p.pair ? 128 : p.bt, false)) return HQ_ERR_INVALID_ARG;
-  if (p.pair && !encode_2d(&a.tmap_sf, a.w, false, 128, (uint64_t)(g.n_tiles * g.k_stages * 128), 128,
-                           (uint32_t)p.pair / 2, false))
+  if (p.pair && !encode_2d(&a.tmap_sf, a.w, false, 128, (uint64_t)(g.n_tiles * g.k_stages * 128), 128, 64, false))
     return HQ_ERR_INVALID_ARG;
   a.a_scale = fmt->act_type == HQ_A_NVFP4 ? A->global_scale
                                             : (fmt->act_type == HQ_A_E4M3_TOKEN || block_scaled(fmt)

@@ -24,6 +24,17 @@ __device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
+// mbar_wait for waits that are short and on the critical path of every K block: the test suspends the thread only as
+// long as the hardware sees fit.  (With a time hint it becomes a sleep, whose end comes hundreds of cycles late.)
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;  // at least limit_ns at clocks up to 3 GHz
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort || clock64() - c0 >= lim) return false;
+  }
+}
+
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -129,7 +140,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
   auto waitf = [&](uint64_t* bar, uint32_t par) {
-    if (ok && !mbar_wait(bar, par, abort_flag, args.wait_ns)) {
+    if (ok && !mbar_wait_soon(bar, par, abort_flag, args.wait_ns)) {
       *abort_flag = 1;
       atomicCAS(args.status, 0, ERR_TIMEOUT);
       ok = false;
@@ -307,24 +318,36 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 //
 // Bound by the MMA: a K block of a 256 x 256 tile takes it 512 cycles, and the promotion of its 128 x 256 sums per CTA
 // by eight warps takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.
+// Accumulators are handed over 128 columns at a time (four slots in tensor memory), so that half of the promoting warps
+// read one half of a tile while the MMA fills the other.
 template <int BN>
 struct PairCfg {
   static constexpr int BROWS = BN / 2;  // weight rows a CTA loads
   static constexpr int STAGE = 16384 + BROWS * 128;
   static constexpr int STAGES = BN == 256 ? 6 : 8;
-  static constexpr int SLOTS = 512 / BN;
+  static constexpr int SN = 128;           // features of an accumulator slot (the MMA's N): one weight tile
+  static constexpr int HALVES = BN / SN;  // slots a K block fills
+  static constexpr int SLOTS = 512 / SN, DEPTH = SLOTS / HALVES;
   static constexpr int HC = BN / 2;  // columns of a promoting warp
-  static constexpr int SMEM = STAGES * STAGE + 1024 /*align*/ + 512 /*barriers*/;
+  static constexpr int TILES = BN / 128;           // weight tiles
+  static constexpr int SK = 8;                     // K blocks in a group of scales
+  static constexpr int SGROUP = SK * TILES * 128;  // [K block][weight tile][token]
+  static constexpr int SGROUPS = 2;
+  static constexpr int SCALES = SGROUPS * SGROUP * 4;
+  static constexpr int SMEM = STAGES * STAGE + SCALES + 1024 /*align*/ + 512 /*barriers*/;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-constexpr int PAIR_THREADS = 384;  // warps 0-7 promote, 8 loads, 9 issues the MMAs (of the cluster's first CTA)
-// registers: 168 x 384 at launch; the promoting warps raise theirs to 224, the others go down to 56 (2 x 224 + 56 = 3 x 168)
+// warps 0-7 promote, 8 loads, 9 and 10 issue the MMAs (of the cluster's first CTA), 11 multiplies the scales
+constexpr int PAIR_THREADS = 384;
+// registers: 168 x 384 at launch; the promoting warps raise theirs to 216, the others go down to 72 (2 x 216 + 72 = 3 x 168)
 constexpr int PAIR_TOKENS = 256;
 constexpr int PAIR_GROUP = 8;  // token tiles per round of feature tiles: the tiles in flight share operands in L2
 
 template <int BN>
 struct PairSmem {
   using C = PairCfg<BN>;
-  uint64_t full[C::STAGES], empty[C::STAGES], dfull[C::SLOTS], dempty[C::SLOTS], drain;
+  uint64_t full[C::STAGES], empty[C::STAGES], dfull[C::SLOTS], dempty[C::SLOTS], sfull[C::SGROUPS],
+      sempty[C::SGROUPS], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -338,6 +361,11 @@ __host__ __device__ inline void pair_tile(int t, int m_tiles, int n_tiles, int& 
   mt = g * PAIR_GROUP + in - nt * rows;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -366,8 +394,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, in
 // Arrival on a barrier of the pair that orders nothing but itself: what it announces, the end of this warp's
 // tensor-memory reads, is ordered by their wait and the tcgen05 fence before it.  (A releasing arrival at cluster scope
 // waits for the thread's outstanding memory operations, some 1000 cycles a K block: 8192 tokens took 888 us with it.)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(bar),
+      "r"(on)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -379,10 +411,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
-}
-// (a0, a1) += (v0, v1) * (s, s), one instruction
-__device__ __forceinline__ void fma2(uint64_t& a, uint32_t v0, uint32_t v1, uint64_t s2) {
-  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(s2));
 }
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -397,8 +425,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   static_assert(sizeof(PairSmem<BN>) <= 512, "shared state");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);  // [SGROUPS][4][TILES][128]
+  PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE + C::SCALES);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler sees it
   const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
   const int kst = args.kst;
   const int f_tiles = BN == 256 ? (args.n_tiles + 1) / 2 : args.n_tiles;  // tiles of BN features
@@ -412,13 +442,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   if (tid == 8 * 32) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.empty[s], C::HALVES);
     }
     for (int d = 0; d < C::SLOTS; ++d) {
       mbar_init(&sh.dfull[d], 1);
-      mbar_init(&sh.dempty[d], 16);
+      mbar_init(&sh.dempty[d], 16 / C::HALVES);
     }
-    mbar_init(&sh.drain, 1);
+    for (int g = 0; g < C::SGROUPS; ++g) {
+      mbar_init(&sh.sfull[g], 32);
+      mbar_init(&sh.sempty[g], 8);
+    }
+    mbar_init(&sh.drain, 2);
     sh.abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&args.tmap_a);
@@ -438,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------ loads: this CTA's tokens and its half of the weight rows
       int s = 0;
@@ -449,20 +483,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         int mt, ft;
         pair_tile(t, args.m_tiles, f_tiles, mt, ft);
         const int m0 = mt * PAIR_TOKENS + rank * 128;
-        // first row of this CTA's weights in the packed buffer, taken as rows of 128 bytes (a feature tile past the
-        // last one is loaded from the last: its columns are not stored)
-        int nt = BN == 256 ? 2 * ft + rank : ft;
-        nt = nt < args.n_tiles ? nt : args.n_tiles - 1;
-        const int w0 = nt * kst * 128 + (BN == 256 ? 0 : rank * C::BROWS);
+        // first rows of this CTA's 64 of each weight tile in the packed buffer, taken as rows of 128 bytes (a weight
+        // tile past the last one is loaded from the last: its columns are not stored)
+        int w0[C::TILES];
+#pragma unroll
+        for (int h = 0; h < C::TILES; ++h) {
+          const int nt = C::TILES * ft + h;
+          w0[h] = (nt < args.n_tiles ? nt : args.n_tiles - 1) * kst * 128 + rank * 64;
+        }
         for (int b = 0; b < kst; ++b) {
-          if (!mbar_wait(&sh.empty[s], ph ^ 1, abort_flag, args.wait_ns)) {
+          if (!mbar_wait_soon(&sh.empty[s], ph ^ 1, abort_flag, args.wait_ns)) {
             fail();
             break;
           }
           const uint32_t bar = cluster_addr(smem_u32(&sh.full[s]), 0);
           uint8_t* dst = smem + s * C::STAGE;
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE);
-          tma_load_2d_pair(dst + 16384, &args.tmap_sf, 0, w0 + b * 128, bar);
+#pragma unroll
+          for (int h = 0; h < C::TILES; ++h)
+            tma_load_2d_pair(dst + 16384 + h * 8192, &args.tmap_sf, 0, w0[h] + b * 128, bar);
           if (!waited) {  // packed weights may be read before the grid dependency wait, activations not
             pdl_wait();
             waited = true;
@@ -483,117 +522,188 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
           if (n > k) mbar_wait(&sh.full[k], (uint32_t)(((n - 1 - k) / C::STAGES) & 1), &never, DRAIN_WAIT_NS);
       if (!ok)
         for (const long long c0 = clock64(); clock64() - c0 < 10000000ll;) {}  // copies that no barrier counts any more
-    } else if (warp == 9 && lane == 0 && rank == 0) {
-      // ------------------------------------------------ MMAs of the pair
-      int s = 0, d = 0;
-      uint32_t ph = 0, dph = 0;
+    } else if ((warp == 9 || warp == 10) && rank == 0) {
+      // ------------------------------------------------ MMAs of the pair: two warps take a tile's slots in turn (waits
+      // and issue take a warp some 250 cycles a slot), each as a whole, so that descriptors and addresses are uniform
+      // registers; one lane issues
+      const bool one = elect_one();
+      const int w = warp - 9;
+      uint32_t dph = 0;  // a bit per accumulator slot
+      uint32_t base = 0;  // stages of the tiles before
       auto waitf = [&](uint64_t* bar, uint32_t par) {
-        if (ok && !mbar_wait(bar, par, abort_flag, args.wait_ns)) fail();
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_soon(bar, par, abort_flag, args.wait_ns))) fail();
         return ok;
       };
-      for (int t = pair; t < tiles && ok; t += pairs)
-        for (int b = 0; b < kst; ++b) {
-          if (!waitf(&sh.dempty[d], dph ^ 1) || !waitf(&sh.full[s], ph)) break;
+      const uint32_t ring = smem_u32(smem);
+      const int h = C::HALVES == 2 ? w : 0;
+      constexpr int STEP = C::HALVES == 2 ? 1 : 2;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int b1 = C::HALVES == 2 ? 0 : w;
+        int s = (int)((base + b1) % C::STAGES);
+        uint32_t ph = ((base + b1) / C::STAGES) & 1;
+        for (int b = b1; b < kst; b += STEP) {
+          const int d = (b & (C::DEPTH - 1)) * C::HALVES + h;  // a tile begins with the first slots
+          if (!waitf(&sh.full[s], ph) || !waitf(&sh.dempty[d], ~(dph >> d) & 1)) break;
+          dph ^= 1u << d;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * C::STAGE), w = a + 16384;
+          const uint64_t x = smem_desc(ring + s * C::STAGE, 16, 1024, 2),
+                         y = smem_desc(ring + s * C::STAGE + 16384 + h * 8192, 16, 1024, 2);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_e4m3_pair(tmem + d * BN, smem_desc(a + 32 * k, 16, 1024, 2), smem_desc(w + 32 * k, 16, 1024, 2),
-                           idesc_e4m3(256, BN), k > 0);
-          umma_commit_pair(&sh.empty[s]);
-          umma_commit_pair(&sh.dfull[d]);
-          if (++s == C::STAGES) {
-            s = 0;
+            for (int k = 0; k < 4; ++k)  // 32 bytes further on: the address field counts 16s
+              umma_e4m3_pair(tmem + d * C::SN, x + 2 * k, y + 2 * k, idesc_e4m3(256, C::SN), k > 0);
+            umma_commit_pair(&sh.dfull[d]);
+            umma_commit_pair(&sh.empty[s]);
+          }
+          s += STEP;
+          if (s >= C::STAGES) {
+            s -= C::STAGES;
             ph ^= 1;
           }
-          if (++d == C::SLOTS) {
-            d = 0;
-            dph ^= 1;
-          }
         }
+        base += (uint32_t)kst;
+      }
       int never = 0;  // every MMA completes before tensor memory is released
-      umma_commit_pair(&sh.drain);
+      if (one) umma_commit_pair(&sh.drain);
       mbar_wait(&sh.drain, 0, &never, DRAIN_WAIT_NS);
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // ------------------------------------------------ promotion: warp -> 32 tokens warp % 4, column half warp / 4
-    pdl_wait();
-    const int h = warp >> 2;
-    const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * C::HC;
-    int d = 0;
-    uint32_t dph = 0;
-    const bool quad = (kst & 3) == 0;
-    uint32_t dempty[C::SLOTS];
-#pragma unroll
-    for (int i = 0; i < C::SLOTS; ++i) dempty[i] = cluster_addr(smem_u32(&sh.dempty[i]), 0);
-    for (int t = pair; t < tiles; t += pairs) {
-      int mt, ft;
-      pair_tile(t, args.m_tiles, f_tiles, mt, ft);
-      const int m = mt * PAIR_TOKENS + rank * 128 + (warp & 3) * 32 + lane;
-      const int nt = BN == 256 ? 2 * ft + h : ft;
-      const bool live = m < args.M && nt < args.n_tiles;
-      const float* sa = args.a_scale + (int64_t)(m < args.M ? m : 0) * kst;
-      const float* sw = args.w_gscale + (int64_t)(nt < args.n_tiles ? nt : 0) * kst;
-      // scales of four K blocks, loaded four ahead
-      float sc[4], next[4];
-      auto load_scales = [&](int b) {
-        if (!live || b >= kst) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) next[i] = 0.0f;
-        } else if (quad) {
-          const float4 x = *reinterpret_cast<const float4*>(sa + b), y = *reinterpret_cast<const float4*>(sw + b);
-          next[0] = x.x * y.x;
-          next[1] = x.y * y.y;
-          next[2] = x.z * y.z;
-          next[3] = x.w * y.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) next[i] = b + i < kst ? sa[b + i] * sw[b + i] : 0.0f;
-        }
-      };
-      uint64_t acc[C::HC / 2];
-#pragma unroll
-      for (int j = 0; j < C::HC / 2; ++j) acc[j] = 0;
-      load_scales(0);
-      for (int b0 = 0; b0 < kst && ok; b0 += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] = next[i];
-        load_scales(b0 + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (b0 + i >= kst) break;
-          if (!mbar_wait(&sh.dfull[d], dph, abort_flag, args.wait_ns)) {
+    } else if (warp == 11) {
+      // ------------------------------------------------ scales: token scale times weight scale of a group of K blocks,
+      // four tokens a thread
+      pdl_wait();
+      const int r = lane;
+      const bool quad = (kst & 3) == 0;
+      int g = 0;
+      uint32_t ph = 0;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        int mt, ft;
+        pair_tile(t, args.m_tiles, f_tiles, mt, ft);
+        for (int b0 = 0; b0 < kst; b0 += C::SK) {
+          if (!mbar_wait_soon(&sh.sempty[g], ph ^ 1, abort_flag, args.wait_ns)) {
             fail();
             break;
           }
-          tc_fence_after();
-          uint64_t s2;
-          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(sc[i]));
-          uint32_t v[2][32];
-          tmem_ld32(src + d * BN, v[0]);
+          const int end = b0 + C::SK < kst ? b0 + C::SK : kst;
+          float* o = scales + g * C::SGROUP + r;
+          for (int b = b0; b < end; b += 4) {
+            float a[4][4];
 #pragma unroll
-          for (int c = 0; c < C::HC / 32; ++c) {
-            tmem_wait_ld();
-            if (c + 1 < C::HC / 32) {
-              tmem_ld32(src + d * BN + 32 * (c + 1), v[(c + 1) & 1]);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(dempty[d]);
+            for (int u = 0; u < 4; ++u) {
+              const int m = mt * PAIR_TOKENS + rank * 128 + r + 32 * u;
+              const float* p = args.a_scale + (int64_t)m * kst + b;
+              if (m < args.M && quad) {
+                *reinterpret_cast<float4*>(a[u]) = *reinterpret_cast<const float4*>(p);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[u][i] = m < args.M && b + i < kst ? p[i] : 0.0f;
+              }
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s2);
+            for (int h = 0; h < C::TILES; ++h) {
+              const int nt = C::TILES * ft + h < args.n_tiles ? C::TILES * ft + h : args.n_tiles - 1;
+              const float* p = args.w_gscale + (int64_t)nt * kst + b;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float w = b + i < kst ? p[i] : 0.0f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[(i * C::TILES + h) * 128 + 32 * u] = a[u][i] * w;
+              }
+            }
+            o += 4 * C::TILES * 128;
           }
-          if (++d == C::SLOTS) {
-            d = 0;
-            dph ^= 1;
+          mbar_arrive(&sh.sfull[g]);
+          if (++g == C::SGROUPS) {
+            g = 0;
+            ph ^= 1;
           }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------ promotion: warp -> 32 tokens warp % 4, column half warp / 4
+    pdl_wait();
+    const int h = warp >> 2;
+    // K block b of a tile lies in slot b % DEPTH (of this warp's half, where a slot holds half a tile)
+    const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + h * (C::HALVES == 2 ? C::SN : C::HC);
+    const uint32_t dempty = cluster_addr(smem_u32(&sh.dempty[C::HALVES == 2 ? h : 0]), 0);
+    uint64_t* dfull = &sh.dfull[C::HALVES == 2 ? h : 0];
+    constexpr int CHUNKS = C::HC / 32;  // 4 or 2
+    constexpr int UNROLL = 8;           // K blocks; divides a group
+    uint32_t dph = 0;  // a bit per slot
+    const float* sc = scales + (BN == 256 ? h * 128 : 0) + (warp & 3) * 32 + lane;
+    int g = 0;
+    uint32_t gph = 0;
+    // two buffers of 32 columns: a slot is given back when its last columns are read, before they are added
+    uint32_t v[2][32];
+    // the slot's sums are there: the first of them are on their way
+    auto open = [&](int d) {
+      if (!mbar_wait_soon(dfull + d * C::HALVES, (dph >> d) & 1, abort_flag, args.wait_ns)) fail();
+      dph ^= 1u << d;
+      tc_fence_after();
+      tmem_ld32(src + d * (C::HALVES * C::SN), v[0]);
+      tmem_ld32(src + d * (C::HALVES * C::SN) + 32, v[1]);
+    };
+    float f, fn = 0.0f;  // this K block's scale and the next one's
+    const float* at = sc;
+    auto group = [&] {
+      if (!mbar_wait_soon(&sh.sfull[g], gph, abort_flag, args.wait_ns)) fail();
+      at = sc + g * C::SGROUP;
+      fn = *at;
+    };
+    group();
+    for (int t = pair; t < tiles; t += pairs) {
+      float2 acc[C::HC / 2];
+#pragma unroll
+      for (int j = 0; j < C::HC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+      auto add = [&](const uint32_t (&x)[32], int c) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          acc[16 * c + j] = __ffma2_rn(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
+                                       make_float2(f, f), acc[16 * c + j]);
+      };
+      open(0);
+      for (int b0 = 0; b0 < kst; b0 += UNROLL) {
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+          if (b0 + i >= kst) break;
+          const int d = i % C::DEPTH;
+          const uint32_t from = src + d * (C::HALVES * C::SN);
+          f = fn;
+          tmem_wait_ld();
+          if (CHUNKS == 4) {
+            add(v[0], 0);
+            tmem_ld32(from + 64, v[0]);
+            add(v[1], 1);
+            tmem_ld32(from + 96, v[1]);
+            tmem_wait_ld();
+          }
+          tc_fence_before();
+          mbar_arrive_cluster_if(dempty + 8 * C::HALVES * d, lane == 0);
+          if (i + 1 < UNROLL) fn = at[(i + 1) * C::TILES * 128];
+          add(v[0], CHUNKS - 2);
+          add(v[1], CHUNKS - 1);
+          if (b0 + i + 1 < kst) open((i + 1) % C::DEPTH);
+        }
+        const int next = b0 + UNROLL;
+        at += UNROLL * C::TILES * 128;
+        if (next % C::SK == 0 || next >= kst) {
+          mbar_arrive_if(&sh.sempty[g], lane == 0);
+          if (++g == C::SGROUPS) {
+            g = 0;
+            gph ^= 1;
+          }
+          if (next < kst || t + pairs < tiles) group();
+        } else {
+          fn = *at;
         }
       }
       if (!ok) break;
       // ------------------------------------------------ output: a thread's row, HC columns of it
-      int row = live ? m : -1;
+      int mt, ft;
+      pair_tile(t, args.m_tiles, f_tiles, mt, ft);
+      const int m = mt * PAIR_TOKENS + rank * 128 + (warp & 3) * 32 + lane;
+      const int nt = BN == 256 ? 2 * ft + h : ft;
+      int row = m < args.M && nt < args.n_tiles ? m : -1;
 #if HQ_DEBUG_BOUNDS
       if (row >= 0) row = dbg_row(row, args.dbg_c_rows, args.status);
 #endif
@@ -606,8 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
           if (n0 + j >= args.N) break;
           float y[16];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(y[2 * k]), "=f"(y[2 * k + 1]) : "l"(acc[j / 2 + k]));
+          for (int k = 0; k < 8; ++k) y[2 * k] = acc[j / 2 + k].x, y[2 * k + 1] = acc[j / 2 + k].y;
           if (args.bias) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
