@@ -200,6 +200,8 @@ _BF16 = (torch.bfloat16,)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
+_bf16, _f32, _i32t, _i64t = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 class _Args:
@@ -356,22 +358,49 @@ def make_workspace(fmt, rows, topk=1, device="cuda", stream=None):
     return ws
 
 
+# bytes of an activation row, and of its scales, by type: multiples and divisors of K; the scales' dtype
+_ROW = {HQ_A_BF16: (2, 1, 0, 1, None), HQ_A_E4M3_TOKEN: (1, 1, 4, 0, _f32), HQ_A_MXFP8: (1, 1, 1, 32, None),
+        HQ_A_NVFP4: (1, 2, 1, 16, None), HQ_A_MXFP4: (1, 2, 1, 32, None), HQ_A_E4M3_BLOCK: (1, 1, 4, 128, _f32)}
+
+
+def _has(t, nbytes, dev, dtype=None):
+    """Whether an optional tensor of a call is right."""
+    return t is None or (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()
+                         and t.nbytes >= nbytes and (dtype is None or t.dtype is dtype))
+
+
 def gemm(fmt, act, packed, M, bias=None, out=None, workspace=None, stream=None):
     """C[M, N] bf16 = A . Wdeq^T (+ bias).  `act` is {'data', 'scale'?, 'gscale'?} of device tensors."""
     w = "hq_gemm"
-    args = _Args(w).act(act, fmt, M).add(packed, "packed", packed_bytes(fmt)).add(bias, "bias", 2 * fmt.N, _BF16)
-    args.add(out, "out", 2 * M * fmt.N, _BF16).add(workspace, "workspace")
-    pd, ps, pg, pw, pb, pc, pws = args.ptrs()
-    dev = act["data"].device
+    N, K, at = fmt.N, fmt.K, fmt.act_type
+    row = _ROW.get(at)
+    dev = _device() if isinstance(act, dict) and row is not None and torch.cuda.is_initialized() else None
+    right = False
+    if dev is not None:  # a call whose tensors are right looks at each of them once, in place
+        d, s, g = act.get("data"), act.get("scale"), act.get("gscale")
+        mul, div, smul, sdiv, sdt = row
+        right = (d is not None and _has(d, M * (mul * K // div), dev, _bf16 if at == HQ_A_BF16 else None)
+                 and _has(s, M * (smul * K // sdiv if sdiv else smul), dev, sdt)
+                 and _has(g, 4 if at == HQ_A_NVFP4 else 0, dev, _f32) and packed is not None
+                 and _has(packed, packed_bytes(fmt), dev) and _has(bias, 2 * N, dev, _bf16)
+                 and _has(out, 2 * M * N, dev, _bf16) and _has(workspace, 0, dev))
+    if right:
+        A = Act(d.data_ptr(), None if s is None else s.data_ptr(), None if g is None else g.data_ptr())
+        pw, pb = packed.data_ptr(), None if bias is None else bias.data_ptr()
+    else:
+        args = _Args(w).act(act, fmt, M).add(packed, "packed", packed_bytes(fmt)).add(bias, "bias", 2 * fmt.N, _BF16)
+        args.add(out, "out", 2 * M * fmt.N, _BF16).add(workspace, "workspace")
+        pd, ps, pg, pw, pb, _, _ = args.ptrs()
+        A = Act(pd, ps, pg)
     if out is None:
-        out = torch.empty((M, fmt.N), dtype=torch.bfloat16, device=dev)
-        pc = _ptr(out)
+        out = torch.empty((M, N), dtype=_bf16, device=act["data"].device)
     if workspace is None:
-        workspace = make_workspace(fmt, M, 1, dev, stream)
-        pws = _ptr(workspace)
-    A = Act(pd, ps, pg)
-    _check(_lib.hq_gemm(ctypes.byref(fmt), ctypes.byref(A), pw, pb, pc, int(M), fmt.N, fmt.K, pws,
-                        _nbytes(workspace), _stream(stream)), w)
+        workspace = make_workspace(fmt, M, 1, act["data"].device, stream)
+    st = _lib.hq_gemm(ctypes.byref(fmt), ctypes.byref(A), pw, pb, out.data_ptr(), int(M), N, K, workspace.data_ptr(),
+                      workspace.nbytes, (_raw_stream(dev) if right else torch.cuda.current_stream().cuda_stream)
+                      if stream is None else stream.cuda_stream)
+    if st != HQ_OK:
+        raise HQError(st, w)
     return out
 
 
@@ -541,39 +570,38 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
 
 def _new_act(at, rows, width, device, stream=None):
     """An activation operand that a call fills: bf16 rows, or e4m3 codes with a scale per row or per 128 elements."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # the new tensors belong to the stream the call runs on
+            return _new_act(at, rows, width, device)
     if at == HQ_A_BF16:
-        return dict(data=_on(stream, torch.empty, (rows, width), dtype=torch.bfloat16, device=device))
-    shape = (rows, width // 128) if at == HQ_A_E4M3_BLOCK else (rows,)
-    return dict(data=_on(stream, torch.empty, (rows, width), dtype=torch.uint8, device=device),
-                scale=_on(stream, torch.empty, shape, dtype=torch.float32, device=device))
+        return {"data": torch.empty((rows, width), dtype=_bf16, device=device)}
+    return {"data": torch.empty((rows, width), dtype=torch.uint8, device=device),
+            "scale": torch.empty((rows, width // 128) if at == HQ_A_E4M3_BLOCK else rows, dtype=_f32, device=device)}
 
 
-def _act_items(w, at, out, rows, width):
-    """The tensors of an activation operand that a call writes, for _right_or_raise."""
-    if out is None:
-        return ()
+def _out_act(w, at, out, rows, width, dev):
+    """Whether a given activation operand is right to be filled, and the items that _Args judges where it is not."""
     if not isinstance(out, dict) or "data" not in out or (at != HQ_A_BF16 and out.get("scale") is None):
         raise HQArgError(w, "out must be a dict with 'data' and, in 8 bits, 'scale'")
-    n = rows * width
+    d, n = out["data"], rows * width
     if at == HQ_A_BF16:
-        return ((out["data"], "out['data']", n, _bf16),)
-    if isinstance(out["data"], torch.Tensor) and out["data"].element_size() != 1:
-        raise HQArgError(w, f"out['data'] has dtype {out['data'].dtype}; expected one byte per element")
-    return ((out["data"], "out['data']", n, None),
-            (out["scale"], "out['scale']", n // 128 if at == HQ_A_E4M3_BLOCK else rows, _f32))
+        return d is not None and _has(d, 2 * n, dev, _bf16), ((d, "out['data']", 2 * n, _BF16),)
+    if isinstance(d, torch.Tensor) and d.element_size() != 1:
+        raise HQArgError(w, f"out['data'] has dtype {d.dtype}; expected one byte per element")
+    m = 4 * (n // 128 if at == HQ_A_E4M3_BLOCK else rows)
+    return (d is not None and _has(d, n, dev) and _has(out["scale"], m, dev, _f32),
+            ((d, "out['data']", n, None), (out["scale"], "out['scale']", m, _F32)))
 
 
-def _right_or_raise(w, items, dev):
-    """Checks the tensors of a call, items (tensor or None, name, elements, dtype or None for bytes): one look at each
-    right one; at the first that is not, all are judged and HQArgError is raised."""
-    for t, name, n, dt in items:
-        if t is not None and not (isinstance(t, torch.Tensor) and (dt is None or t.dtype is dt)
-                                  and t.get_device() == dev and t.is_contiguous() and t.numel() >= n):
-            args = _Args(w)
-            for t, name, n, dt in items:
-                args.add(t, name, n * (dt.itemsize if dt else 1), (dt,) if dt else None)
-            args.ptrs()
-            raise HQArgError(w, "the tensors are on different devices")
+def _judge(w, items):
+    """Raises the error of a call whose tensors are not all right."""
+    args = _Args(w)
+    for t, name, nbytes, dtypes in items:
+        if t is None:
+            raise HQArgError(w, f"{name} is required")
+        args.add(t, name, nbytes, dtypes)
+    args.ptrs()
+    raise HQArgError(w, "the tensors are not on one device")
 
 
 def swiglu_quantize(afmt, x, out=None, stream=None):
@@ -585,9 +613,12 @@ def swiglu_quantize(afmt, x, out=None, stream=None):
         raise HQArgError(w, f"afmt must be 'e4m3_tok' or 'e4m3_block', not {afmt!r}")
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] % 2:
         raise HQArgError(w, "x must be a 2-D [R, 2I] tensor")
-    R, I = x.shape[0], x.shape[1] // 2
+    R, I = x.shape
+    I //= 2
     dev = _device() if x.is_cuda else None  # (no tensor is on device None: host tensors are refused)
-    _right_or_raise(w, ((x, "x", 2 * R * I, _bf16), *_act_items(w, at, out, R, I)), dev)
+    right, items = (True, ()) if out is None else _out_act(w, at, out, R, I, dev)
+    if not (right and x.dtype is _bf16 and x.get_device() == dev and x.is_contiguous()):
+        _judge(w, ((x, "x", 4 * R * I, _BF16), *items))
     if out is None:
         out = _new_act(at, R, I, x.device, stream)
     st = _lib.hq_swiglu_quantize(at, x.data_ptr(), R, I, out["data"].data_ptr(), out["scale"].data_ptr(),
@@ -597,16 +628,17 @@ def swiglu_quantize(afmt, x, out=None, stream=None):
     return out
 
 
-def _rows_of(w, t, name, K):
-    """Row stride of a 2-D [T, K] tensor whose rows are contiguous and do not overlap, and a tensor to check in its
-    place (itself, or its first row where rows lie apart)."""
+def _row_stride(w, t, name, T, K):
+    """Row stride of a 2-D [T, K] tensor whose rows are contiguous and do not overlap."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] != K:
         raise HQArgError(w, f"{name} must be a 2-D [T, {K}] tensor")
-    if t.shape[0] <= 1 or t.stride(0) == K:
-        return K, t
+    if t.shape[0] != T:
+        raise HQArgError(w, f"{name} has {t.shape[0]} rows, x has {T}")
+    if t.is_contiguous():
+        return K
     if t.stride(0) < K or (K > 1 and t.stride(1) != 1):
         raise HQArgError(w, f"{name}'s rows must be contiguous and must not overlap")
-    return t.stride(0), t[0]
+    return t.stride(0)
 
 
 def add_rms_norm(afmt, x, weight, residual=None, eps=1e-6, residual_out=None, out=None, stream=None):
@@ -622,31 +654,31 @@ def add_rms_norm(afmt, x, weight, residual=None, eps=1e-6, residual_out=None, ou
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise HQArgError(w, "x must be a 2-D [T, K] tensor")
     T, K = x.shape
-    if weight is None:
-        raise HQArgError(w, "weight is required")
-    sx, x1 = _rows_of(w, x, "x", K)
-    items = [(x1, "x", x1.numel(), _bf16), (weight, "weight", K, _bf16)]
-    sr = so = K
-    if residual is None:
-        if residual_out is not None:
-            raise HQArgError(w, "residual_out needs a residual")
-    else:
-        sr, r1 = _rows_of(w, residual, "residual", K)
-        items.append((r1, "residual", r1.numel(), _bf16))
-        if residual_out is not None:
-            so, o1 = _rows_of(w, residual_out, "residual_out", K)
-            items.append((o1, "residual_out", o1.numel(), _bf16))
-        for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-            if t is not None and t.shape[0] != T:
-                raise HQArgError(w, f"{name} has {t.shape[0]} rows, x has {T}")
+    sx, sr, so = _row_stride(w, x, "x", T, K), K, K
     dev = _device() if x.is_cuda else None  # (no tensor is on device None: host tensors are refused)
-    _right_or_raise(w, (*items, *_act_items(w, at, out, T, K)), dev)
+    right = (x.dtype is _bf16 and x.get_device() == dev and weight is not None and _has(weight, 2 * K, dev, _bf16))
+    if residual is not None:
+        sr = _row_stride(w, residual, "residual", T, K)
+        right = right and residual.dtype is _bf16 and residual.get_device() == dev
+        if residual_out is not None:
+            so = _row_stride(w, residual_out, "residual_out", T, K)
+            right = right and residual_out.dtype is _bf16 and residual_out.get_device() == dev
+    elif residual_out is not None:
+        raise HQArgError(w, "residual_out needs a residual")
+    fill, items = (True, ()) if out is None else _out_act(w, at, out, T, K, dev)
+    if not (right and fill):
+        rows = [(t[:1], n, 2 * K if T else 0, _BF16) for t, n in
+                ((x, "x"), (residual, "residual"), (residual_out, "residual_out")) if t is not None]
+        _judge(w, (*rows, (weight, "weight", 2 * K, _BF16), *items))
     if out is None:
         out = _new_act(at, T, K, x.device, stream)
-    if residual is not None and residual_out is None:
-        residual_out = _on(stream, torch.empty, (T, K), dtype=_bf16, device=x.device)
-    a = _kv_pack(w, _NORM, at, eps, T, K, x.data_ptr(), sx, 0 if residual is None else residual.data_ptr(), sr,
-                 weight.data_ptr(), 0 if residual is None else residual_out.data_ptr(), so, out["data"].data_ptr(),
+    pr = po = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = (torch.empty((T, K), dtype=_bf16, device=x.device) if stream is None else
+                            _on(stream, torch.empty, (T, K), dtype=_bf16, device=x.device))
+        pr, po = residual.data_ptr(), residual_out.data_ptr()
+    a = _kv_pack(w, _NORM, at, eps, T, K, x.data_ptr(), sx, pr, sr, weight.data_ptr(), po, so, out["data"].data_ptr(),
                  0 if at == HQ_A_BF16 else out["scale"].data_ptr())
     st = _lib.hq_add_rms_norm(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
@@ -745,8 +777,6 @@ def _on(stream, make, *a, **k):
 
 # A decoding step makes these calls for every layer, so a call whose tensors are right looks at each of them once, in
 # place; at the first one that is not, _kv_ptrs judges them all and raises.
-_bf16, _f32, _i32t, _i64t = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _kv_cache(w, cache):

@@ -21,9 +21,6 @@ __device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
   return d;
 }
-__device__ __forceinline__ uint4 bf16x8_of(const float (&f)[8]) {
-  return make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
-}
 
 // two floats -> two e4m3 bytes (lo = a), round to nearest even, saturating
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
@@ -58,36 +55,64 @@ __device__ __forceinline__ float absmax_bits_to_f32(uint32_t m) {
   return __uint_as_float(h << 16);
 }
 
-// The e4m3 scale of values whose largest magnitude has the bits `amax`: s = amax / 448, and what division by it needs.
-// Magnitudes are compared as unsigned bit patterns, which order like the numbers and put infinity and NaN on top, so a
-// NaN is not lost: it becomes the scale.
+// ---- eight values as four pairs (two fp32 operations an instruction)
+__device__ __forceinline__ void bf16x8_to_f32x2(const uint4& v, float2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 bf16x8_of(const float2 (&f)[4]) {
+  return make_uint4(bf16x2_of(f[0].x, f[0].y), bf16x2_of(f[1].x, f[1].y), bf16x2_of(f[2].x, f[2].y),
+                    bf16x2_of(f[3].x, f[3].y));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// the larger of three magnitudes; a NaN among them wins
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+// largest magnitude of `m` (not negative) and eight values, as its bits: unsigned bit patterns order like the numbers
+// and put infinity and NaN on top, so that further maxima keep a NaN
+__device__ __forceinline__ uint32_t absmax_bits(const float2 (&f)[4], float m = 0.0f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max3_nan(m, f[i].x, f[i].y);
+  return __float_as_uint(m) & 0x7FFFFFFFu;
+}
+
+// The e4m3 scale of values whose largest magnitude has the bits `amax`: s = amax / 448, and the codes of values divided
+// by it.  Quotients are those of IEEE division: div_by's two steps after a multiplication by the reciprocal (of the
+// scale: approximated, with one Newton step), in the range where its residuals are exact (what matters is above 2^-10,
+// so that they stay above 2^-93 from a scale of 2^-60 on), plain division outside.
 struct E4m3Scale {
   float s, inv;
-  bool on, fast;
+  bool fast;
   __device__ __forceinline__ explicit E4m3Scale(uint32_t amax) {
-    s = __fdiv_rn(__uint_as_float(amax), 448.0f);
-    inv = __frcp_rn(s);
-    on = s > 0.0f;          // a scale of zero (or NaN) has zero codes
-    fast = s >= 0x1p-60f;  // div_by's residual is exact: the quotients that matter are above 2^-10
+    const float m = __uint_as_float(amax);
+    fast = m >= 0x1p-50f && m <= 0x1p126f;
+    s = fast ? div_by(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = fmaf(inv, fmaf(-s, inv, 1.0f), inv);
   }
-  // e4m3 codes of eight values
-  __device__ __forceinline__ uint2 codes(const float (&f)[8]) const {
-    if (!on) return make_uint2(0u, 0u);
+  __device__ __forceinline__ uint2 codes(const float2 (&f)[4]) const {
     uint32_t b[4];
+    if (fast) {
+      const float2 y = both(inv), ns = both(-s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      b[i] = fast ? cvt_e4m3x2(div_by(f[2 * i], s, inv), div_by(f[2 * i + 1], s, inv))
-                  : cvt_e4m3x2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s));
+      for (int i = 0; i < 4; ++i) {
+        const float2 q = __fmul2_rn(f[i], y);
+        const float2 r = __ffma2_rn(q, ns, f[i]);
+        const float2 z = __ffma2_rn(r, y, q);
+        b[i] = cvt_e4m3x2(z.x, z.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // a scale of zero, or one that is no number, has zero codes
+        b[i] = s > 0.0f ? cvt_e4m3x2(__fdiv_rn(f[i].x, s), __fdiv_rn(f[i].y, s)) : 0u;
+    }
     return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   }
 };
-
-// largest magnitude of eight values, as its bits
-__device__ __forceinline__ uint32_t absmax_bits(const float (&f)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  return m;
-}
 
 }  // namespace hq

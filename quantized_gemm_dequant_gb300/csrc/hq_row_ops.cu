@@ -10,6 +10,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "hq_launch.h"
 #include "hq_ptx.cuh"
 #include "hq_quant.cuh"
@@ -21,20 +23,35 @@ namespace {
 
 enum RowSrc { SRC_NORM = 0, SRC_ADD_NORM = 1, SRC_SWIGLU = 2 };
 
-// silu(g) * u = g * u / (1 + exp(-g)).  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's fp32 rounding
-// error, found by an FMA, together with the part of log2(e) below fp32, corrects the power to first order
+// silu(g) * u = g * u / (1 + exp(-g)) of eight pairs.  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's
+// fp32 rounding error, found by an FMA, together with the part of log2(e) below fp32, corrects the power to first order
 // (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to |t| 2^-24.  The reciprocal gets one Newton
-// step.  Past 2^+-127 the quotient is 0 or 1, as it is when the power over- or underflows (infinite gates among them).
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  const float t = g * -1.44269504f;
-  const float d = fmaf(g, -1.44269504f, -t) + g * -1.925963033e-8f;
-  float p, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(p) : "f"(fminf(t, 127.0f)));
-  const float q = 1.0f + fmaf(p, d * 0.693147181f, p);
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(q));
-  r = fmaf(r, fmaf(-q, r, 1.0f), r);
-  if (fabsf(t) > 127.0f) r = t > 0.0f ? 0.0f : 1.0f;
-  return g * r * u;
+// step.  Two values go through each instruction but the power's and the reciprocal's.  Where a power over- or
+// underflows (and where a gate is no number or infinite) the quotient is taken as 0 or 1.
+__device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
+  constexpr float kHi = -1.44269504f, kLo = -1.925963033e-8f, kLn2 = 0.693147181f;
+  float2 t[4], r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = __fmul2_rn(g[i], both(kHi));
+    const float2 d = __ffma2_rn(g[i], both(kLo), __ffma2_rn(g[i], both(kHi), make_float2(-t[i].x, -t[i].y)));
+    float2 p;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.x) : "f"(t[i].x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(p.y) : "f"(t[i].y));
+    const float2 q = __fadd2_rn(__ffma2_rn(p, __fmul2_rn(d, both(kLn2)), p), both(1.0f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r[i].x) : "f"(q.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r[i].y) : "f"(q.y));
+    r[i] = __ffma2_rn(r[i], __ffma2_rn(make_float2(-q.x, -q.y), r[i], both(1.0f)), r[i]);
+  }
+  if (!(__uint_as_float(absmax_bits(t)) <= 126.0f)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (fabsf(t[i].x) > 126.0f) r[i].x = t[i].x > 0.0f ? 0.0f : 1.0f;
+      if (fabsf(t[i].y) > 126.0f) r[i].y = t[i].y > 0.0f ? 0.0f : 1.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = __fmul2_rn(__fmul2_rn(g[i], r[i]), u[i]);
 }
 
 // Reductions over a row's threads: a warp, or the CTA (every thread calls them; `turn` alternates between the two
@@ -55,14 +72,14 @@ __device__ __forceinline__ T row_reduce(T v, T zero, T (*red)[32], int& turn, F&
 }
 
 // One row per CTA, or per warp (WARP, eight rows a CTA), CH chunks of 8 elements per thread; the next row of the same
-// threads is loaded while the current one is reduced and written.
-template <int SRC, int OUT, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kernel(const RowArgs a) {
+// threads is loaded while the current one is reduced and written.  LONG: rows past 2048 chunks on 1024 threads, whose
+// registers leave no room for that, nor for the norm's weights.
+template <int SRC, int OUT, int CH, bool WARP, bool LONG>
+__global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) row_kernel(const RowArgs a) {
   __shared__ float red_f[2][32];
   __shared__ uint32_t red_u[2][32];
   constexpr bool NORM = SRC != SRC_SWIGLU;
   constexpr bool TWO = SRC != SRC_NORM;  // two operands a chunk: x and residual, or gate and up
-  constexpr bool AHEAD = CH <= 4;        // registers for the next row
   int turn_f = 0, turn_u = 0;
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int n = WARP ? 32 : blockDim.x;
@@ -71,38 +88,48 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kerne
   int64_t row = (int64_t)blockIdx.x * (WARP ? 8 : 1) + (WARP ? (threadIdx.x >> 5) : 0);
   pdl_trigger();
   pdl_wait();
-  uint4 w[CH], va[CH], vb[CH];
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 w[LONG ? 1 : CH], va[LONG ? 1 : CH], vb[LONG ? 1 : CH];
+  auto first = [&](int64_t r) { return reinterpret_cast<const uint4*>(a.x + r * a.x_stride); };
+  auto second = [&](int64_t r) {
+    return SRC == SRC_SWIGLU ? first(r) + chunks : reinterpret_cast<const uint4*>(a.residual + r * a.residual_stride);
+  };
+  auto weight = [&](int c) { return c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.weight) + c) : none; };
   auto load = [&](int64_t r) {
-    const uint4* pa = reinterpret_cast<const uint4*>(a.x + r * a.x_stride);
-    const uint4* pb = SRC == SRC_SWIGLU ? pa + chunks : reinterpret_cast<const uint4*>(a.residual + r * a.residual_stride);
+    const uint4 *pa = first(r), *pb = TWO ? second(r) : pa;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = t + j * n;
-      va[j] = c < chunks ? pa[c] : make_uint4(0u, 0u, 0u, 0u);
-      if (TWO) vb[j] = c < chunks ? pb[c] : make_uint4(0u, 0u, 0u, 0u);
+      va[j] = c < chunks ? pa[c] : none;
+      if (TWO) vb[j] = c < chunks ? pb[c] : none;
     }
   };
-  if (row < a.rows) load(row);
-  if (NORM) {
+  if (!LONG) {
+    if (row < a.rows) load(row);
+    if (NORM) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = t + j * n;
-      w[j] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.weight) + c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < CH; ++j) w[j] = weight(t + j * n);
     }
   }
   for (; row < a.rows; row += step) {
-    float f[CH][8];
+    float2 f[CH][4];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      bf16x8_to_f32(va[j], f[j]);
+      const int c = t + j * n;
+      const uint4 x = LONG ? (c < chunks ? first(row)[c] : none) : va[LONG ? 0 : j];
+      bf16x8_to_f32x2(x, f[j]);
       if (TWO) {
-        float g[8];
-        bf16x8_to_f32(vb[j], g);
+        float2 g[4];
+        bf16x8_to_f32x2(LONG ? (c < chunks ? second(row)[c] : none) : vb[LONG ? 0 : j], g);
+        if (SRC == SRC_SWIGLU) {
+          silu_mul(f[j], g);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[j][i] = SRC == SRC_SWIGLU ? silu_mul(f[j][i], g[i]) : f[j][i] + g[i];
+          for (int i = 0; i < 4; ++i) f[j][i] = __fadd2_rn(f[j][i], g[i]);
+        }
       }
     }
-    if (AHEAD && row + step < a.rows) load(row + step);
+    if (!LONG && row + step < a.rows) load(row + step);
     if (SRC == SRC_ADD_NORM) {
       uint4* ro = reinterpret_cast<uint4*>(a.residual_out + row * a.residual_out_stride);
 #pragma unroll
@@ -112,12 +139,12 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kerne
     if (NORM) {
       auto add = [](float p, float q) { return p + q; };
       auto squares = [&] {
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float2 s[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
         for (int j = 0; j < CH; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i & 3] = fmaf(f[j][i], f[j][i], s[i & 3]);
-        return row_reduce<WARP>((s[0] + s[1]) + (s[2] + s[3]), 0.0f, red_f, turn_f, add);
+          for (int i = 0; i < 4; ++i) s[i & 1] = __ffma2_rn(f[j][i], f[j][i], s[i & 1]);
+        return row_reduce<WARP>((s[0].x + s[1].x) + (s[0].y + s[1].y), 0.0f, red_f, turn_f, add);
       };
       const float ss = squares();
       float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.width) + a.eps));
@@ -133,17 +160,17 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kerne
 #pragma unroll
           for (int j = 0; j < CH; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[j][i] = ldexpf(f[j][i], -e);
+            for (int i = 0; i < 4; ++i) f[j][i] = make_float2(ldexpf(f[j][i].x, -e), ldexpf(f[j][i].y, -e));
           const double ms = (double)squares() / a.width + ldexp((double)a.eps, -2 * e);
           rstd = (float)(1.0 / sqrt(ms));
         }
       }
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        float g[8];
-        bf16x8_to_f32(w[j], g);
+        float2 g[4];
+        bf16x8_to_f32x2(LONG ? weight(t + j * n) : w[LONG ? 0 : j], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * rstd * g[i];
+        for (int i = 0; i < 4; ++i) f[j][i] = __fmul2_rn(__fmul2_rn(f[j][i], both(rstd)), g[i]);
       }
     }
     if (OUT == ROW_BF16) {
@@ -179,7 +206,6 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 ? 1024 : 512)) row_kerne
         }
       }
     }
-    if (!AHEAD && row + step < a.rows) load(row + step);
   }
 }
 
@@ -211,13 +237,12 @@ __global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __
 #pragma unroll
   for (int j = 0; j < BQ_UNROLL; ++j) {
     const int64_t i = base + j * BQ_THREADS;
-    float f[8];
-    bf16x8_to_f32(va[j], f);
+    float2 f[4];
+    bf16x8_to_f32x2(va[j], f);
     if (SWIGLU) {
-      float u[8];
-      bf16x8_to_f32(vb[j], u);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = silu_mul(f[k], u[k]);
+      float2 u[4];
+      bf16x8_to_f32x2(vb[j], u);
+      silu_mul(f, u);
     }
     uint32_t m = absmax_bits(f);
 #pragma unroll
@@ -231,20 +256,30 @@ __global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __
 }
 
 int sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    n = 1;
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 1;
+    return v < 1 ? 1 : v;
+  }();
   return n;
 }
 
-template <int SRC, int OUT, int CH, bool WARP>
+template <int SRC, int OUT, int CH, bool WARP, bool LONG = false>
 cudaError_t launch_row(const RowArgs& a, int threads, cudaStream_t stream) {
-  void (*k)(RowArgs) = row_kernel<SRC, OUT, CH, WARP>;
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+  void (*k)(RowArgs) = row_kernel<SRC, OUT, CH, WARP, LONG>;
   const int64_t need = WARP ? (a.rows + 7) / 8 : a.rows;
-  const int64_t room = (int64_t)per_sm * sms();
+  int64_t room = sms();
+  if (need > room) {  // CTAs an SM holds, asked once for each CTA size
+    static std::atomic<int> known[33];
+    int per_sm = known[threads / 32].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+      known[threads / 32].store(per_sm, std::memory_order_relaxed);
+    }
+    room *= per_sm;
+  }
   return launch_kernel(k, dim3((unsigned)(need < room ? need : room)), dim3(threads), 0, stream, a);
 }
 
@@ -258,7 +293,7 @@ cudaError_t launch_rows(const RowArgs& a, cudaStream_t stream) {
   if (a.rows <= 2 * sms() && chunks <= 1024) return launch_row<SRC, OUT, 1, false>(a, threads(1), stream);
   if (chunks <= 512) return launch_row<SRC, OUT, 2, false>(a, threads(2), stream);
   if (chunks <= 2048) return launch_row<SRC, OUT, 4, false>(a, threads(4), stream);
-  return launch_row<SRC, OUT, 8, false>(a, threads(8), stream);
+  return launch_row<SRC, OUT, 4, false, true>(a, threads(4), stream);
 }
 
 }  // namespace
