@@ -265,7 +265,7 @@ HQ_API hq_status_t hq_swiglu_quantize(int32_t act_type, const void* x, int64_t R
 /* One hq_add_rms_norm call. */
 typedef struct {
   int32_t act_type;  /* HQ_A_BF16, HQ_A_E4M3_TOKEN or HQ_A_E4M3_BLOCK: what out_data and out_scale hold */
-  float eps;         /* >= 0 */
+  float eps;         /* >= 0, finite */
   int64_t T;         /* rows, >= 0 */
   int64_t K;         /* elements of a row, at most 32768; a multiple of 8 (BF16), 16 (TOKEN) or 128 (BLOCK) */
   const void* x;     /* bf16 [T] rows of K */

@@ -35,6 +35,24 @@ __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, v
   }
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -97,7 +115,8 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* scales = reinterpret_cast<float*>(smem + C::RING);  // [2][KC][BT]
   BlkSmem<BT>& sh = *reinterpret_cast<BlkSmem<BT>*>(smem + C::RING + C::SCALES);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler sees it
   const int split = args.sk;
   const int rank = (int)(blockIdx.x % (unsigned)split), tile = (int)(blockIdx.x / (unsigned)split);
   const int nt = tile / args.m_tiles, m0 = (tile - nt * args.m_tiles) * BT;  // neighbours share a weight tile
@@ -149,9 +168,9 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   };
 
   constexpr int HC = BT / 2;
-  float acc[HC];
+  float2 acc[HC / 2];
 #pragma unroll
-  for (int j = 0; j < HC; ++j) acc[j] = 0.0f;
+  for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
 
   if (warp == BLK_LOAD_WARP) {
     if (lane == 0) {
@@ -174,46 +193,49 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
         if (n > k) mbar_wait(&sh.full[k], (uint32_t)(((n - 1 - k) / C::STAGES) & 1), &never, DRAIN_WAIT_NS);
     }
   } else if (warp == BLK_MMA_WARP) {
-    if (lane == 0) {
-      int s = 0, d = 0;
-      uint32_t ph = 0, dph = 0;
-      for (int i = 0; i < nblk; ++i) {
-        if (!waitf(&sh.dempty[d], dph ^ 1) || !waitf(&sh.full[s], ph)) break;
-        tc_fence_after();
-        const uint32_t w = smem_u32(smem + s * C::STAGE), a = w + 16384;
+    // (the whole warp runs the loop, so that descriptors and addresses are uniform registers; one lane issues)
+    const bool one = elect_one();
+    const uint32_t ring = smem_u32(smem);
+    int s = 0, d = 0;
+    uint32_t ph = 0, dph = 0;
+    for (int i = 0; i < nblk; ++i) {
+      if (!__all_sync(0xffffffffu, waitf(&sh.dempty[d], dph ^ 1) && waitf(&sh.full[s], ph))) break;
+      tc_fence_after();
+      const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2), a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
+      if (one) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_e4m3_ss(tmem + d * BT, smem_desc(w + 32 * k, 16, 1024, 2), smem_desc(a + 32 * k, 16, 1024, 2),
-                       idesc_e4m3(128, BT), k > 0);
+        for (int k = 0; k < 4; ++k)  // 32 bytes further on: the address field counts 16s
+          umma_e4m3_ss(tmem + d * BT, w + 2 * k, a + 2 * k, idesc_e4m3(128, BT), k > 0);
         umma_commit(&sh.empty[s]);
         umma_commit(&sh.dfull[d]);
-        if (++s == C::STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
-        if (++d == C::SLOTS) {
-          d = 0;
-          dph ^= 1;
-        }
       }
-      int never = 0;  // every MMA completes before tensor memory is released
-      umma_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0, &never, DRAIN_WAIT_NS);
+      if (++s == C::STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
+      if (++d == C::SLOTS) {
+        d = 0;
+        dph ^= 1;
+      }
     }
+    int never = 0;  // every MMA completes before tensor memory is released
+    if (one) umma_commit(&sh.drain);
+    mbar_wait(&sh.drain, 0, &never, DRAIN_WAIT_NS);
   } else {
     // ------------------------------------------------ promotion: warp -> lane quarter warp % 4, column half warp / 4
     const int h = warp >> 2;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // a chunk's scales a_scale * w_scale, [KC][BT]: loaded a chunk ahead, in shared memory for the chunk's columns
+    // a chunk's scales a_scale * w_scale, [KC][BT]: loaded a chunk ahead, multiplied on their way to shared memory
     constexpr int PER = (C::KC * BT + 255) / 256;
-    float next[PER];
+    const int kb = tid & (C::KC - 1);  // a thread's K block of a chunk
+    float na[PER], nw;
     auto load_scales = [&](int i0) {
+      const int i = i0 + kb;
+      nw = i < nblk ? args.w_gscale[(int64_t)nt * args.kst + g0 + i] : 0.0f;
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
-        const int idx = tid + 256 * u, i = i0 + (idx & (C::KC - 1)), m = m0 + idx / C::KC;
-        next[u] = (idx < C::KC * BT && i < nblk && m < args.M)
-                      ? args.a_scale[(int64_t)m * args.kst + g0 + i] * args.w_gscale[(int64_t)nt * args.kst + g0 + i]
-                      : 0.0f;
+        const int idx = tid + 256 * u, m = m0 + idx / C::KC;
+        na[u] = (idx < C::KC * BT && i < nblk && m < args.M) ? args.a_scale[(int64_t)m * args.kst + g0 + i] : 0.0f;
       }
     };
     load_scales(0);
@@ -224,33 +246,31 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
         const int idx = tid + 256 * u;
-        if (idx < C::KC * BT) sc[(idx & (C::KC - 1)) * BT + idx / C::KC] = next[u];
+        if (idx < C::KC * BT) sc[kb * BT + idx / C::KC] = na[u] * nw;
       }
       named_bar_sync(1, 256);  // every warp comes here once a chunk, also after a wait has run out
       load_scales(i0 + C::KC);
       const int n = nblk - i0 < C::KC ? nblk - i0 : C::KC;
       for (int i = 0; i < n; ++i) {
-        if (waitf(&sh.dfull[d], dph)) {
-          tc_fence_after();
-          uint32_t v[HC];
+        waitf(&sh.dfull[d], dph);  // (after one that has run out the sums are of no use, but nothing is out of place)
+        tc_fence_after();
+        uint32_t v[HC];
+        const uint32_t from = tmem + lane_base + d * BT + h * HC;
+        if (HC == 8) tmem_ld8(from, *reinterpret_cast<uint32_t(*)[8]>(v));
+        if (HC == 16) tmem_ld16(from, *reinterpret_cast<uint32_t(*)[16]>(v));
+        if (HC >= 32) tmem_ld32(from, *reinterpret_cast<uint32_t(*)[32]>(v));
+        if (HC == 64) tmem_ld32(from + 32, *reinterpret_cast<uint32_t(*)[32]>(v + HC - 32));
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive_if(&sh.dempty[d], lane == 0);  // (the wait above is the whole warp's)
+        const float* f = sc + i * BT + h * HC;
 #pragma unroll
-          for (int j = 0; j < HC; j += 16) {
-            if (HC < 16) tmem_ld8(tmem + lane_base + d * BT + h * HC, *reinterpret_cast<uint32_t(*)[8]>(v));
-            else tmem_ld16(tmem + lane_base + d * BT + h * HC + j, *reinterpret_cast<uint32_t(*)[16]>(v + j));
-          }
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.dempty[d]);
-          const float* f = sc + i * BT + h * HC;
-#pragma unroll
-          for (int j = 0; j < HC; j += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(f + j);
-            acc[j] = fmaf(__uint_as_float(v[j]), s.x, acc[j]);
-            acc[j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, acc[j + 1]);
-            acc[j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, acc[j + 2]);
-            acc[j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, acc[j + 3]);
-          }
+        for (int j = 0; j < HC; j += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(f + j);
+          acc[j / 2] = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(s.x, s.y),
+                                  acc[j / 2]);
+          acc[j / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
+                                      make_float2(s.z, s.w), acc[j / 2 + 1]);
         }
         if (++d == C::SLOTS) {
           d = 0;
@@ -266,7 +286,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   if (warp < 8) {
     const int r = (warp & 3) * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < HC; ++j) red[((warp >> 2) * HC + j) * TILE_N + r] = acc[j];
+    for (int j = 0; j < HC; ++j) red[((warp >> 2) * HC + j) * TILE_N + r] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
   }
   if (split > 1) cluster_sync();
   else __syncthreads();
@@ -361,11 +381,6 @@ __host__ __device__ inline void pair_tile(int t, int m_tiles, int n_tiles, int& 
   mt = g * PAIR_GROUP + in - nt * rows;
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -399,17 +414,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t bar, uint32_t on
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
       "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(bar),
       "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {

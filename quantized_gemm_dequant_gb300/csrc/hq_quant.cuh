@@ -92,12 +92,13 @@ struct E4m3Scale {
     const float m = __uint_as_float(amax);
     fast = m >= 0x1p-50f && m <= 0x1p126f;
     s = fast ? div_by(m, 448.0f, 1.0f / 448.0f) : __fdiv_rn(m, 448.0f);
-    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     inv = fmaf(inv, fmaf(-s, inv, 1.0f), inv);
   }
+  // (every lane of the warp calls it: one plain scale among them takes the warp the plain way)
   __device__ __forceinline__ uint2 codes(const float2 (&f)[4]) const {
     uint32_t b[4];
-    if (fast) {
+    if (__all_sync(0xffffffffu, fast)) {
       const float2 y = both(inv), ns = both(-s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

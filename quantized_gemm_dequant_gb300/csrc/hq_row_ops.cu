@@ -23,7 +23,7 @@ namespace {
 
 enum RowSrc { SRC_NORM = 0, SRC_ADD_NORM = 1, SRC_SWIGLU = 2 };
 
-// silu(g) * u = g * u / (1 + exp(-g)) of eight pairs.  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's
+// silu(g) * u = g * u / (1 + exp(-g)) of eight values (every lane of the warp calls it).  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's
 // fp32 rounding error, found by an FMA, together with the part of log2(e) below fp32, corrects the power to first order
 // (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to |t| 2^-24.  The reciprocal gets one Newton
 // step.  Two values go through each instruction but the power's and the reciprocal's.  Where a power over- or
@@ -36,14 +36,14 @@ __device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
     t[i] = __fmul2_rn(g[i], both(kHi));
     const float2 d = __ffma2_rn(g[i], both(kLo), __ffma2_rn(g[i], both(kHi), make_float2(-t[i].x, -t[i].y)));
     float2 p;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p.x) : "f"(t[i].x));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(p.y) : "f"(t[i].y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(t[i].x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(t[i].y));
     const float2 q = __fadd2_rn(__ffma2_rn(p, __fmul2_rn(d, both(kLn2)), p), both(1.0f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r[i].x) : "f"(q.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r[i].y) : "f"(q.y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i].x) : "f"(q.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i].y) : "f"(q.y));
     r[i] = __ffma2_rn(r[i], __ffma2_rn(make_float2(-q.x, -q.y), r[i], both(1.0f)), r[i]);
   }
-  if (!(__uint_as_float(absmax_bits(t)) <= 126.0f)) {
+  if (__any_sync(0xffffffffu, !(__uint_as_float(absmax_bits(t)) <= 126.0f))) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (fabsf(t[i].x) > 126.0f) r[i].x = t[i].x > 0.0f ? 0.0f : 1.0f;
@@ -71,11 +71,11 @@ __device__ __forceinline__ T row_reduce(T v, T zero, T (*red)[32], int& turn, F&
   return v;
 }
 
-// One row per CTA, or per warp (WARP, eight rows a CTA), CH chunks of 8 elements per thread; the next row of the same
+// One row per CTA, or per warp (WARP, four rows a CTA), CH chunks of 8 elements per thread; the next row of the same
 // threads is loaded while the current one is reduced and written.  LONG: rows past 2048 chunks on 1024 threads, whose
 // registers leave no room for that, nor for the norm's weights.
 template <int SRC, int OUT, int CH, bool WARP, bool LONG>
-__global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) row_kernel(const RowArgs a) {
   __shared__ float red_f[2][32];
   __shared__ uint32_t red_u[2][32];
   constexpr bool NORM = SRC != SRC_SWIGLU;
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int n = WARP ? 32 : blockDim.x;
   const int chunks = a.width >> 3;
-  const int64_t step = (int64_t)gridDim.x * (WARP ? 8 : 1);
-  int64_t row = (int64_t)blockIdx.x * (WARP ? 8 : 1) + (WARP ? (threadIdx.x >> 5) : 0);
+  const int64_t step = (int64_t)gridDim.x * (WARP ? 4 : 1);
+  int64_t row = (int64_t)blockIdx.x * (WARP ? 4 : 1) + (WARP ? (threadIdx.x >> 5) : 0);
   pdl_trigger();
   pdl_wait();
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
       if (TWO) vb[j] = c < chunks ? pb[c] : none;
     }
   };
+  const float width = (float)a.width, inv_width = __frcp_rn(width);
   if (!LONG) {
     if (row < a.rows) load(row);
     if (NORM) {
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
         float2 g[4];
         bf16x8_to_f32x2(LONG ? (c < chunks ? second(row)[c] : none) : vb[LONG ? 0 : j], g);
         if (SRC == SRC_SWIGLU) {
-          silu_mul(f[j], g);
+          if (!WARP || j * n < chunks) silu_mul(f[j], g);  // (a warp's short row leaves its last chunks out)
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[j][i] = __fadd2_rn(f[j][i], g[i]);
@@ -147,7 +148,11 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
         return row_reduce<WARP>((s[0].x + s[1].x) + (s[0].y + s[1].y), 0.0f, red_f, turn_f, add);
       };
       const float ss = squares();
-      float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.width) + a.eps));
+      // 1 / sqrt(mean + eps): the approximation and one Newton step
+      const float v = div_by(ss, width, inv_width) + a.eps;
+      float rstd;
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rstd) : "f"(v));
+      rstd = fmaf(rstd, fmaf(-0.5f * v * rstd, rstd, 0.5f), rstd);
       // A sum that overflowed, or one that lost small squares where eps does not cover them, is taken again with the
       // row divided by a power of two near its largest magnitude.
       if (!(ss <= FLT_MAX) || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
@@ -188,8 +193,10 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
         const E4m3Scale s(m);
         if (t == 0) a.scale[row] = s.s;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-          if (t + j * n < chunks) o[t + j * n] = s.codes(f[j]);
+        for (int j = 0; j < CH; ++j) {
+          const uint2 q = s.codes(f[j]);
+          if (t + j * n < chunks) o[t + j * n] = q;
+        }
       } else {
         // the 16 chunks of a block are 16 neighbouring lanes (the row's threads are a multiple of 32)
 #pragma unroll
@@ -199,43 +206,54 @@ __global__ void __launch_bounds__(WARP ? 256 : (CH == 1 || LONG ? 1024 : 512)) r
           for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
           const E4m3Scale s(m);
           const int c = t + j * n;
-          if (c < chunks) {
-            o[c] = s.codes(f[j]);
-            if ((c & 15) == 0) a.scale[row * (a.width >> 7) + (c >> 4)] = s.s;
-          }
+          const uint2 q = s.codes(f[j]);
+          if (c < chunks) o[c] = q;
+          if (c < chunks && (t & 15) == 0) a.scale[row * (a.width >> 7) + (c >> 4)] = s.s;
         }
       }
     }
   }
 }
 
-// A scale per 128 outputs needs no statistics of the row: every thread takes UNROLL chunks of 8 outputs, all loads
-// first; 16 neighbouring lanes hold a block.
+// A scale per 128 outputs needs no statistics of the row: every thread takes U chunks of 8 outputs, all loads first; 16
+// neighbouring lanes hold a block.
 constexpr int BQ_THREADS = 256;
-constexpr int BQ_UNROLL = 2;
-template <bool SWIGLU>
-__global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __restrict__ x, int64_t n8, uint32_t per_row,
+// i / d for 0 <= i < n.  Up to n = 2^31 by a multiplication: with m = floor(2^(31 + s) / d) + 1 and 2^s >= d the error
+// of i m / 2^(31 + s) is below i / 2^(31 + s) < 1 / d.  (Division is a software routine.)
+struct RowDivide {
+  uint32_t d, m, shift;  // m = 0: plain division
+  RowDivide(int64_t n, uint32_t d_) : d(d_), m(0), shift(0) {
+    if (n > ((int64_t)1 << 31)) return;
+    while ((1u << (shift + 1)) < d) ++shift;  // 2^(shift + 1) >= d, and m below 2^32 as d > 2^shift
+    m = (uint32_t)(((uint64_t)1 << (32 + shift)) / d) + 1u;
+  }
+  __device__ __forceinline__ int64_t of(int64_t i) const {
+    return m ? (int64_t)(__umulhi((uint32_t)i, m) >> shift) : i / d;
+  }
+};
+template <bool SWIGLU, int U>
+__global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __restrict__ x, int64_t n8, RowDivide per_row,
                                                                  uint2* __restrict__ q, float* __restrict__ s_out) {
   pdl_trigger();
   pdl_wait();
-  uint4 va[BQ_UNROLL], vb[BQ_UNROLL];
-  const int64_t base = (int64_t)blockIdx.x * (BQ_THREADS * BQ_UNROLL) + threadIdx.x;
+  uint4 va[U], vb[U];
+  const int64_t base = (int64_t)blockIdx.x * (BQ_THREADS * U) + threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < BQ_UNROLL; ++j) {
+  for (int j = 0; j < U; ++j) {
     const int64_t i = base + j * BQ_THREADS;
     va[j] = vb[j] = make_uint4(0u, 0u, 0u, 0u);
     if (i < n8) {
-      int64_t at = i;
-      if (SWIGLU) {  // [gate | up] rows; 32-bit division where it fits (the 64-bit one is a long software routine)
-        const int64_t r = n8 <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / per_row) : i / per_row;
-        at = i + r * per_row;
-        vb[j] = __ldg(x + at + per_row);
+      if (SWIGLU) {  // [gate | up] rows
+        const uint4* p = x + i + per_row.of(i) * per_row.d;
+        va[j] = __ldg(p);
+        vb[j] = __ldg(p + per_row.d);
+      } else {
+        va[j] = __ldg(x + i);
       }
-      va[j] = __ldg(x + at);
     }
   }
 #pragma unroll
-  for (int j = 0; j < BQ_UNROLL; ++j) {
+  for (int j = 0; j < U; ++j) {
     const int64_t i = base + j * BQ_THREADS;
     float2 f[4];
     bf16x8_to_f32x2(va[j], f);
@@ -248,10 +266,9 @@ __global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __
 #pragma unroll
     for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
     const E4m3Scale s(m);
-    if (i < n8) {
-      q[i] = s.codes(f);
-      if ((threadIdx.x & 15) == 0) s_out[i >> 4] = s.s;
-    }
+    const uint2 c = s.codes(f);
+    if (i < n8) q[i] = c;
+    if (i < n8 && (threadIdx.x & 15) == 0) s_out[i >> 4] = s.s;
   }
 }
 
@@ -269,7 +286,7 @@ int sms() {
 template <int SRC, int OUT, int CH, bool WARP, bool LONG = false>
 cudaError_t launch_row(const RowArgs& a, int threads, cudaStream_t stream) {
   void (*k)(RowArgs) = row_kernel<SRC, OUT, CH, WARP, LONG>;
-  const int64_t need = WARP ? (a.rows + 7) / 8 : a.rows;
+  const int64_t need = WARP ? (a.rows + 3) / 4 : a.rows;
   int64_t room = sms();
   if (need > room) {  // CTAs an SM holds, asked once for each CTA size
     static std::atomic<int> known[33];
@@ -288,10 +305,10 @@ cudaError_t launch_rows(const RowArgs& a, cudaStream_t stream) {
   const int chunks = a.width / 8;
   const auto threads = [&](int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; };
   // Rows that a warp holds in four chunks a lane, and enough of them to fill the SMs' warps: no barriers.
-  if (chunks <= 128 && a.rows >= 2048) return launch_row<SRC, OUT, 4, true>(a, 256, stream);
+  if (chunks <= 128 && a.rows >= 2048) return launch_row<SRC, OUT, 4, true>(a, 128, stream);
   // Few rows: as many threads as the row has chunks, for the shortest chain of work.
   if (a.rows <= 2 * sms() && chunks <= 1024) return launch_row<SRC, OUT, 1, false>(a, threads(1), stream);
-  if (chunks <= 512) return launch_row<SRC, OUT, 2, false>(a, threads(2), stream);
+  if (chunks <= 256) return launch_row<SRC, OUT, 2, false>(a, threads(2), stream);
   if (chunks <= 2048) return launch_row<SRC, OUT, 4, false>(a, threads(4), stream);
   return launch_row<SRC, OUT, 4, false, true>(a, threads(4), stream);
 }
@@ -315,12 +332,17 @@ cudaError_t launch_swiglu_token(const RowArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_block_quant(bool swiglu, const void* x, int64_t rows, int64_t width, void* data, void* scale,
                                cudaStream_t stream) {
-  const int64_t n8 = rows * (width >> 3), per_cta = BQ_THREADS * BQ_UNROLL;
-  const int64_t grid = (n8 + per_cta - 1) / per_cta;
+  const int64_t n8 = rows * (width >> 3);
+  // One chunk a thread where that leaves no SM more than two CTAs (16 x 7168 SwiGLU: 2.4 -> 2.05 us), else two of the
+  // SwiGLU (four: 53.5 -> 55 us at 8192 x 7168) and four of plain rows (two: 28.7 -> 30.4 us at 8192 x 7168).
+  const int unroll = n8 <= (int64_t)2 * sms() * BQ_THREADS ? 1 : (swiglu ? 2 : 4);
+  const int64_t grid = (n8 + BQ_THREADS * unroll - 1) / (BQ_THREADS * unroll);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_kernel(swiglu ? block_quant_kernel<true> : block_quant_kernel<false>, dim3((unsigned)grid),
-                       dim3(BQ_THREADS), 0, stream, static_cast<const uint4*>(x), n8, (uint32_t)(width >> 3),
-                       static_cast<uint2*>(data), static_cast<float*>(scale));
+  void (*k)(const uint4*, int64_t, RowDivide, uint2*, float*) =
+      swiglu ? (unroll == 1 ? block_quant_kernel<true, 1> : block_quant_kernel<true, 2>)
+             : (unroll == 1 ? block_quant_kernel<false, 1> : block_quant_kernel<false, 4>);
+  return launch_kernel(k, dim3((unsigned)grid), dim3(BQ_THREADS), 0, stream, static_cast<const uint4*>(x), n8,
+                       RowDivide(n8, (uint32_t)(width >> 3)), static_cast<uint2*>(data), static_cast<float*>(scale));
 }
 
 }  // namespace hq

@@ -20,7 +20,7 @@ def _norm(**kw):
 @pytest.mark.parametrize("status,changed", [
     ("UNSUPPORTED", dict(act_type=hq.HQ_A_NVFP4)), ("UNSUPPORTED", dict(act_type=0)),
     ("INVALID_ARG", dict(T=-1)), ("INVALID_ARG", dict(K=0)), ("INVALID_ARG", dict(eps=-1.0)),
-    ("INVALID_ARG", dict(eps=float("nan"))), ("ALIGNMENT", dict(K=200)),
+    ("INVALID_ARG", dict(eps=float("nan"))), ("INVALID_ARG", dict(eps=float("inf"))), ("ALIGNMENT", dict(K=200)),
     ("ALIGNMENT", dict(act_type=hq.HQ_A_E4M3_TOKEN, K=24)), ("ALIGNMENT", dict(act_type=hq.HQ_A_BF16, K=12)),
     ("UNSUPPORTED", dict(K=32768 + 128, x_stride=1 << 16, residual_stride=1 << 16, residual_out_stride=1 << 16)),
     ("INVALID_ARG", dict(residual=None)), ("INVALID_ARG", dict(residual_out=None)),
