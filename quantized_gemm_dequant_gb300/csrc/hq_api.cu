@@ -28,6 +28,7 @@ cudaError_t launch_gemm_mxfp4x(const GemmArgs& a, int bt, int grid, cudaStream_t
 cudaError_t launch_gemm_small(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_small_fmt(int dec, const GemmArgs& a, int bt, int grid, cudaStream_t stream);
 cudaError_t launch_gemm_block(const GemmArgs& a, int bt, int grid, cudaStream_t stream);
+int gemm_block_room(int bt, int sk);
 cudaError_t launch_gemm_block_pair(const GemmArgs& a, int bn, int grid, cudaStream_t stream);
 cudaError_t launch_splitk_reduce(int path, const GemmArgs& a, int bt, int gemm_grid, int grid, cudaStream_t stream);
 cudaError_t launch_combine_round(const float* acc, int64_t n, uint16_t* c, cudaStream_t stream);
@@ -228,34 +229,48 @@ void plan_tiles(Plan& p, int64_t M_or_T, int32_t topk, bool moe, int64_t E, int6
 }
 
 // Block-scaled e4m3 products, no workspace past the header: the CTA-pair kernel (256 tokens by 128 or 256 features), or
-// the kernel for few tokens (a token tile, and CTAs per tile: a cluster that splits K).  HQ_TUNE: kernel 0 / 1, bt the
-// pair's features or the token tile, sk the CTAs per tile.
+// the kernel for few tokens (a token tile, and CTAs per tile: a cluster that splits K).
+//
+// The choice is the least of the candidates' estimated times: 3 us a call, then for every wave of tiles (or of clusters,
+// as many as the device holds at once) 1 us, 0.5 us more where sums cross a cluster, and the K blocks of a CTA at what
+// one takes where memory does not hold it up, measured at K = 16384 with one wave: 420 and 285 ns (the pair kernel's 256
+// and 128 features), 297, 269, 254 and 243 ns (128, 64, 32 and 16 tokens).  Estimates within a microsecond of 46 of 52
+// measured calls of 64 to 512 tokens, N 1001 to 14336, K 2048 to 16384; the fastest candidate or one within 8% of it in
+// all of them.
+// HQ_TUNE: kernel 0 / 1 (pair / few tokens), bt the pair's features or the token tile, sk the CTAs per tile.
 void plan_block(Plan& p, int64_t M, int sms) {
   TuneChoice tc;
   tune_env_override(tc);
-  // the pair kernel reads the packed weights as rows of 128 bytes, whose index is an int
-  const bool may_pair = p.n_tiles * p.kst < ((int64_t)1 << 24);
   p.ws_bytes = kHeaderBytes;
-  bool pair = M > 256;
-  if (tc.kernel >= 0) pair = tc.kernel == 0;
-  if (pair && may_pair) {
-    p.pair = tc.bt == 128 || tc.bt == 256 ? tc.bt : 256;
-    p.bt = 256;
-    p.m_tiles = (M + 255) / 256;
-    p.max_tiles = p.m_tiles * (p.pair == 256 ? (p.n_tiles + 1) / 2 : p.n_tiles);
-    const int64_t pairs = sms / 2 < 1 ? 1 : sms / 2;
-    p.grid = (int)(2 * (p.max_tiles < pairs ? p.max_tiles : pairs));
-    return;
+  int64_t best = INT64_MAX;
+  const auto take = [&](int pair, int bt, int sk, int64_t tiles, int64_t m_tiles, int64_t room, int64_t ns) {
+    const int64_t ctas = tiles * sk, waves = (ctas + room - 1) / room;
+    const int64_t cost = waves * (((p.kst + sk - 1) / sk) * ns + 1000 + (sk > 1 ? 500 : 0));
+    if (cost >= best) return;
+    best = cost;
+    p.pair = pair;
+    p.bt = bt;
+    p.sk = sk;
+    p.m_tiles = m_tiles;
+    p.max_tiles = tiles;
+    p.grid = (int)(pair ? 2 * (tiles < room ? tiles : room) : ctas);
+  };
+  // the pair kernel reads the packed weights as rows of 128 bytes, whose index is an int
+  if (tc.kernel != 1 && p.n_tiles * p.kst < ((int64_t)1 << 24)) {
+    const int64_t m = (M + 255) / 256, pairs = sms / 2 < 1 ? 1 : sms / 2;
+    if (tc.bt != 128) take(256, 256, 1, m * ((p.n_tiles + 1) / 2), m, pairs, 420);
+    if (tc.bt != 256) take(128, 256, 1, m * p.n_tiles, m, pairs, 285);
+    if (tc.kernel == 0) best = 0;
   }
-  p.bt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
-  if (tc.bt == 16 || tc.bt == 32 || tc.bt == 64 || tc.bt == 128) p.bt = tc.bt;
-  p.m_tiles = (M + p.bt - 1) / p.bt;
-  p.max_tiles = p.m_tiles * p.n_tiles;
-  const int64_t room = (int64_t)sms * (p.bt <= 64 ? 2 : 1);
-  p.sk = 1;
-  while (p.sk < 8 && p.max_tiles * p.sk * 2 <= room && p.kst >= 4 * p.sk) p.sk *= 2;
-  if (tc.sk >= 1 && tc.sk <= 8 && tc.sk <= p.kst) p.sk = tc.sk;
-  p.grid = (int)(p.max_tiles * p.sk);
+  int bt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  if (tc.kernel == 1 && (tc.bt == 16 || tc.bt == 32 || tc.bt == 64 || tc.bt == 128)) bt = tc.bt;
+  const int64_t m = (M + bt - 1) / bt;
+  for (int sk = 1; sk <= 8 && sk <= p.kst; ++sk) {
+    if (tc.kernel == 1 && tc.sk >= 1 && tc.sk <= 8 && tc.sk <= p.kst && sk != tc.sk) continue;
+    const int per_sm = bt <= 32 ? 2 : 1, held = gemm_block_room(bt, sk);
+    take(0, bt, sk, m * p.n_tiles, m, held > 0 ? held : (int64_t)(per_sm * sms / sk < 1 ? 1 : per_sm * sms / sk) * sk,
+         bt == 128 ? 297 : (bt == 64 ? 269 : (bt == 32 ? 254 : 243)));
+  }
 }
 
 // The built-in rule, then the tuned table's row for (format class, size bucket), then HQ_TUNE; every choice is

@@ -73,30 +73,44 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 }
 
 // ------------------------------------------------------------------ few tokens
-// Weights are the MMA's A operand (128 output features, one per tensor-memory lane) and BT tokens its B operand, so
-// that a step of one token still fills the MMA's rows.  A tile is 128 features by BT tokens; its K blocks are split
-// over the CTAs of a cluster (up to 8), which read each other's fp32 sums from shared memory and add them in rank
-// order: one kernel, no workspace, and the result does not depend on timing.
+// A tile is 128 output features by BT tokens; its K blocks are split over the CTAs of a cluster (up to 8), which read
+// each other's fp32 sums from shared memory and add them in rank order: one kernel, no workspace, and the result does
+// not depend on timing.
 //
-// Bound by the weights' bytes: every CTA keeps a ring of 16 KB weight blocks in flight.
+// Up to 32 tokens the weights are the MMA's A operand (a feature per tensor-memory lane) and the tokens its B operand,
+// so that a step of one token still fills the MMA's rows; a column's scale is then its token's, read from shared memory
+// by every warp (128 bytes into the registers for each column).  From 64 tokens on that read takes longer than the rest,
+// and the tokens are the A operand: a lane is a token and its scale one register (128 tokens, N = 14336, K = 4096: 19.5
+// -> 14.8 us).  The A operand of 64 tokens is still 128 rows: the MMA reads what follows them in shared memory, whatever
+// it is, into sums that nothing reads.
+//
+// Bound by the weights' bytes: every CTA keeps a ring of 16 KB weight blocks in flight, and two warps issue the MMAs of
+// every second block each (waits and issue take a warp some 500 cycles a block, as long as its bytes take to arrive).
 template <int BT>
 struct BlkCfg {
+  static constexpr bool LANES = BT >= 64;         // tokens on the lanes
   static constexpr int STAGE = 16384 + BT * 128;  // weight block, token rows x 128 bytes
-  static constexpr int PER_SM = BT <= 64 ? 2 : 1;
-  static constexpr int STAGES = BT == 16 ? 6 : (BT == 32 ? 5 : (BT == 64 ? 4 : 6));
-  static constexpr int SLOTS = 4;                 // accumulators in tensor memory
-  static constexpr int COLS = SLOTS * BT;         // 64 .. 512: two CTAs of up to 64 tokens share an SM's 512 columns
-  static constexpr int KC = 8;                    // K blocks per chunk of scales
+  static constexpr int PER_SM = LANES ? 1 : 2;
+  static constexpr int STAGES = BT == 16 ? 6 : (BT == 32 ? 5 : (BT == 64 ? 8 : 6));
+  static constexpr int SLOTS = 4;                    // accumulators in tensor memory
+  static constexpr int WIDTH = LANES ? TILE_N : BT;  // columns of one
+  static constexpr int COLS = SLOTS * WIDTH;         // 64, 128 (two CTAs share an SM's 512 columns), or all 512
+  static constexpr int HC = WIDTH / 2;               // columns of a promoting warp
+  static constexpr int ACTIVE = LANES ? BT / 16 : 8;  // promoting warps
+  static constexpr int KC = 8;                       // K blocks per chunk of scales
+  static constexpr int PITCH = LANES ? TILE_N + 4 : TILE_N;  // floats of a token's sums in shared memory
   static constexpr int RING = STAGES * STAGE;
   static constexpr int SCALES = 2 * KC * BT * 4;
-  static constexpr int SMEM = RING + SCALES + 1024 /*align*/ + 512 /*barriers*/;
-  static_assert(RING >= BT * TILE_N * 4, "the sums overlay the ring");
+  static constexpr int TAIL = SCALES + 512 /*barriers*/;
+  // behind the ring there is as much as the MMA reads past the last stage's 64 tokens
+  static constexpr int SMEM = RING + (BT == 64 && TAIL < 8192 ? 8192 : TAIL) + 1024 /*align*/;
+  static_assert(RING >= BT * PITCH * 4, "the sums overlay the ring");
   // at most PER_SM CTAs on an SM, so that their tensor memory always fits and no CTA of a cluster waits for columns
   // that another cluster's CTA holds
   static_assert((PER_SM + 1) * (SMEM + 1024) > 228 * 1024 && PER_SM * (SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 };
-constexpr int BLK_THREADS = 320;
-constexpr int BLK_LOAD_WARP = 8, BLK_MMA_WARP = 9;
+constexpr int BLK_THREADS = 352;
+constexpr int BLK_LOAD_WARP = 8, BLK_MMA_WARP = 9;  // 9 and 10 issue the MMAs
 
 template <int BT>
 struct BlkSmem {
@@ -143,9 +157,9 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     }
     for (int d = 0; d < C::SLOTS; ++d) {
       mbar_init(&sh.dfull[d], 1);
-      mbar_init(&sh.dempty[d], 8);
+      mbar_init(&sh.dempty[d], C::ACTIVE);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&args.tmap_a);
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     return ok;
   };
 
-  constexpr int HC = BT / 2;
+  constexpr int HC = C::HC;
   float2 acc[HC / 2];
 #pragma unroll
   for (int j = 0; j < HC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -192,29 +206,33 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
       for (int k = 0; k < C::STAGES; ++k)
         if (n > k) mbar_wait(&sh.full[k], (uint32_t)(((n - 1 - k) / C::STAGES) & 1), &never, DRAIN_WAIT_NS);
     }
-  } else if (warp == BLK_MMA_WARP) {
+  } else if (warp >= BLK_MMA_WARP) {
     // (the whole warp runs the loop, so that descriptors and addresses are uniform registers; one lane issues)
     const bool one = elect_one();
     const uint32_t ring = smem_u32(smem);
-    int s = 0, d = 0;
+    int s = warp - BLK_MMA_WARP, d = warp - BLK_MMA_WARP;
     uint32_t ph = 0, dph = 0;
-    for (int i = 0; i < nblk; ++i) {
+    static_assert(C::STAGES >= 2 && C::SLOTS % 2 == 0, "a warp takes every second stage and slot");
+    for (int i = warp - BLK_MMA_WARP; i < nblk; i += 2) {
       if (!__all_sync(0xffffffffu, waitf(&sh.dempty[d], dph ^ 1) && waitf(&sh.full[s], ph))) break;
       tc_fence_after();
       const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2), a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
       if (one) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 bytes further on: the address field counts 16s
-          umma_e4m3_ss(tmem + d * BT, w + 2 * k, a + 2 * k, idesc_e4m3(128, BT), k > 0);
+          umma_e4m3_ss(tmem + d * C::WIDTH, (C::LANES ? a : w) + 2 * k, (C::LANES ? w : a) + 2 * k,
+                       idesc_e4m3(128, C::WIDTH), k > 0);
         umma_commit(&sh.empty[s]);
         umma_commit(&sh.dfull[d]);
       }
-      if (++s == C::STAGES) {
-        s = 0;
+      s += 2;
+      if (s >= C::STAGES) {
+        s -= C::STAGES;
         ph ^= 1;
       }
-      if (++d == C::SLOTS) {
-        d = 0;
+      d += 2;
+      if (d >= C::SLOTS) {
+        d -= C::SLOTS;
         dph ^= 1;
       }
     }
@@ -224,6 +242,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   } else {
     // ------------------------------------------------ promotion: warp -> lane quarter warp % 4, column half warp / 4
     const int h = warp >> 2;
+    const bool active = !C::LANES || (warp & 3) * 32 < BT;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // a chunk's scales a_scale * w_scale, [KC][BT]: loaded a chunk ahead, multiplied on their way to shared memory
     constexpr int PER = (C::KC * BT + 255) / 256;
@@ -250,12 +269,12 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
       }
       named_bar_sync(1, 256);  // every warp comes here once a chunk, also after a wait has run out
       load_scales(i0 + C::KC);
-      const int n = nblk - i0 < C::KC ? nblk - i0 : C::KC;
+      const int n = !active ? 0 : (nblk - i0 < C::KC ? nblk - i0 : C::KC);
       for (int i = 0; i < n; ++i) {
         waitf(&sh.dfull[d], dph);  // (after one that has run out the sums are of no use, but nothing is out of place)
         tc_fence_after();
         uint32_t v[HC];
-        const uint32_t from = tmem + lane_base + d * BT + h * HC;
+        const uint32_t from = tmem + lane_base + d * C::WIDTH + h * HC;
         if (HC == 8) tmem_ld8(from, *reinterpret_cast<uint32_t(*)[8]>(v));
         if (HC == 16) tmem_ld16(from, *reinterpret_cast<uint32_t(*)[16]>(v));
         if (HC >= 32) tmem_ld32(from, *reinterpret_cast<uint32_t(*)[32]>(v));
@@ -263,10 +282,11 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive_if(&sh.dempty[d], lane == 0);  // (the wait above is the whole warp's)
-        const float* f = sc + i * BT + h * HC;
+        const float* f = sc + i * BT + (C::LANES ? (warp & 3) * 32 + lane : h * HC);
+        const float own = *f;
 #pragma unroll
         for (int j = 0; j < HC; j += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(f + j);
+          const float4 s = C::LANES ? make_float4(own, own, own, own) : *reinterpret_cast<const float4*>(f + j);
           acc[j / 2] = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(s.x, s.y),
                                   acc[j / 2]);
           acc[j / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
@@ -282,11 +302,18 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 
   // ------------------------------------------------ sums -> shared memory -> output rows
   __syncthreads();  // every copy has landed and every MMA has read its stage
-  float* red = reinterpret_cast<float*>(smem);  // [BT][128]
-  if (warp < 8) {
+  float* red = reinterpret_cast<float*>(smem);  // [BT][PITCH]
+  if (warp < 8 && (!C::LANES || (warp & 3) * 32 < BT)) {
     const int r = (warp & 3) * 32 + lane;
+    if (C::LANES) {
 #pragma unroll
-    for (int j = 0; j < HC; ++j) red[((warp >> 2) * HC + j) * TILE_N + r] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+      for (int j = 0; j < HC; j += 4)
+        *reinterpret_cast<float4*>(red + r * C::PITCH + (warp >> 2) * HC + j) =
+            make_float4(acc[j / 2].x, acc[j / 2].y, acc[j / 2 + 1].x, acc[j / 2 + 1].y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < HC; ++j) red[((warp >> 2) * HC + j) * C::PITCH + r] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+    }
   }
   if (split > 1) cluster_sync();
   else __syncthreads();
@@ -299,10 +326,10 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     const bool wide = (args.N & 3) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 7) == 0;
     for (int t = warp * split + rank; t < nrows; t += 8 * split) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const uint32_t at = smem_u32(red + t * TILE_N + lane * 4);
+      const uint32_t at = smem_u32(red + t * C::PITCH + lane * 4);
       for (int k = 0; k < split; ++k) {
         const float4 p = split > 1 ? ld_cluster_f32x4(cluster_addr(at, (uint32_t)k))
-                                   : *reinterpret_cast<const float4*>(red + t * TILE_N + lane * 4);
+                                   : *reinterpret_cast<const float4*>(red + t * C::PITCH + lane * 4);
         v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
       }
       int row = m0 + t;
@@ -354,7 +381,9 @@ struct PairCfg {
   static constexpr int SGROUP = SK * TILES * 128;  // [K block][weight tile][token]
   static constexpr int SGROUPS = 2;
   static constexpr int SCALES = SGROUPS * SGROUP * 4;
-  static constexpr int SMEM = STAGES * STAGE + SCALES + 1024 /*align*/ + 512 /*barriers*/;
+  static constexpr int OUT_PITCH = 18;  // bf16 values of a row of 16 on their way out
+  static constexpr int OUT = 8 * 32 * OUT_PITCH * 2;
+  static constexpr int SMEM = STAGES * STAGE + SCALES + OUT + 1024 /*align*/ + 512 /*barriers*/;
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 // warps 0-7 promote, 8 loads, 9 and 10 issue the MMAs (of the cluster's first CTA), 11 multiplies the scales
@@ -430,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);  // [SGROUPS][4][TILES][128]
-  PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE + C::SCALES);
+  PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE + C::SCALES + C::OUT);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler sees it
   const int rank = (int)(blockIdx.x & 1), pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
@@ -711,31 +740,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
 #if HQ_DEBUG_BOUNDS
       if (row >= 0) row = dbg_row(row, args.dbg_c_rows, args.status);
 #endif
-      if (row >= 0) {
-        const int n0 = BN == 256 ? nt * 128 : nt * 128 + h * C::HC;
-        uint16_t* o = args.c + (int64_t)row * args.N + n0;
-        const bool wide = (args.N & 15) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 31) == 0;
+      const int n0 = BN == 256 ? nt * 128 : nt * 128 + h * C::HC;
+      const bool wide = (args.N & 15) == 0 && (reinterpret_cast<uintptr_t>(args.c) & 31) == 0;
+      uint16_t* stage = reinterpret_cast<uint16_t*>(scales + C::SGROUPS * C::SGROUP) + warp * (32 * C::OUT_PITCH);
 #pragma unroll
-        for (int j = 0; j < C::HC; j += 16) {
-          if (n0 + j >= args.N) break;
-          float y[16];
+      for (int j = 0; j < C::HC; j += 16) {
+        if (n0 + j >= args.N) break;
+        float y[16];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[2 * k] = acc[j / 2 + k].x, y[2 * k + 1] = acc[j / 2 + k].y;
-          if (args.bias) {
+        for (int k = 0; k < 8; ++k) y[2 * k] = acc[j / 2 + k].x, y[2 * k + 1] = acc[j / 2 + k].y;
+        if (args.bias) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (n0 + j + k < args.N) y[k] += bf16_to_f32(args.bias[n0 + j + k]);
+          for (int k = 0; k < 16; ++k)
+            if (n0 + j + k < args.N) y[k] += bf16_to_f32(args.bias[n0 + j + k]);
+        }
+        uint32_t p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = pack_bf16x2(y[2 * k], y[2 * k + 1]);
+        if (wide) {  // a whole 32-byte sector of the thread's row
+          if (row >= 0) st_global_32b(args.c + (int64_t)row * args.N + n0 + j, p);
+        } else {
+          // rows that start anywhere: 16 lanes write 16 neighbouring outputs of a row
+#pragma unroll
+          for (int k = 0; k < 8; ++k) reinterpret_cast<uint32_t*>(stage + lane * C::OUT_PITCH)[k] = p[k];
+          __syncwarp();
+          const int c = lane & 15;
+#pragma unroll 4
+          for (int r = lane >> 4; r < 32; r += 2) {
+            const int to = __shfl_sync(0xffffffffu, row, r);
+            if (to >= 0 && n0 + j + c < args.N) args.c[(int64_t)to * args.N + n0 + j + c] = stage[r * C::OUT_PITCH + c];
           }
-          uint32_t p[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) p[k] = pack_bf16x2(y[2 * k], y[2 * k + 1]);
-          if (wide) {
-            st_global_32b(o + j, p);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (n0 + j + k < args.N) o[j + k] = (uint16_t)(p[k / 2] >> (16 * (k & 1)));
-          }
+          __syncwarp();
         }
       }
     }
