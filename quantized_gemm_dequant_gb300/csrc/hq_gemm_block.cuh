@@ -24,14 +24,15 @@ __device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
-// mbar_wait for waits that are short and on the critical path of every K block: the test suspends the thread only as
-// long as the hardware sees fit.  (With a time hint it becomes a sleep, whose end comes hundreds of cycles late.)
+// mbar_wait for waits that are short and on the critical path of every K block: its tests suspend the thread only as
+// long as the hardware sees fit (with a time hint they become sleeps, whose end comes hundreds of cycles late), the
+// first of them too unless the limit is below a microsecond.
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (limit_ns >= 1000 ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
   const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;  // at least limit_ns at clocks up to 3 GHz
   for (;;) {
+    if (clock64() - c0 >= lim || *abort) return false;
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort || clock64() - c0 >= lim) return false;
   }
 }
 
@@ -730,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
           fn = *at;
         }
       }
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;  // (a warp's lanes stay together: tensor-memory reads are the warp's)
       // ------------------------------------------------ output: a thread's row, HC columns of it
       int mt, ft;
       pair_tile(t, args.m_tiles, f_tiles, mt, ft);
