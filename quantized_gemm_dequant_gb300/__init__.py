@@ -201,6 +201,7 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
 _bf16, _f32, _i32t, _i64t = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_u8, _empty = torch.uint8, torch.empty
 _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -373,17 +374,19 @@ def gemm(fmt, act, packed, M, bias=None, out=None, workspace=None, stream=None):
     """C[M, N] bf16 = A . Wdeq^T (+ bias).  `act` is {'data', 'scale'?, 'gscale'?} of device tensors."""
     w = "hq_gemm"
     N, K, at = fmt.N, fmt.K, fmt.act_type
-    row = _ROW.get(at)
-    dev = _device() if isinstance(act, dict) and row is not None and torch.cuda.is_initialized() else None
-    right = False
-    if dev is not None:  # a call whose tensors are right looks at each of them once, in place
+    row, right = _ROW.get(at), False
+    if row is not None and isinstance(act, dict) and isinstance(packed, torch.Tensor) and packed.is_cuda:
+        # a call whose tensors are right looks at each of them once, in place
+        dev, (mul, div, smul, sdiv, sdt) = _device(), row
         d, s, g = act.get("data"), act.get("scale"), act.get("gscale")
-        mul, div, smul, sdiv, sdt = row
-        right = (d is not None and _has(d, M * (mul * K // div), dev, _bf16 if at == HQ_A_BF16 else None)
-                 and _has(s, M * (smul * K // sdiv if sdiv else smul), dev, sdt)
-                 and _has(g, 4 if at == HQ_A_NVFP4 else 0, dev, _f32) and packed is not None
-                 and _has(packed, packed_bytes(fmt), dev) and _has(bias, 2 * N, dev, _bf16)
-                 and _has(out, 2 * M * N, dev, _bf16) and _has(workspace, 0, dev))
+        right = (isinstance(d, torch.Tensor) and d.get_device() == dev and d.is_contiguous()
+                 and d.nbytes >= M * (mul * K // div) and (at != HQ_A_BF16 or d.dtype is _bf16)
+                 and (s is None or _has(s, M * (smul * K // sdiv if sdiv else smul), dev, sdt))
+                 and (g is None or _has(g, 4 if at == HQ_A_NVFP4 else 0, dev, _f32))
+                 and packed.get_device() == dev and packed.is_contiguous()
+                 and packed.nbytes >= _lib.hq_packed_bytes(fmt)
+                 and (bias is None or _has(bias, 2 * N, dev, _bf16)) and (out is None or _has(out, 2 * M * N, dev, _bf16))
+                 and (workspace is None or _has(workspace, 0, dev)))
     if right:
         A = Act(d.data_ptr(), None if s is None else s.data_ptr(), None if g is None else g.data_ptr())
         pw, pb = packed.data_ptr(), None if bias is None else bias.data_ptr()
@@ -391,14 +394,13 @@ def gemm(fmt, act, packed, M, bias=None, out=None, workspace=None, stream=None):
         args = _Args(w).act(act, fmt, M).add(packed, "packed", packed_bytes(fmt)).add(bias, "bias", 2 * fmt.N, _BF16)
         args.add(out, "out", 2 * M * fmt.N, _BF16).add(workspace, "workspace")
         pd, ps, pg, pw, pb, _, _ = args.ptrs()
-        A = Act(pd, ps, pg)
+        A, d, dev = Act(pd, ps, pg), act["data"], _device()
     if out is None:
-        out = torch.empty((M, N), dtype=_bf16, device=act["data"].device)
+        out = torch.empty((M, N), dtype=_bf16, device=d.device)
     if workspace is None:
-        workspace = make_workspace(fmt, M, 1, act["data"].device, stream)
-    st = _lib.hq_gemm(ctypes.byref(fmt), ctypes.byref(A), pw, pb, out.data_ptr(), int(M), N, K, workspace.data_ptr(),
-                      workspace.nbytes, (_raw_stream(dev) if right else torch.cuda.current_stream().cuda_stream)
-                      if stream is None else stream.cuda_stream)
+        workspace = make_workspace(fmt, M, 1, d.device, stream)
+    st = _lib.hq_gemm(fmt, A, pw, pb, out.data_ptr(), int(M), N, K, workspace.data_ptr(), workspace.nbytes,
+                      _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st != HQ_OK:
         raise HQError(st, w)
     return out
@@ -574,9 +576,9 @@ def _new_act(at, rows, width, device, stream=None):
         with torch.cuda.stream(stream):  # the new tensors belong to the stream the call runs on
             return _new_act(at, rows, width, device)
     if at == HQ_A_BF16:
-        return {"data": torch.empty((rows, width), dtype=_bf16, device=device)}
-    return {"data": torch.empty((rows, width), dtype=torch.uint8, device=device),
-            "scale": torch.empty((rows, width // 128) if at == HQ_A_E4M3_BLOCK else rows, dtype=_f32, device=device)}
+        return {"data": _empty((rows, width), dtype=_bf16, device=device)}
+    return {"data": _empty((rows, width), dtype=_u8, device=device),
+            "scale": _empty((rows, width // 128) if at == HQ_A_E4M3_BLOCK else rows, dtype=_f32, device=device)}
 
 
 def _out_act(w, at, out, rows, width, dev):
@@ -654,9 +656,12 @@ def add_rms_norm(afmt, x, weight, residual=None, eps=1e-6, residual_out=None, ou
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise HQArgError(w, "x must be a 2-D [T, K] tensor")
     T, K = x.shape
-    sx, sr, so = _row_stride(w, x, "x", T, K), K, K
+    sx = sr = so = K
     dev = _device() if x.is_cuda else None  # (no tensor is on device None: host tensors are refused)
-    right = (x.dtype is _bf16 and x.get_device() == dev and weight is not None and _has(weight, 2 * K, dev, _bf16))
+    if not x.is_contiguous():
+        sx = _row_stride(w, x, "x", T, K)
+    right = (x.dtype is _bf16 and x.get_device() == dev and isinstance(weight, torch.Tensor) and weight.dtype is _bf16
+             and weight.get_device() == dev and weight.is_contiguous() and weight.numel() >= K)
     if residual is not None:
         sr = _row_stride(w, residual, "residual", T, K)
         right = right and residual.dtype is _bf16 and residual.get_device() == dev
@@ -675,7 +680,7 @@ def add_rms_norm(afmt, x, weight, residual=None, eps=1e-6, residual_out=None, ou
     pr = po = 0
     if residual is not None:
         if residual_out is None:
-            residual_out = (torch.empty((T, K), dtype=_bf16, device=x.device) if stream is None else
+            residual_out = (_empty((T, K), dtype=_bf16, device=x.device) if stream is None else
                             _on(stream, torch.empty, (T, K), dtype=_bf16, device=x.device))
         pr, po = residual.data_ptr(), residual_out.data_ptr()
     a = _kv_pack(w, _NORM, at, eps, T, K, x.data_ptr(), sx, pr, sr, weight.data_ptr(), po, so, out["data"].data_ptr(),
