@@ -25,15 +25,25 @@ __device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t adesc, ui
 }
 
 // mbar_wait for waits that are short and on the critical path of every K block: its tests suspend the thread only as
-// long as the hardware sees fit (with a time hint they become sleeps, whose end comes hundreds of cycles late), the
-// first of them too unless the limit is below a microsecond.
+// long as the hardware sees fit.  (With a time hint they become sleeps, whose end comes hundreds of cycles late.)
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (limit_ns >= 1000 ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;  // at least limit_ns at clocks up to 3 GHz
   for (;;) {
     if (clock64() - c0 >= lim || *abort) return false;
     if (mbar_try_wait(bar, parity)) return true;
   }
+}
+// The same where a limit below a microsecond runs out at a phase that is not complete at once: a kernel needs one such
+// wait to end early, the others then see the abort flag.  (In every wait the choice cost 8192 tokens 350 -> 370 us.)
+__device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                 uint64_t limit_ns) {
+  if (mbar_test_wait(bar, parity)) return true;
+  if (limit_ns >= 1000) return mbar_wait_soon(bar, parity, abort, limit_ns);
+  const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;
+  while (clock64() - c0 < lim && !*abort)
+    if (mbar_test_wait(bar, parity)) return true;
+  return false;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -173,12 +183,13 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
+  auto timed_out = [&] {
+    *abort_flag = 1;
+    atomicCAS(args.status, 0, ERR_TIMEOUT);
+    ok = false;
+  };
   auto waitf = [&](uint64_t* bar, uint32_t par) {
-    if (ok && !mbar_wait_soon(bar, par, abort_flag, args.wait_ns)) {
-      *abort_flag = 1;
-      atomicCAS(args.status, 0, ERR_TIMEOUT);
-      ok = false;
-    }
+    if (ok && !mbar_wait_soon(bar, par, abort_flag, args.wait_ns)) timed_out();
     return ok;
   };
 
@@ -215,7 +226,8 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     uint32_t ph = 0, dph = 0;
     static_assert(C::STAGES >= 2 && C::SLOTS % 2 == 0, "a warp takes every second stage and slot");
     for (int i = warp - BLK_MMA_WARP; i < nblk; i += 2) {
-      if (!__all_sync(0xffffffffu, waitf(&sh.dempty[d], dph ^ 1) && waitf(&sh.full[s], ph))) break;
+      if (!ok || !mbar_wait_strict(&sh.full[s], ph, abort_flag, args.wait_ns)) timed_out();
+      if (!__all_sync(0xffffffffu, ok && waitf(&sh.dempty[d], dph ^ 1))) break;
       tc_fence_after();
       const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2), a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
       if (one) {
@@ -526,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
           w0[h] = (nt < args.n_tiles ? nt : args.n_tiles - 1) * kst * 128 + rank * 64;
         }
         for (int b = 0; b < kst; ++b) {
-          if (!mbar_wait_soon(&sh.empty[s], ph ^ 1, abort_flag, args.wait_ns)) {
+          if (!mbar_wait_strict(&sh.empty[s], ph ^ 1, abort_flag, args.wait_ns)) {
             fail();
             break;
           }
@@ -571,8 +583,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
       const uint32_t ring = smem_u32(smem);
       const int h = C::HALVES == 2 ? w : 0;
       constexpr int STEP = C::HALVES == 2 ? 1 : 2;
+      const int b1 = C::HALVES == 2 ? 0 : w;  // the first K block of a tile that this warp takes
+      if (pair < tiles && b1 < kst &&
+          !__all_sync(0xffffffffu, mbar_wait_strict(&sh.full[b1], 0, abort_flag, args.wait_ns)))
+        fail();
       for (int t = pair; t < tiles && ok; t += pairs) {
-        const int b1 = C::HALVES == 2 ? 0 : w;
         int s = (int)((base + b1) % C::STAGES);
         uint32_t ph = ((base + b1) / C::STAGES) & 1;
         for (int b = b1; b < kst; b += STEP) {
