@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libhq.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libhq_debug.so")
 SOURCES = ["hq_api.cu", "hq_pack.cu", "hq_route.cu", "hq_gemm_int4.cu", "hq_gemm_nvfp4.cu", "hq_gemm_mxfp4.cu", "hq_gemm_mxfp4a.cu", "hq_gemm_mxfp4x.cu", "hq_gemm_mxfp4x_comb.cu", "hq_gemm_small.cu", "hq_gemm_small_fmt.cu", "hq_gemm_small_bits.cu", "hq_splitk.cu", "hq_noalloc.cu", "hq_act_quant.cu", "hq_moe_combine.cu", "hq_gemm_int4_comb.cu", "hq_gemm_nvfp4_comb.cu", "hq_gemm_mxfp4_comb.cu",
-           "hq_gemm_block.cu", "hq_row_ops.cu",
+           "block/hq_gemm_block.cu", "block/hq_row_ops.cu",
            "kv/hq_kv_api.cu", "kv/hq_kv_write.cu", "kv/hq_kv_read.cu",
            "kv/hq_kv_attention_bf16.cu", "kv/hq_kv_attention_e4m3.cu", "kv/hq_kv_attention_nvfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,7 +49,8 @@ def build(verbose=False, force=False, debug=False):
     flags = FLAGS + (["-DHQ_DEBUG_BOUNDS=1"] if debug else [])
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
-    headers = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "kv")) for f in os.listdir(d)
+    headers = [os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "kv"), os.path.join(CSRC, "block"))
+               for f in os.listdir(d)
                if f.endswith((".cuh", ".h"))]
     headers.append(os.path.join(os.path.dirname(HERE), "include", "hq.h"))
     jobs = []

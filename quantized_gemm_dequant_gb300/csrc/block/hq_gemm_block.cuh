@@ -5,7 +5,7 @@
 // block is multiplied into an accumulator of its own in tensor memory (four tcgen05.mma kind::f8f6f4 steps of 32 K),
 // and warps add it, times its scale, to fp32 sums in registers ("promotion") while the MMA fills the next slot.
 #pragma once
-#include "hq_gemm_kernel.cuh"
+#include "../hq_gemm_kernel.cuh"
 
 namespace hq {
 

@@ -12,9 +12,9 @@
 
 #include <atomic>
 
-#include "hq_launch.h"
-#include "hq_ptx.cuh"
-#include "hq_quant.cuh"
+#include "../hq_launch.h"
+#include "../hq_ptx.cuh"
+#include "../hq_quant.cuh"
 #include "hq_row_ops.h"
 
 namespace hq {

@@ -12,7 +12,7 @@
 #include "hq_act_quant.h"
 #include "hq_gemm_kernel.cuh"
 #include "hq_layout.h"
-#include "hq_row_ops.h"
+#include "block/hq_row_ops.h"
 #include "hq_tune.h"
 
 namespace hq {

@@ -110,7 +110,7 @@ inline int decode_kind(int weight_type) {
 inline bool register_decode_only(int weight_type) { return weight_type >= WK_INT8_SYM; }
 // tcgen05 kernel variants; PATH_MXFP4A: MXFP4 weights with MXFP8 activations (e8m0 block scales on both operands)
 // PATH_MXFP4X: MXFP4 weights with MXFP4 activations (e8m0 block scales on both operands, packed e2m1 in the MMA)
-// PATH_E4M3B: e4m3 weights and activations with fp32 scales per block of 128 (kernels of their own, hq_gemm_block.cuh)
+// PATH_E4M3B: e4m3 weights and activations with fp32 scales per block of 128 (kernels of their own, block/hq_gemm_block.cuh)
 enum KernelPath { PATH_INT4 = 0, PATH_NVFP4 = 1, PATH_MXFP4 = 2, PATH_MXFP4A = 3, PATH_MXFP4X = 4, PATH_E4M3B = 5 };
 
 constexpr int TILE_N = 128;  // weight rows per tile (the UMMA M dimension)
