@@ -65,8 +65,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 }
 
 // ------------------------------------------------------------------ clusters
+// The lanes of a warp leave a wait, or a branch of one lane, one by one; barriers and tensor-memory instructions are the
+// whole warp's.  A __syncwarp() therefore stands between every such wait or branch and the next of those: a warp that
+// comes to them in parts is undefined behaviour.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cta_sync() {
+  __syncwarp();
+  __syncthreads();
 }
 // shared::cluster address of a shared::cta address in the CTA of cluster rank `rank`
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   pdl_trigger();
   pdl_wait();
   tc_fence_before();
-  __syncthreads();
+  cta_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   bool ok = true;
@@ -280,11 +288,13 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
         const int idx = tid + 256 * u;
         if (idx < C::KC * BT) sc[kb * BT + idx / C::KC] = na[u] * nw;
       }
+      __syncwarp();
       named_bar_sync(1, 256);  // every warp comes here once a chunk, also after a wait has run out
       load_scales(i0 + C::KC);
       const int n = !active ? 0 : (nblk - i0 < C::KC ? nblk - i0 : C::KC);
       for (int i = 0; i < n; ++i) {
         waitf(&sh.dfull[d], dph);  // (after one that has run out the sums are of no use, but nothing is out of place)
+        __syncwarp();
         tc_fence_after();
         uint32_t v[HC];
         const uint32_t from = tmem + lane_base + d * C::WIDTH + h * HC;
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
   }
 
   // ------------------------------------------------ sums -> shared memory -> output rows
-  __syncthreads();  // every copy has landed and every MMA has read its stage
+  cta_sync();  // every copy has landed and every MMA has read its stage
   float* red = reinterpret_cast<float*>(smem);  // [BT][PITCH]
   if (warp < 8 && (!C::LANES || (warp & 3) * 32 < BT)) {
     const int r = (warp & 3) * 32 + lane;
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     }
   }
   if (split > 1) cluster_sync();
-  else __syncthreads();
+  else cta_sync();
   const int nrows = args.M - m0 < BT ? args.M - m0 : BT;
   if (warp < 8) {
     const int n = nt * TILE_N + lane * 4;
@@ -362,8 +372,9 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     }
   }
   if (split > 1) cluster_sync();  // the sums stay until every CTA of the cluster has read them
-  else __syncthreads();
+  else cta_sync();
   if (warp == 0) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::COLS);
   }
@@ -506,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   }
   pdl_trigger();
   tc_fence_before();
-  __syncthreads();
+  cta_sync();
   cluster_sync();  // both CTAs' barriers stand before either is signalled
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
@@ -517,6 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     ok = false;
   };
 
+  __syncwarp();
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8 && lane == 0) {
@@ -688,6 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     auto open = [&](int d) {
       if (!mbar_wait_soon(dfull + d * C::HALVES, (dph >> d) & 1, abort_flag, args.wait_ns)) fail();
       dph ^= 1u << d;
+      __syncwarp();
       tc_fence_after();
       tmem_ld32(src + d * (C::HALVES * C::SN), v[0]);
       tmem_ld32(src + d * (C::HALVES * C::SN) + 32, v[1]);
@@ -696,6 +709,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     const float* at = sc;
     auto group = [&] {
       if (!mbar_wait_soon(&sh.sfull[g], gph, abort_flag, args.wait_ns)) fail();
+      __syncwarp();
       at = sc + g * C::SGROUP;
       fn = *at;
     };
@@ -793,9 +807,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  cta_sync();
   cluster_sync();  // neither CTA leaves while the other's MMAs, copies or arrivals may still reach it
   if (warp == 0) {
+    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
