@@ -110,7 +110,7 @@ struct BlkCfg {
   static constexpr bool LANES = BT >= 64;         // tokens on the lanes
   static constexpr int STAGE = 16384 + BT * 128;  // weight block, token rows x 128 bytes
   static constexpr int PER_SM = LANES ? 1 : 2;
-  static constexpr int STAGES = BT == 16 ? 6 : (BT == 32 ? 5 : (BT == 64 ? 8 : 6));
+  static constexpr int STAGES = BT == 16 ? 6 : (BT == 32 ? 4 : (BT == 64 ? 8 : 6));
   static constexpr int SLOTS = 4;                    // accumulators in tensor memory
   static constexpr int WIDTH = LANES ? TILE_N : BT;  // columns of one
   static constexpr int COLS = SLOTS * WIDTH;         // 64, 128 (two CTAs share an SM's 512 columns), or all 512
@@ -232,10 +232,13 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
     const uint32_t ring = smem_u32(smem);
     int s = warp - BLK_MMA_WARP, d = warp - BLK_MMA_WARP;
     uint32_t ph = 0, dph = 0;
-    static_assert(C::STAGES >= 2 && C::SLOTS % 2 == 0, "a warp takes every second stage and slot");
+    // A parity wait tells a barrier's next phase from the one before the last only by what its waiter knows: a warp
+    // that took a stage's every second fill could pass on the fill before (copies end out of order).  So the numbers are
+    // even, a stage and a slot belong to one warp, which waits for each of their phases in turn.
+    static_assert(C::STAGES % 2 == 0 && C::SLOTS % 2 == 0, "a stage and a slot belong to one issuing warp");
     for (int i = warp - BLK_MMA_WARP; i < nblk; i += 2) {
-      if (!ok || !mbar_wait_strict(&sh.full[s], ph, abort_flag, args.wait_ns)) timed_out();
-      if (!__all_sync(0xffffffffu, ok && waitf(&sh.dempty[d], dph ^ 1))) break;
+      if (waitf(&sh.dempty[d], dph ^ 1) && !mbar_wait_strict(&sh.full[s], ph, abort_flag, args.wait_ns)) timed_out();
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2), a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
       if (one) {
@@ -604,7 +607,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         uint32_t ph = ((base + b1) / C::STAGES) & 1;
         for (int b = b1; b < kst; b += STEP) {
           const int d = (b & (C::DEPTH - 1)) * C::HALVES + h;  // a tile begins with the first slots
-          if (!waitf(&sh.full[s], ph) || !waitf(&sh.dempty[d], ~(dph >> d) & 1)) break;
+          // The slot first: tiles of 128 features with an odd number of K blocks give a stage to either warp, and that
+          // its last fill but one is over, without which a parity wait could pass on it, follows from the slot (block
+          // i - 7 or a later one has been promoted, in order, and i - 8 with it).
+          if (!waitf(&sh.dempty[d], ~(dph >> d) & 1) || !waitf(&sh.full[s], ph)) break;
           dph ^= 1u << d;
           tc_fence_after();
           const uint64_t x = smem_desc(ring + s * C::STAGE, 16, 1024, 2),
