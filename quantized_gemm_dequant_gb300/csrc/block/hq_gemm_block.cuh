@@ -100,7 +100,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 // so that a step of one token still fills the MMA's rows; a column's scale is then its token's, read from shared memory
 // by every warp (128 bytes into the registers for each column).  From 64 tokens on that read takes longer than the rest,
 // and the tokens are the A operand: a lane is a token and its scale one register (128 tokens, N = 14336, K = 4096: 19.5
-// -> 14.8 us).  The A operand of 64 tokens is still 128 rows: the MMA reads what follows them in shared memory, whatever
+// to 14.8 us).  The A operand of 64 tokens is still 128 rows: the MMA reads what follows them in shared memory, whatever
 // it is, into sums that nothing reads.
 //
 // Bound by the weights' bytes: every CTA keeps a ring of 16 KB weight blocks in flight, and two warps issue the MMAs of
@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
       if (waitf(&sh.dempty[d], dph ^ 1) && !mbar_wait_strict(&sh.full[s], ph, abort_flag, args.wait_ns)) timed_out();
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2), a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
+      const uint64_t w = smem_desc(ring + s * C::STAGE, 16, 1024, 2),
+                     a = smem_desc(ring + s * C::STAGE + 16384, 16, 1024, 2);
       if (one) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // 32 bytes further on: the address field counts 16s
@@ -390,8 +391,11 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 // thread's sums share one token scale and (128 columns) one weight scale, and a K block costs a thread one scale and
 // an FMA per sum.  Two FMAs go in one instruction.
 //
-// Bound by the MMA: a K block of a 256 x 256 tile takes it 512 cycles, and the promotion of its 128 x 256 sums per CTA
-// by eight warps takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.
+// A K block of a 256 x 256 tile takes the MMA 512 cycles, and the promotion of its 128 x 256 sums per CTA by eight warps
+// takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.  Measured: 8192
+// tokens, 14336 x 4096, 356 us = 2.70 PFLOP/s, 900 cycles a K block (the same loads and MMAs without promotion: 270 us,
+// 3.56 PFLOP/s).  What is left over the MMA is the promoting warps' own chain: a wait (110 cycles with the phase over),
+// the first 64 columns (200), the rest of them between the sums, and the two warps of a scheduler in phase.
 // Accumulators are handed over 128 columns at a time (four slots in tensor memory), so that half of the promoting warps
 // read one half of a tile while the MMA fills the other.
 template <int BN>
@@ -415,7 +419,8 @@ struct PairCfg {
 };
 // warps 0-7 promote, 8 loads, 9 and 10 issue the MMAs (of the cluster's first CTA), 11 multiplies the scales
 constexpr int PAIR_THREADS = 384;
-// registers: 168 x 384 at launch; the promoting warps raise theirs to 216, the others go down to 72 (2 x 216 + 72 = 3 x 168)
+// registers: 168 x 384 at launch; the promoting warps raise theirs to 216, the others go down to 72, and 2 x 216 + 72 =
+// 3 x 168
 constexpr int PAIR_TOKENS = 256;
 constexpr int PAIR_GROUP = 8;  // token tiles per round of feature tiles: the tiles in flight share operands in L2
 
@@ -496,7 +501,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   volatile int* abort_flag = &sh.abort_flag;
 
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem_base)) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem_base))
+                 : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (tid == 8 * 32) {

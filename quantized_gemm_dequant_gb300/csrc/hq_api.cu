@@ -231,21 +231,21 @@ void plan_tiles(Plan& p, int64_t M_or_T, int32_t topk, bool moe, int64_t E, int6
 // Block-scaled e4m3 products, no workspace past the header: the CTA-pair kernel (256 tokens by 128 or 256 features), or
 // the kernel for few tokens (a token tile, and CTAs per tile: a cluster that splits K).
 //
-// The choice is the least of the candidates' estimated times: 3 us a call, then for every wave of tiles (or of clusters,
-// as many as the device holds at once) 1 us, 0.5 us more where sums cross a cluster, and the K blocks of a CTA at what
-// one takes where memory does not hold it up, measured at K = 16384 with one wave: 420 and 285 ns (the pair kernel's 256
-// and 128 features), 297, 269, 254 and 243 ns (128, 64, 32 and 16 tokens).  Estimates within a microsecond of 46 of 52
-// measured calls of 64 to 512 tokens, N 1001 to 14336, K 2048 to 16384; the fastest candidate or one within 8% of it in
-// all of them.
+// The choice is the least of the candidates' estimated times: for every wave of tiles (or of clusters, as many as the
+// device holds at once) 1 us, 0.5 us more where sums cross a cluster, and the K blocks of a CTA at what one takes where
+// memory does not hold it up, measured at K = 16384 with one wave: 420 and 285 ns (the pair kernel's 256 and 128
+// features), 297, 269, 254 and 243 ns (128, 64, 32 and 16 tokens).  Of 54 sizes (1 to 2000 tokens, N 1001 to 16000, K
+// 1024 to 16384) it takes the fastest candidate, or one within 3% of it, in 45, within 8% in 50; at worst it loses 19%
+// (333 tokens, 2048 x 16384: 27.0 us for 22.7).
 // HQ_TUNE: kernel 0 / 1 (pair / few tokens), bt the pair's features or the token tile, sk the CTAs per tile.
 void plan_block(Plan& p, int64_t M, int sms) {
   TuneChoice tc;
   tune_env_override(tc);
   p.ws_bytes = kHeaderBytes;
-  int64_t best = INT64_MAX;
+  double best = 1e300;
   const auto take = [&](int pair, int bt, int sk, int64_t tiles, int64_t m_tiles, int64_t room, int64_t ns) {
     const int64_t ctas = tiles * sk, waves = (ctas + room - 1) / room;
-    const int64_t cost = waves * (((p.kst + sk - 1) / sk) * ns + 1000 + (sk > 1 ? 500 : 0));
+    const double cost = (double)waves * ((double)((p.kst + sk - 1) / sk * ns) + 1000.0 + (sk > 1 ? 500.0 : 0.0));
     if (cost >= best) return;
     best = cost;
     p.pair = pair;
@@ -260,7 +260,7 @@ void plan_block(Plan& p, int64_t M, int sms) {
     const int64_t m = (M + 255) / 256, pairs = sms / 2 < 1 ? 1 : sms / 2;
     if (tc.bt != 128) take(256, 256, 1, m * ((p.n_tiles + 1) / 2), m, pairs, 420);
     if (tc.bt != 256) take(128, 256, 1, m * p.n_tiles, m, pairs, 285);
-    if (tc.kernel == 0) best = 0;
+    if (tc.kernel == 0) best = 0.0;
   }
   int bt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
   if (tc.kernel == 1 && (tc.bt == 16 || tc.bt == 32 || tc.bt == 64 || tc.bt == 128)) bt = tc.bt;
