@@ -204,8 +204,9 @@ HQ_API hq_status_t hq_workspace_init(void* workspace, size_t bytes, hq_stream_t 
  * E4M3_TOKEN by the row's token scale.  M may be 0 (no work).  Accumulation is
  * fp32; C is rounded to nearest-even bf16.
  * E4M3 weights with F32 scales: C[m, n] = bias[n] + sum_b s(A)[m, b] * s(W)[n / 128, b] * sum_{k in block b} A[m, k] *
- * W[n, k]; every 128-K block is summed by itself and added, times its scale, in fp32, in an order that does not depend
- * on timing.  The workspace holds the status header alone; A's scales and C are 16-byte aligned. */
+ * W[n, k]; every 128-K block is summed by itself and added, times its scale s(A) * s(W) (rounded to fp32, so that it
+ * should lie in fp32's normal range), in fp32, in an order that does not depend on timing.  The
+ * workspace holds the status header alone; A's scales and C are 16-byte aligned. */
 HQ_API hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packedW, const void* bias, void* C,
                     int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes, hq_stream_t stream);
 

@@ -9,7 +9,7 @@ namespace {
 
 // The shared-memory limit of a kernel, set once per device.
 template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, int (&done)[64]) {
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<int> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
@@ -20,7 +20,7 @@ cudaError_t allow_smem(K kernel, int bytes, int (&done)[64]) {
 
 template <int BT>
 cudaError_t launch_bt(const GemmArgs& a, int grid, cudaStream_t stream) {
-  static int done[64] = {0};
+  static std::atomic<int> done[64];
   const cudaError_t e = allow_smem(gemm_block_kernel<BT>, BlkCfg<BT>::SMEM, done);
   if (e != cudaSuccess) return e;
   return launch_cluster_kernel(gemm_block_kernel<BT>, grid, a.sk, BLK_THREADS, BlkCfg<BT>::SMEM, stream, a);
@@ -31,7 +31,7 @@ int clusters_of(int n) {
   static std::atomic<int> known[9];
   int c = known[n].load(std::memory_order_relaxed);
   if (c != 0) return c;
-  static int done[64] = {0};
+  static std::atomic<int> done[64];
   if (allow_smem(gemm_block_kernel<128>, BlkCfg<128>::SMEM, done) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)n);
@@ -53,7 +53,7 @@ int clusters_of(int n) {
 
 template <int BN>
 cudaError_t launch_pair(const GemmArgs& a, int grid, cudaStream_t stream) {
-  static int done[64] = {0};
+  static std::atomic<int> done[64];
   const cudaError_t e = allow_smem(gemm_block_pair_kernel<BN>, PairCfg<BN>::SMEM, done);
   if (e != cudaSuccess) return e;
   return launch_kernel(gemm_block_pair_kernel<BN>, dim3((unsigned)grid), dim3(PAIR_THREADS), PairCfg<BN>::SMEM, stream,

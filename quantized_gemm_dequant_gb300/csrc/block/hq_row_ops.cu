@@ -27,11 +27,12 @@ namespace {
 
 enum RowSrc { SRC_NORM = 0, SRC_ADD_NORM = 1, SRC_SWIGLU = 2 };
 
-// silu(g) * u = g * u / (1 + exp(-g)) of eight values (every lane of the warp calls it).  exp(-g) = 2^t with t = -g log2(e) in two parts: the product's
-// fp32 rounding error, found by an FMA, together with the part of log2(e) below fp32, corrects the power to first order
-// (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to |t| 2^-24.  The reciprocal gets one Newton
-// step.  Two values go through each instruction but the power's and the reciprocal's.  Where a power over- or
-// underflows (and where a gate is no number or infinite) the quotient is taken as 0 or 1.
+// silu(g) * u = g * u / (1 + exp(-g)) of eight values (every lane of the warp calls it).  exp(-g) = 2^t with
+// t = -g log2(e) in two parts: the product's fp32 rounding error, found by an FMA, together with the part of log2(e)
+// below fp32, corrects the power to first order (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to
+// |t| 2^-24.  The reciprocal gets one Newton step.  Two values go through each instruction but the power's and the
+// reciprocal's.  Where a power over- or underflows (and where a gate is no number or infinite) the quotient is taken as
+// 0 or 1.
 __device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
   constexpr float kHi = -1.44269504f, kLo = -1.925963033e-8f, kLn2 = 0.693147181f;
   float2 t[4], r[4];
@@ -157,9 +158,9 @@ __global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) r
       float rstd;
       asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rstd) : "f"(v));
       rstd = fmaf(rstd, fmaf(-0.5f * v * rstd, rstd, 0.5f), rstd);
-      // A sum that overflowed, or one that lost small squares where eps does not cover them, is taken again with the
-      // row divided by a power of two near its largest magnitude.
-      if (!(ss <= FLT_MAX) || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
+      // A sum that overflowed (of squares, or of their mean and eps), or one that lost small squares where eps does not
+      // cover them, is taken again with the row divided by a power of two near its largest magnitude.
+      if (!(v <= FLT_MAX) || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < CH; ++j) m = max(m, absmax_bits(f[j]));
@@ -236,8 +237,9 @@ struct RowDivide {
   }
 };
 template <bool SWIGLU, int U>
-__global__ void __launch_bounds__(BQ_THREADS) block_quant_kernel(const uint4* __restrict__ x, int64_t n8, RowDivide per_row,
-                                                                 uint2* __restrict__ q, float* __restrict__ s_out) {
+__global__ void __launch_bounds__(BQ_THREADS)
+    block_quant_kernel(const uint4* __restrict__ x, int64_t n8, RowDivide per_row, uint2* __restrict__ q,
+                       float* __restrict__ s_out) {
   pdl_trigger();
   pdl_wait();
   uint4 va[U], vb[U];

@@ -449,7 +449,8 @@ bool act_maps(GemmArgs& a, const hq_format_t* f, const hq_act_t* A, int64_t rows
   const uint32_t box_rows = moe ? 1u : (uint32_t)bt;
   const uint64_t K = (uint64_t)f->K;
   if (f->act_type == HQ_A_BF16) return encode_2d(&a.tmap_a, A->data, true, K, rows, 64, box_rows, true);
-  if (f->act_type == HQ_A_E4M3_TOKEN || f->act_type == HQ_A_E4M3_BLOCK) return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true);
+  if (f->act_type == HQ_A_E4M3_TOKEN || f->act_type == HQ_A_E4M3_BLOCK)
+    return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true);
   if (f->act_type == HQ_A_MXFP8)
     return encode_2d(&a.tmap_a, A->data, false, K, rows, 128, box_rows, true) &&
            encode_2d(&a.tmap_sf, A->scale, false, K / 32, rows, 16, box_rows, false);

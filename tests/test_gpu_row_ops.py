@@ -101,6 +101,14 @@ def test_norm_at_the_ends_of_the_range(lib, afmt, size, eps):
         B.check_act(act, want, afmt == "e4m3_block")
 
 
+def test_norm_mean_and_eps_that_overflow_together(lib):
+    """Squares whose sum still fits fp32, and an eps with which their mean does not."""
+    x = torch.tensor([[6e18, -6e18] * 4, [1e18] * 8]).to(torch.bfloat16)
+    w = _weight(1, 8)
+    act, _ = lib.add_rms_norm("bf16", x.cuda(), w.cuda(), eps=3.2e38)
+    B.check_bf16(act["data"], B.norm(B.f64(x), B.f64(w)[None], float(np.float32(3.2e38))))
+
+
 @pytest.mark.parametrize("afmt", ["e4m3_tok", "e4m3_block"])
 def test_not_numbers_make_their_scale_not_a_number(lib, afmt):
     T, K = 5, 512
