@@ -46,6 +46,16 @@ __device__ __forceinline__ bool mbar_wait_strict(uint64_t* bar, uint32_t parity,
   return false;
 }
 
+// The whole warp's wait (every lane calls it): each test is put to the vote, so that the lanes stay together.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long c0 = clock64(), lim = 3ll * (long long)limit_ns;
+  for (;;) {
+    if (__any_sync(0xffffffffu, clock64() - c0 >= lim || *abort)) return false;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  }
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -297,8 +307,8 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
       load_scales(i0 + C::KC);
       const int n = !active ? 0 : (nblk - i0 < C::KC ? nblk - i0 : C::KC);
       for (int i = 0; i < n; ++i) {
-        waitf(&sh.dfull[d], dph);  // (after one that has run out the sums are of no use, but nothing is out of place)
-        __syncwarp();
+        // (after a wait that has run out the sums are of no use, but nothing is out of place)
+        if (ok && !mbar_wait_warp(&sh.dfull[d], dph, abort_flag, args.wait_ns)) timed_out();
         tc_fence_after();
         uint32_t v[HC];
         const uint32_t from = tmem + lane_base + d * C::WIDTH + h * HC;
@@ -598,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
       uint32_t dph = 0;  // a bit per accumulator slot
       uint32_t base = 0;  // stages of the tiles before
       auto waitf = [&](uint64_t* bar, uint32_t par) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait_soon(bar, par, abort_flag, args.wait_ns))) fail();
+        if (ok && !mbar_wait_warp(bar, par, abort_flag, args.wait_ns)) fail();
         return ok;
       };
       const uint32_t ring = smem_u32(smem);
@@ -651,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
         int mt, ft;
         pair_tile(t, args.m_tiles, f_tiles, mt, ft);
         for (int b0 = 0; b0 < kst; b0 += C::SK) {
-          if (!mbar_wait_soon(&sh.sempty[g], ph ^ 1, abort_flag, args.wait_ns)) {
+          if (!mbar_wait_warp(&sh.sempty[g], ph ^ 1, abort_flag, args.wait_ns)) {
             fail();
             break;
           }
@@ -710,9 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     uint32_t v[2][32];
     // the slot's sums are there: the first of them are on their way
     auto open = [&](int d) {
-      if (!mbar_wait_soon(dfull + d * C::HALVES, (dph >> d) & 1, abort_flag, args.wait_ns)) fail();
+      if (!mbar_wait_warp(dfull + d * C::HALVES, (dph >> d) & 1, abort_flag, args.wait_ns)) fail();
       dph ^= 1u << d;
-      __syncwarp();
       tc_fence_after();
       tmem_ld32(src + d * (C::HALVES * C::SN), v[0]);
       tmem_ld32(src + d * (C::HALVES * C::SN) + 32, v[1]);
@@ -720,8 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
     float f, fn = 0.0f;  // this K block's scale and the next one's
     const float* at = sc;
     auto group = [&] {
-      if (!mbar_wait_soon(&sh.sfull[g], gph, abort_flag, args.wait_ns)) fail();
-      __syncwarp();
+      if (!mbar_wait_warp(&sh.sfull[g], gph, abort_flag, args.wait_ns)) fail();
       at = sc + g * C::SGROUP;
       fn = *at;
     };
