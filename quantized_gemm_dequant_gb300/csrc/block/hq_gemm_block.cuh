@@ -401,11 +401,16 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 // thread's sums share one token scale and (128 columns) one weight scale, and a K block costs a thread one scale and
 // an FMA per sum.  Two FMAs go in one instruction.
 //
-// A K block of a 256 x 256 tile takes the MMA 512 cycles, and the promotion of its 128 x 256 sums per CTA by eight warps
-// takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.  Measured: 8192
-// tokens, 14336 x 4096, 356 us = 2.70 PFLOP/s, 900 cycles a K block (the same loads and MMAs without promotion: 270 us,
-// 3.56 PFLOP/s).  What is left over the MMA is the promoting warps' own chain: a wait (110 cycles with the phase over),
-// the first 64 columns (200), the rest of them between the sums, and the two warps of a scheduler in phase.
+// A K block of a 256 x 256 tile keeps the tensor pipe busy for 650 cycles, and the promotion of its 128 x 256 sums per
+// CTA by eight warps takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.
+// Measured: 8192 tokens, 14336 x 4096, 370 us = 2.6 PFLOP/s (355 to 400 from run to run: a long call draws the card's
+// full power); one wave of tiles, 2048 x 2048 x 16384, 55 us = 820 cycles a K block.  With the additions left out that
+// takes 45 us, at the MMA's pace; with a quarter of the MMAs and neither reads nor additions 41, which is what copies,
+// barriers and hand-overs between the CTAs cost by themselves.  What is left over the MMA is the circle of a slot: filled,
+// announced to both CTAs, read, given back.  Tried for it: sixteen promoting warps with 64 columns each (69 us), one MMA
+// and slot for 256 columns, which reads a third less shared memory but leaves two slots (61), weights copied and half
+// the scales multiplied by two more warps (63), waits by one lane of a warp (70), the next slot tested and read before
+// the last additions (56).
 // Accumulators are handed over 128 columns at a time (four slots in tensor memory), so that half of the promoting warps
 // read one half of a tile while the MMA fills the other.
 template <int BN>
