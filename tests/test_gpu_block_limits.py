@@ -77,6 +77,18 @@ def test_rows_past_32_bits(lib, afmt):
         assert not q["data"][T // 2].any()
 
 
+def test_more_than_2_to_the_31_chunks(lib):
+    """More chunks of 8 outputs than a 31-bit index holds, where a chunk's row comes from a plain division."""
+    I, last = 32768, 3
+    R = (1 << 31) // (I // 8) + last + 2
+    x = torch.zeros(R, 2 * I, dtype=torch.bfloat16, device="cuda")
+    end = torch.randn(last, 2 * I, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    x[-last:] = end.cuda()
+    q = lib.swiglu_quantize("e4m3_block", x)
+    B.check_act({k: t[-last:] for k, t in q.items()}, B.swiglu(B.f64(end)), True)
+    assert not q["data"][R - last - 1].any() and not q["scale"][:-last].any()
+
+
 @pytest.mark.parametrize("M,choice", [(5, "kernel=1,sk=2"), (30, "kernel=1,sk=4"), (60, "kernel=1,sk=2"),
                                       (100, "kernel=1,sk=8"), (600, "kernel=0,bt=256"), (600, "kernel=0,bt=128")])
 def test_waits_that_run_out_are_reported_and_the_next_call_is_right(lib, monkeypatch, M, choice):
