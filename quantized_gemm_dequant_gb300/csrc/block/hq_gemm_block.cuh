@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 // takes 45 us, at the MMA's pace; with a quarter of the MMAs and neither reads nor additions 41, which is what copies,
 // barriers and hand-overs between the CTAs cost by themselves.  What is left over the MMA is the circle of a slot: filled,
 // announced to both CTAs, read, given back.  Tried for it: sixteen promoting warps with 64 columns each (69 us), one MMA
-// and slot for 256 columns, which reads a third less shared memory but leaves two slots (61), weights copied and half
+// and slot for 256 columns, which reads a third less shared memory but leaves two slots (59), weights copied and half
 // the scales multiplied by two more warps (63), waits by one lane of a warp (70), the next slot tested and read before
 // the last additions (56).
 // Accumulators are handed over 128 columns at a time (four slots in tensor memory), so that half of the promoting warps
