@@ -285,7 +285,8 @@ typedef struct {
  *   r = x + residual,  residual_out = bf16(r),  y = r / sqrt(mean(r^2) + eps) * weight
  * y takes the sum as it is, before its rounding to bf16, and is rounded once: to bf16, or to e4m3 codes whose scale is
  * absmax / 448 of the row or of each 128 elements, as hq_quantize_act makes them from bf16 rows.  Sums of squares that
- * leave fp32's range are taken again with the row scaled.  A NaN or an infinity in r makes the row's values NaN.
+ * leave fp32's range are taken again with the row scaled.  A NaN or an infinity in r makes the row's values NaN, and so
+ * does a row of zeros with eps = 0 (0 / 0); with any other eps it stays zeros.
  * The strides of residual and residual_out are read only where residual is given.  Pointers 16-byte aligned; outputs
  * must not overlap anything else that the call reads.  One kernel, no workspace. */
 HQ_API hq_status_t hq_add_rms_norm(const hq_norm_t* args, hq_stream_t stream);

@@ -159,14 +159,15 @@ __global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) r
       asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rstd) : "f"(v));
       rstd = fmaf(rstd, fmaf(-0.5f * v * rstd, rstd, 0.5f), rstd);
       // A sum that overflowed (of squares, or of their mean and eps), or one that lost small squares where eps does not
-      // cover them, is taken again with the row divided by a power of two near its largest magnitude.
+      // cover them, is taken again with the row divided by a power of two near its largest magnitude.  (A row of zeros
+      // too: the approximation above takes an eps below 2^-126 as zero.)
       if (!(v <= FLT_MAX) || (ss < 0x1p-80f && a.eps < 0x1p-60f)) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < CH; ++j) m = max(m, absmax_bits(f[j]));
         m = row_reduce<WARP>(m, 0u, red_u, turn_u, [](uint32_t p, uint32_t q) { return max(p, q); });
-        if (m > 0u && m < 0x7F800000u) {
-          const int e = ilogbf(__uint_as_float(m));
+        if (m < 0x7F800000u) {
+          const int e = m > 0u ? ilogbf(__uint_as_float(m)) : 0;
 #pragma unroll
           for (int j = 0; j < CH; ++j)
 #pragma unroll

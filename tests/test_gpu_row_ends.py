@@ -1,0 +1,50 @@
+"""The row operators at the ends of what their arguments may be, against plain 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+from tests import block_ref as B
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = {"bf16": 8, "e4m3_tok": 16, "e4m3_block": 128}
+
+
+# a warp a row, a CTA a row with one, two and four chunks a thread, and rows past the registers' prefetch
+@pytest.mark.parametrize("T,K", [(2100, 256), (5, 256), (400, 1024), (400, 4096), (3, 32768)])
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1.1e-38, 1.2e-38, 1e-30])
+@pytest.mark.parametrize("afmt", FORMATS)
+@pytest.mark.parametrize("add", [True, False])
+def test_norm_rows_of_zeros_with_a_tiny_eps(lib, afmt, eps, T, K, add):
+    """0 / sqrt(0 + eps) is 0 for every eps above 0, fp32's subnormals among them; other rows keep to the formula."""
+    eps = float(np.float32(eps))
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(T, K, generator=g).to(torch.bfloat16)
+    zeros = list(range(0, T, 3))
+    x[zeros] = 0
+    x[1] *= 1e-22  # squares of eps's own size
+    r = torch.zeros(T, K, dtype=torch.bfloat16)
+    if add:  # sums that cancel are zeros as well
+        r[zeros] = torch.randn(len(zeros), K, generator=g).to(torch.bfloat16)
+        x[zeros] = -r[zeros]
+    w = (1 + 0.3 * torch.randn(K, generator=g)).to(torch.bfloat16)
+    act, res = lib.add_rms_norm(afmt, x.cuda(), w.cuda(), residual=r.cuda() if add else None, eps=eps)
+    total = B.f64(x) + B.f64(r)
+    want = B.norm(total, B.f64(w)[None], eps)
+    if afmt == "bf16":
+        B.check_bf16(act["data"], want)
+        assert not act["data"][zeros].any()
+    else:
+        B.check_act(act, want, afmt == "e4m3_block", rows_of_zeros=zeros)
+    if add:
+        B.check_bf16(res, total)
+
+
+@pytest.mark.parametrize("afmt", FORMATS)
+def test_norm_rows_of_zeros_without_eps(lib, afmt):
+    """0 / sqrt(0) is no number."""
+    x = torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    x[1] = 3
+    act, _ = lib.add_rms_norm(afmt, x, torch.ones(256, dtype=torch.bfloat16, device="cuda"), eps=0.0)
+    y = act["data" if afmt == "bf16" else "scale"].float()
+    assert torch.isnan(y[0]).all() and torch.isfinite(y[1]).all()
