@@ -31,9 +31,9 @@ enum RowSrc { SRC_NORM = 0, SRC_ADD_NORM = 1, SRC_SWIGLU = 2 };
 // t = -g log2(e) in two parts: the product's fp32 rounding error, found by an FMA, together with the part of log2(e)
 // below fp32, corrects the power to first order (2^(t + d) = 2^t (1 + d ln 2)), which without it would be off by up to
 // |t| 2^-24.  The reciprocal gets one Newton step.  Two values go through each instruction but the power's and the
-// reciprocal's.  Where a power over- or underflows (and where a gate is no number or infinite) the quotient is taken as
-// 0 or 1.
-__device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
+// reciprocal's.  Where a power over- or underflows (and where a gate is infinite) the quotient is taken as 0 or 1; true is
+// returned to all lanes, and silu_far has the values behind the zeros.
+__device__ __forceinline__ bool silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
   constexpr float kHi = -1.44269504f, kLo = -1.925963033e-8f, kLn2 = 0.693147181f;
   float2 t[4], r[4];
 #pragma unroll
@@ -48,7 +48,8 @@ __device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r[i].y) : "f"(q.y));
     r[i] = __ffma2_rn(r[i], __ffma2_rn(make_float2(-q.x, -q.y), r[i], both(1.0f)), r[i]);
   }
-  if (__any_sync(0xffffffffu, !(__uint_as_float(absmax_bits(t)) <= 126.0f))) {
+  const bool ends = __any_sync(0xffffffffu, !(__uint_as_float(absmax_bits(t)) <= 126.0f));
+  if (ends) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (fabsf(t[i].x) > 126.0f) r[i].x = t[i].x > 0.0f ? 0.0f : 1.0f;
@@ -57,6 +58,33 @@ __device__ __forceinline__ void silu_mul(float2 (&g)[4], const float2 (&u)[4]) {
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) g[i] = __fmul2_rn(__fmul2_rn(g[i], r[i]), u[i]);
+  return ends;
+}
+
+// silu(g) * u where t = -g log2(e) is above 126: there 1 / (1 + exp(-g)) is exp(g) to fp32's precision and leaves its
+// normal range, but g exp(g) u need not.  exp(g) = 2^-t is therefore taken 2^192 times larger (t - 192 is exact), with
+// the correction of silu_mul's power, and the factor divided out in halves, u's first: what that loses of a small u is
+// below fp32's smallest number in the result.  Past t = 290 the largest u leaves less than half of that number.
+// Gate and up are read again, so that a path which ordinary activations never take costs the others no registers (with
+// the values at hand 8192 x 7168 took 55 us for 53, 2048 x 32768 80 for 70).
+__device__ __forceinline__ void silu_far(float2 (&y)[4], const uint4* gate, const uint4* up) {
+  const auto far = [](uint32_t gbits, uint32_t ubits, float y) {
+    constexpr float kHi = -1.44269504f, kLo = -1.925963033e-8f, kLn2 = 0.693147181f;
+    const float g = __uint_as_float(gbits), u = __uint_as_float(ubits), t = __fmul_rn(g, kHi);
+    if (!(t > 126.0f && t <= 290.0f)) return y;
+    const float d = fmaf(g, kLo, fmaf(g, kHi, -t));
+    float p;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(192.0f - t));
+    p = fmaf(p, -kLn2 * d, p);
+    return __fmul_rn(__fmul_rn(__fmul_rn(g, p), __fmul_rn(u, 0x1p-96f)), 0x1p-96f);
+  };
+  const uint4 vg = *gate, vu = *up;
+  const uint32_t g[4] = {vg.x, vg.y, vg.z, vg.w}, u[4] = {vu.x, vu.y, vu.z, vu.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i].x = far(g[i] << 16, u[i] << 16, y[i].x);
+    y[i].y = far(g[i] & 0xFFFF0000u, u[i] & 0xFFFF0000u, y[i].y);
+  }
 }
 
 // Reductions over a row's threads: a warp, or the CTA (every thread calls them; `turn` alternates between the two
@@ -76,11 +104,54 @@ __device__ __forceinline__ T row_reduce(T v, T zero, T (*red)[32], int& turn, F&
   return v;
 }
 
+// SwiGLU rows with gates far below zero (silu_far), done again with a scale per row after the row kernel's own loop: a
+// function of its own, whose registers ordinary rows do not pay for.
+template <bool WARP>
+__device__ __noinline__ void swiglu_rows_again(const uint16_t* rows_in, int64_t rows, int width, void* out, float* scale,
+                                               uint32_t (*red)[32]) {
+  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x, n = WARP ? 32 : blockDim.x, chunks = width >> 3;
+  const auto most = [](uint32_t p, uint32_t q) { return max(p, q); };
+  int turn = 0;
+  if (!WARP) __syncthreads();
+  for (int64_t row = (int64_t)blockIdx.x * (WARP ? 4 : 1) + (WARP ? (threadIdx.x >> 5) : 0); row < rows;
+       row += (int64_t)gridDim.x * (WARP ? 4 : 1)) {
+    const uint4* x = reinterpret_cast<const uint4*>(rows_in) + row * 2 * chunks;
+    const auto chunk = [&](int c, float2 (&f)[4]) {  // (the whole warp's: zeros behind the row)
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      float2 u[4];
+      bf16x8_to_f32x2(c < chunks ? x[c] : none, f);
+      bf16x8_to_f32x2(c < chunks ? x[chunks + c] : none, u);
+      const bool ends = silu_mul(f, u);
+      if (ends && c < chunks) silu_far(f, x + c, x + chunks + c);
+      return ends;
+    };
+    float2 f[4];
+    uint32_t m = 0;
+    bool ends = false;
+#pragma unroll 1
+    for (int c0 = 0; c0 < chunks; c0 += n) {
+      ends |= chunk(t + c0, f);
+      m = max(m, absmax_bits(f));
+    }
+    if (!row_reduce<WARP>((uint32_t)ends, 0u, red, turn, most)) continue;
+    m = row_reduce<WARP>(m, 0u, red, turn, most);
+    const E4m3Scale s(m);
+    if (t == 0) scale[row] = s.s;
+#pragma unroll 1
+    for (int c0 = 0; c0 < chunks; c0 += n) {
+      chunk(t + c0, f);
+      const uint2 q = s.codes(f);
+      if (t + c0 < chunks) static_cast<uint2*>(out)[row * chunks + t + c0] = q;
+    }
+  }
+}
+
 // One row per CTA, or per warp (WARP, four rows a CTA), CH chunks of 8 elements per thread; the next row of the same
 // threads is loaded while the current one is reduced and written.  LONG: rows past 2048 chunks on 1024 threads, whose
 // registers leave no room for that, nor for the norm's weights.
 template <int SRC, int OUT, int CH, bool WARP, bool LONG>
-__global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(WARP || (SRC == SRC_SWIGLU && CH == 2) ? 128 : (CH == 1 || LONG ? 1024 : 512),
+                                  SRC == SRC_SWIGLU && CH == 2 ? 9 : 0) row_kernel(const RowArgs a) {
   __shared__ float red_f[2][32];
   __shared__ uint32_t red_u[2][32];
   constexpr bool NORM = SRC != SRC_SWIGLU;
@@ -117,6 +188,7 @@ __global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) r
       for (int j = 0; j < CH; ++j) w[j] = weight(t + j * n);
     }
   }
+  bool ends = false;
   for (; row < a.rows; row += step) {
     float2 f[CH][4];
 #pragma unroll
@@ -128,7 +200,7 @@ __global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) r
         float2 g[4];
         bf16x8_to_f32x2(LONG ? (c < chunks ? second(row)[c] : none) : vb[LONG ? 0 : j], g);
         if (SRC == SRC_SWIGLU) {
-          if (!WARP || j * n < chunks) silu_mul(f[j], g);  // (a warp's short row leaves its last chunks out)
+          if (!WARP || j * n < chunks) ends |= silu_mul(f[j], g);  // (a warp's short row leaves its last chunks out)
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[j][i] = __fadd2_rn(f[j][i], g[i]);
@@ -219,6 +291,8 @@ __global__ void __launch_bounds__(WARP ? 128 : (CH == 1 || LONG ? 1024 : 512)) r
       }
     }
   }
+  if (SRC == SRC_SWIGLU && (WARP ? (int)ends : __syncthreads_or(ends))) 
+    swiglu_rows_again<WARP>(a.x, a.rows, a.width, a.out, a.scale, red_u);
 }
 
 // A scale per 128 outputs needs no statistics of the row: every thread takes U chunks of 8 outputs, all loads first; 16
@@ -259,16 +333,7 @@ __global__ void __launch_bounds__(BQ_THREADS)
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const int64_t i = base + j * BQ_THREADS;
-    float2 f[4];
-    bf16x8_to_f32x2(va[j], f);
-    if (SWIGLU) {
-      float2 u[4];
-      bf16x8_to_f32x2(vb[j], u);
-      silu_mul(f, u);
-    }
+  const auto out = [&](int64_t i, const float2 (&f)[4]) {
     uint32_t m = absmax_bits(f);
 #pragma unroll
     for (int k = 8; k > 0; k >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -276,6 +341,35 @@ __global__ void __launch_bounds__(BQ_THREADS)
     const uint2 c = s.codes(f);
     if (i < n8) q[i] = c;
     if (i < n8 && (threadIdx.x & 15) == 0) s_out[i >> 4] = s.s;
+  };
+  bool ends = false;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float2 f[4];
+    bf16x8_to_f32x2(va[j], f);
+    if (SWIGLU) {
+      float2 u[4];
+      bf16x8_to_f32x2(vb[j], u);
+      ends |= silu_mul(f, u);
+    }
+    out(base + j * BQ_THREADS, f);
+  }
+  if (SWIGLU && ends) {  // a warp with gates far below zero does its chunks again
+    for (int j = 0; j < U; ++j) {
+      const int64_t i = base + j * BQ_THREADS;
+      const uint4 *pg = x, *pu = x;
+      float2 f[4], u[4] = {};
+      for (int k = 0; k < 4; ++k) f[k] = both(0.0f);
+      if (i < n8) {
+        pg = x + i + per_row.of(i) * per_row.d;
+        pu = pg + per_row.d;
+        bf16x8_to_f32x2(*pg, f);
+        bf16x8_to_f32x2(*pu, u);
+      }
+      silu_mul(f, u);
+      if (i < n8) silu_far(f, pg, pu);
+      out(i, f);
+    }
   }
 }
 

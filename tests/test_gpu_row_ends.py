@@ -48,3 +48,23 @@ def test_norm_rows_of_zeros_without_eps(lib, afmt):
     act, _ = lib.add_rms_norm(afmt, x, torch.ones(256, dtype=torch.bfloat16, device="cuda"), eps=0.0)
     y = act["data" if afmt == "bf16" else "scale"].float()
     assert torch.isnan(y[0]).all() and torch.isfinite(y[1]).all()
+
+
+# every layout of the rows: a warp a row, a CTA a row, and the kernel with a scale per 128
+@pytest.mark.parametrize("afmt,copies,I", [("e4m3_tok", 1, 128), ("e4m3_tok", 16, 128), ("e4m3_tok", 1, 4096),
+                                           ("e4m3_tok", 0, 4096), ("e4m3_tok", 1, 16400), ("e4m3_block", 0, 128),
+                                           ("e4m3_block", 1, 128), ("e4m3_block", 16, 256)])
+def test_swiglu_gates_far_below_zero(lib, afmt, copies, I):
+    """silu(g) for gates whose sigmoid leaves fp32's normal range is still a number that `up` can make large: every bf16
+    gate in [-210, -86] with ups up to bf16's largest, alone in its row or block and beside an ordinary value."""
+    g = torch.arange(1 << 16).to(torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    g = g[(g >= -210) & (g <= -86)]
+    up = torch.tensor([1.0, -1e10, 1e30, 1e38, -3.3e38])
+    pairs = torch.cartesian_prod(g, up).repeat(max(copies, 1), 1).to(torch.bfloat16)
+    if copies == 0:
+        pairs = pairs[::7]
+    x = torch.zeros(len(pairs), 2 * I, dtype=torch.bfloat16)
+    x[:, 7], x[:, I + 7] = pairs[:, 0], pairs[:, 1]
+    x[::2, 9], x[::2, I + 9] = 4, 3
+    x[3::5, 7] = 1.5  # rows without such a gate between the others
+    B.check_act(lib.swiglu_quantize(afmt, x.cuda()), B.swiglu(B.f64(x)), afmt == "e4m3_block")
