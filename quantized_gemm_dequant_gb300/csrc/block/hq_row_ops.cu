@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(WARP || (SRC == SRC_SWIGLU && CH == 2) ? 128 :
   auto second = [&](int64_t r) {
     return SRC == SRC_SWIGLU ? first(r) + chunks : reinterpret_cast<const uint4*>(a.residual + r * a.residual_stride);
   };
-  auto weight = [&](int c) { return c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.weight) + c) : none; };
+  auto weight = [&](int c) { return c < chunks ? reinterpret_cast<const uint4*>(a.weight)[c] : none; };
   auto load = [&](int64_t r) {
     const uint4 *pa = first(r), *pb = TWO ? second(r) : pa;
 #pragma unroll
@@ -313,7 +313,7 @@ struct RowDivide {
 };
 template <bool SWIGLU, int U>
 __global__ void __launch_bounds__(BQ_THREADS)
-    block_quant_kernel(const uint4* __restrict__ x, int64_t n8, RowDivide per_row, uint2* __restrict__ q,
+    block_quant_kernel(const uint4* x, int64_t n8, RowDivide per_row, uint2* __restrict__ q,
                        float* __restrict__ s_out) {
   pdl_trigger();
   pdl_wait();
@@ -326,10 +326,10 @@ __global__ void __launch_bounds__(BQ_THREADS)
     if (i < n8) {
       if (SWIGLU) {  // [gate | up] rows
         const uint4* p = x + i + per_row.of(i) * per_row.d;
-        va[j] = __ldg(p);
-        vb[j] = __ldg(p + per_row.d);
+        va[j] = *p;
+        vb[j] = p[per_row.d];
       } else {
-        va[j] = __ldg(x + i);
+        va[j] = x[i];
       }
     }
   }

@@ -88,7 +88,7 @@ __device__ __forceinline__ uint2 quant8_e4m3(const uint4& w, float s, float si, 
 // read once and kept in registers between the absmax and the quantization (with the CTA's next row in flight);
 // longer rows are read twice (the second read hits L1/L2).
 template <int CH>
-__global__ void __launch_bounds__(AQ_THREADS) act_quant_e4m3_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+__global__ void __launch_bounds__(AQ_THREADS) act_quant_e4m3_kernel(const uint16_t* x, int64_t M, int64_t K,
                                                                     uint8_t* __restrict__ q, float* __restrict__ s_out) {
   __shared__ float red[AQ_THREADS / 32];
   pdl_trigger();
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(AQ_THREADS) act_quant_e4m3_kernel(const uint16
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int64_t c = threadIdx.x + (int64_t)j * AQ_THREADS;
-      dst[j] = c < chunks ? __ldg(xr + c) : make_uint4(0u, 0u, 0u, 0u);
+      dst[j] = c < chunks ? xr[c] : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   if (cached && (int64_t)blockIdx.x < M) load_row(blockIdx.x, v);
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(AQ_THREADS) act_quant_e4m3_kernel(const uint16
 #pragma unroll
       for (int j = 0; j < CH; ++j) mb = bf16x8_absmax_bits(v[j], mb);
     } else {
-      for (int64_t c = threadIdx.x; c < chunks; c += AQ_THREADS) mb = bf16x8_absmax_bits(__ldg(xr + c), mb);
+      for (int64_t c = threadIdx.x; c < chunks; c += AQ_THREADS) mb = bf16x8_absmax_bits(xr[c], mb);
     }
     const float amax = block_max(absmax_bits_to_f32(mb), red);
     const float s = __fdiv_rn(amax, 448.0f);
@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(AQ_THREADS) act_quant_e4m3_kernel(const uint16
       }
     } else {
       for (int64_t c = threadIdx.x; c < chunks; c += AQ_THREADS)
-        qr[c] = s > 0.0f ? quant8_e4m3(__ldg(xr + c), s, si, fast) : make_uint2(0u, 0u);
+        qr[c] = s > 0.0f ? quant8_e4m3(xr[c], s, si, fast) : make_uint2(0u, 0u);
     }
   }
 }
 
 // NVFP4, first pass (only without a calibrated amax): largest magnitude, one partial per CTA.
-__global__ void __launch_bounds__(AQ_THREADS) act_amax_kernel(const uint16_t* __restrict__ x, int64_t n8,
+__global__ void __launch_bounds__(AQ_THREADS) act_amax_kernel(const uint16_t* x, int64_t n8,
                                                               float* __restrict__ partial) {
   __shared__ float red[AQ_THREADS / 32];
   pdl_trigger();
@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(AQ_THREADS) act_amax_kernel(const uint16_t* __
   const int64_t stride = (int64_t)gridDim.x * AQ_THREADS;
   int64_t c = (int64_t)blockIdx.x * AQ_THREADS + threadIdx.x;
   for (; c + 3 * stride < n8; c += 4 * stride) {
-    const uint4 v0 = __ldg(xv + c), v1 = __ldg(xv + c + stride), v2 = __ldg(xv + c + 2 * stride),
-                v3 = __ldg(xv + c + 3 * stride);
+    const uint4 v0 = xv[c], v1 = xv[c + stride], v2 = xv[c + 2 * stride],
+                v3 = xv[c + 3 * stride];
     mb[0] = bf16x8_absmax_bits(v0, mb[0]);
     mb[1] = bf16x8_absmax_bits(v1, mb[1]);
     mb[2] = bf16x8_absmax_bits(v2, mb[2]);
     mb[3] = bf16x8_absmax_bits(v3, mb[3]);
   }
-  for (; c < n8; c += stride) mb[0] = bf16x8_absmax_bits(__ldg(xv + c), mb[0]);
+  for (; c < n8; c += stride) mb[0] = bf16x8_absmax_bits(xv[c], mb[0]);
   const uint32_t all = __vmaxu2(__vmaxu2(mb[0], mb[1]), __vmaxu2(mb[2], mb[3]));
   const float m = block_max(absmax_bits_to_f32(all), red);
   if (threadIdx.x == 0) partial[blockIdx.x] = m;
@@ -188,9 +188,9 @@ __device__ __forceinline__ uint2 quant16_e2m1(const uint4& w0, const uint4& w1, 
 
 // NVFP4 quantization: one 16-element block per thread and step, a persistent grid (the CTAs the SMs hold at once).
 // K % 16 == 0.
-__global__ void __launch_bounds__(AQ_THREADS) act_quant_nvfp4_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
-                                                                     const float* __restrict__ amax_in,
-                                                                     const float* __restrict__ partial, int nparts,
+__global__ void __launch_bounds__(AQ_THREADS) act_quant_nvfp4_kernel(const uint16_t* x, int64_t M, int64_t K,
+                                                                     const float* amax_in,
+                                                                     const float* partial, int nparts,
                                                                      uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                                      float* __restrict__ g_out) {
   __shared__ float red[AQ_THREADS / 32];
@@ -219,14 +219,14 @@ __global__ void __launch_bounds__(AQ_THREADS) act_quant_nvfp4_kernel(const uint1
   int64_t b = (int64_t)blockIdx.x * AQ_THREADS + threadIdx.x;
   uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
   if (b < nblk) {
-    n0 = __ldg(xv + 2 * b);
-    n1 = __ldg(xv + 2 * b + 1);
+    n0 = xv[2 * b];
+    n1 = xv[2 * b + 1];
   }
   for (; b < nblk; b += stride) {
     const uint4 w0 = n0, w1 = n1;
     if (b + stride < nblk) {
-      n0 = __ldg(xv + 2 * (b + stride));
-      n1 = __ldg(xv + 2 * (b + stride) + 1);
+      n0 = xv[2 * (b + stride)];
+      n1 = xv[2 * (b + stride) + 1];
     }
     const float mb = absmax_bits_to_f32(bf16x8_absmax_bits(w1, bf16x8_absmax_bits(w0, 0u)));
     uint32_t sb = 0;

@@ -2,7 +2,9 @@
 //
 // A kernel launched this way may be scheduled while the previous kernel of the stream is still running;
 // every kernel of this library therefore executes pdl_wait() before its first access to global memory that
-// a previous kernel could write (activations, routing tables, workspace, outputs).  Packed weights are
+// a previous kernel could write (activations, routing tables, workspace, outputs), and reads it with ordinary
+// loads: the read-only path (__ldg, const __restrict__ parameters) is for memory that nobody writes from the
+// reading kernel's start on, and neither the compiler nor the cache holds such a load back.  Packed weights are
 // read-only inputs: the dense GEMM kernels start copying them before the wait.  They must therefore be
 // complete when the kernel before the call allows its dependents to launch; kernels that never execute
 // griddepcontrol.launch_dependents (the repack kernel, ordinary kernels) allow it only when they finish.

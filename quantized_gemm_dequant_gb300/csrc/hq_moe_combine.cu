@@ -27,7 +27,7 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float a, float b) {  // lo = a, ro
 }
 
 // C[i] = bf16(acc[i]) for i < n (n % 4 == 0: 16-byte loads, 8-byte stores)
-__global__ void __launch_bounds__(EW_THREADS) combine_round_kernel(const float* __restrict__ acc, int64_t n4,
+__global__ void __launch_bounds__(EW_THREADS) combine_round_kernel(const float* acc, int64_t n4,
                                                                    uint16_t* __restrict__ c) {
   pdl_trigger();
   pdl_wait();  // the sums come from the GEMM (and its split-K reduction)
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(EW_THREADS) combine_round_kernel(const float* 
 }
 
 // out[r, c] = bf16(silu(g) * u), g = x[r, c], u = x[r, I + c]; silu(g) = g / (1 + exp(-g)) in fp32.  I % 8 == 0.
-__global__ void __launch_bounds__(EW_THREADS) swiglu_kernel(const uint16_t* __restrict__ x, int64_t R, int64_t I,
+__global__ void __launch_bounds__(EW_THREADS) swiglu_kernel(const uint16_t* x, int64_t R, int64_t I,
                                                             uint16_t* __restrict__ out) {
   pdl_trigger();
   pdl_wait();

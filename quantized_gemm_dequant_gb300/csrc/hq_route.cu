@@ -16,7 +16,7 @@ namespace hq {
 constexpr int ROUTE_ROWS = 1024;
 constexpr int kErrBadRouting = 6;
 
-__global__ void __launch_bounds__(256) route_kernel(const int32_t* __restrict__ ids, int64_t rows, int E, int cap,
+__global__ void __launch_bounds__(256) route_kernel(const int32_t* ids, int64_t rows, int E, int cap,
                                                     int* __restrict__ counts, int* __restrict__ region,
                                                     int* __restrict__ status) {
   extern __shared__ int sh[];  // hist[E], base[E]
@@ -77,10 +77,10 @@ namespace hq {
 // offsets from the counts (E <= 512); block 0 publishes them in row_off[0..E].
 constexpr int PERMUTE_ROWS = 16;
 
-__global__ void __launch_bounds__(256) moe_permute_kernel(const int* __restrict__ counts, const int* __restrict__ region,
-                                                          int cap, int E, int topk, const uint8_t* __restrict__ src,
+__global__ void __launch_bounds__(256) moe_permute_kernel(const int* counts, const int* region,
+                                                          int cap, int E, int topk, const uint8_t* src,
                                                           int row_bytes, uint8_t* __restrict__ dst,
-                                                          const uint8_t* __restrict__ sf_src, int sf_bytes,
+                                                          const uint8_t* sf_src, int sf_bytes,
                                                           uint8_t* __restrict__ sf_dst, int* __restrict__ row_off) {
   __shared__ int off[513];
   __shared__ int src_row[PERMUTE_ROWS];
