@@ -286,6 +286,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream, make, *a, **k):
+    """A new tensor that belongs to the stream the call runs on, so that its memory is not handed out to another
+    stream's work before the call has finished."""
+    if stream is None:
+        return make(*a, **k)
+    with torch.cuda.stream(stream):
+        return make(*a, **k)
+
+
 def packed_bytes(fmt):
     return int(_lib.hq_packed_bytes(ctypes.byref(fmt)))
 
@@ -300,7 +309,7 @@ def pack_weights(fmt, codes, scales, zeros=None, global_scale=None, out=None, st
     args = _standard(fmt, codes, scales, zeros, global_scale, "hq_pack_weights").add(out, "out", nb)
     p = args.ptrs()
     if out is None:
-        out = torch.empty(nb, dtype=torch.uint8, device=codes.device)
+        out = _on(stream, torch.empty, nb, dtype=torch.uint8, device=codes.device)
         p[4] = _ptr(out)
     _check(_lib.hq_pack_weights(ctypes.byref(fmt), *p, _stream(stream)), "hq_pack_weights")
     return out
@@ -354,7 +363,7 @@ def make_workspace(fmt, rows, topk=1, device="cuda", stream=None):
     nb = workspace_bytes(fmt, rows, topk)
     if nb == 0:
         raise HQError(HQ_ERR_INVALID_ARG, "hq_workspace_bytes")
-    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws = _on(stream, torch.empty, nb, dtype=torch.uint8, device=device)
     _check(_lib.hq_workspace_init(_ptr(ws), nb, _stream(stream)), "hq_workspace_init")
     return ws
 
@@ -396,7 +405,8 @@ def gemm(fmt, act, packed, M, bias=None, out=None, workspace=None, stream=None):
         pd, ps, pg, pw, pb, _, _ = args.ptrs()
         A, d, dev = Act(pd, ps, pg), act["data"], _device()
     if out is None:
-        out = torch.empty((M, N), dtype=_bf16, device=d.device)
+        out = (_empty((M, N), dtype=_bf16, device=d.device) if stream is None else
+               _on(stream, torch.empty, (M, N), dtype=_bf16, device=d.device))
     if workspace is None:
         workspace = make_workspace(fmt, M, 1, d.device, stream)
     st = _lib.hq_gemm(fmt, A, pw, pb, out.data_ptr(), int(M), N, K, workspace.data_ptr(), workspace.nbytes,
@@ -412,7 +422,7 @@ def gemm_static_scratch(fmt, act, packed, M, bias=None, out=None, stream=None):
     args = _Args(w).act(act, fmt, M).add(packed, "packed", packed_bytes(fmt)).add(bias, "bias", 2 * fmt.N, _BF16)
     pd, ps, pg, pw, pb, pc = args.add(out, "out", 2 * M * fmt.N, _BF16).ptrs()
     if out is None:
-        out = torch.empty((M, fmt.N), dtype=torch.bfloat16, device=act["data"].device)
+        out = _on(stream, torch.empty, (M, fmt.N), dtype=torch.bfloat16, device=act["data"].device)
         pc = _ptr(out)
     A = Act(pd, ps, pg)
     _check(_lib.hq_gemm_static_scratch(ctypes.byref(fmt), ctypes.byref(A), pw, pb, pc, int(M), fmt.N, fmt.K,
@@ -440,7 +450,7 @@ def moe_gemm(fmt, act, packed, topk_ids, topk_weights=None, out=None, workspace=
     pid, ptw, pd, ps, pg, pw, pc, pws = args.ptrs()
     dev = act["data"].device
     if out is None:
-        out = torch.empty((T * k, fmt.N), dtype=torch.bfloat16, device=dev)
+        out = _on(stream, torch.empty, (T * k, fmt.N), dtype=torch.bfloat16, device=dev)
         pc = _ptr(out)
     if workspace is None:
         workspace = make_workspace(fmt, T, k, dev, stream)
@@ -456,7 +466,7 @@ def make_combine_workspace(fmt, T, topk, device="cuda", stream=None):
     nb = int(_lib.hq_moe_combine_workspace_bytes(ctypes.byref(fmt), int(T), int(topk)))
     if nb == 0:
         raise HQError(HQ_ERR_INVALID_ARG, "hq_moe_combine_workspace_bytes")
-    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws = _on(stream, torch.empty, nb, dtype=torch.uint8, device=device)
     _check(_lib.hq_workspace_init(_ptr(ws), nb, _stream(stream)), "hq_workspace_init")
     return ws
 
@@ -469,7 +479,7 @@ def moe_gemm_combine(fmt, act, packed, topk_ids, topk_weights=None, out=None, wo
     pid, ptw, pd, ps, pg, pw, pc, pws = args.ptrs()
     dev = act["data"].device
     if out is None:
-        out = torch.empty((T, fmt.N), dtype=torch.bfloat16, device=dev)
+        out = _on(stream, torch.empty, (T, fmt.N), dtype=torch.bfloat16, device=dev)
         pc = _ptr(out)
     if workspace is None:
         workspace = make_combine_workspace(fmt, T, k, dev, stream)
@@ -488,7 +498,7 @@ def swiglu(x, out=None, stream=None):
     R, I2 = x.shape
     px, po = _Args(w).add(x, "x", 2 * R * I2, _BF16).add(out, "out", R * I2, _BF16).ptrs()
     if out is None:
-        out = torch.empty((R, I2 // 2), dtype=torch.bfloat16, device=x.device)
+        out = _on(stream, torch.empty, (R, I2 // 2), dtype=torch.bfloat16, device=x.device)
         po = _ptr(out)
     _check(_lib.hq_swiglu(px, int(R), int(I2 // 2), po, _stream(stream)), w)
     return out
@@ -548,22 +558,14 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
     p = args.ptrs()
     dev = x.device
     if out is None:
-        if afmt == "e4m3_block":
-            out = _new_act(at, M, K, dev, stream)
-        elif afmt == "e4m3_tok":
-            out = dict(data=torch.empty((M, K), dtype=torch.uint8, device=dev),
-                       scale=torch.empty((M,), dtype=torch.float32, device=dev))
-        else:
-            out = dict(data=torch.empty((M, K // 2), dtype=torch.uint8, device=dev),
-                       scale=torch.empty((M, K // 16), dtype=torch.uint8, device=dev),
-                       gscale=torch.empty((1,), dtype=torch.float32, device=dev))
+        out = _new_act(at, M, K, dev, stream)
         pd, ps, pg = _ptr(out["data"]), _ptr(out["scale"]), _ptr(out.get("gscale"))
     else:
         pd, ps, pg = p[2:5]
     pws = p[-1]
     need = quantize_act_workspace_bytes(afmt, M, K)
     if workspace is None and need > 0 and global_amax is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _on(stream, torch.empty, need, dtype=torch.uint8, device=dev)
         pws = _ptr(workspace)
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     _check(_lib.hq_quantize_act(at, p[0], M, K, p[1], pd, ps, pg, pws, ws_bytes, _stream(stream)), w)
@@ -571,12 +573,17 @@ def quantize_act(afmt, x, global_amax=None, out=None, workspace=None, stream=Non
 
 
 def _new_act(at, rows, width, device, stream=None):
-    """An activation operand that a call fills: bf16 rows, or e4m3 codes with a scale per row or per 128 elements."""
+    """An activation operand that a call fills: bf16 rows, e4m3 codes with a scale per row or per 128 elements, or
+    packed e2m1 codes with a ue4m3 scale per 16 elements and a global scale."""
     if stream is not None:
         with torch.cuda.stream(stream):  # the new tensors belong to the stream the call runs on
             return _new_act(at, rows, width, device)
     if at == HQ_A_BF16:
         return {"data": _empty((rows, width), dtype=_bf16, device=device)}
+    if at == HQ_A_NVFP4:
+        return {"data": _empty((rows, width // 2), dtype=_u8, device=device),
+                "scale": _empty((rows, width // 16), dtype=_u8, device=device),
+                "gscale": _empty((1,), dtype=_f32, device=device)}
     return {"data": _empty((rows, width), dtype=_u8, device=device),
             "scale": _empty((rows, width // 128) if at == HQ_A_E4M3_BLOCK else rows, dtype=_f32, device=device)}
 
@@ -769,15 +776,6 @@ def make_kv_workspace(cache, batch=0, num_q_heads=0, stream=None):
     ws = _on(stream, torch.empty, nb, dtype=torch.uint8, device=cache.device)
     _check(_lib.hq_workspace_init(_ptr(ws), nb, _stream(stream)), "hq_workspace_init")
     return ws
-
-
-def _on(stream, make, *a, **k):
-    """A new tensor that belongs to the stream the call runs on, so that its memory is not handed out to another
-    stream's work before the call has finished."""
-    if stream is None:
-        return make(*a, **k)
-    with torch.cuda.stream(stream):
-        return make(*a, **k)
 
 
 # A decoding step makes these calls for every layer, so a call whose tensors are right looks at each of them once, in
