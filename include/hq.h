@@ -151,6 +151,7 @@ HQ_API size_t hq_packed_bytes(const hq_format_t* fmt);
  *                of the row, position p being bit p % 8 of byte p / 8)
  *   scales       [E][N][K/group] of scale_type (bf16 as 16-bit patterns, ue4m3/e8m0 bytes); F32: fp32
  *                [ceil(N/128)][K/128], one per 128 x 128 block
+ *                (HQ_ERR_ALIGNMENT for scales that are not aligned to their own type)
  *   zeros        uint8 [E][N][K/group], values 0..2^b - 1 for the b-bit zero-point formats
  *                (UINT4_ZP, UINT3_ZP, UINT2_ZP, UINT1_ZP), else NULL
  *   global_scale fp32 [E] (NVFP4), else NULL

@@ -47,6 +47,12 @@ constexpr size_t kHeaderBytes = 256;  // [0] device status, [1] epoch of the las
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Standard-format scales and global scales, aligned to their own type (bytes need nothing).
+bool aligned_scales(const hq_format_t* f, const void* scales, const void* global_scale) {
+  const uintptr_t mask = f->scale_type == HQ_S_F32 ? 3u : (f->scale_type == HQ_S_BF16 ? 1u : 0u);
+  return (reinterpret_cast<uintptr_t>(scales) & mask) == 0 &&
+         (!f->has_global_scale || (reinterpret_cast<uintptr_t>(global_scale) & 3u) == 0);
+}
 
 // Validate the descriptor against the supported combinations.
 hq_status_t check_format(const hq_format_t* f) {
@@ -480,7 +486,7 @@ hq_status_t hq_pack_weights(const hq_format_t* fmt, const uint8_t* codes, const 
   if (!codes || !scales || !packed) return HQ_ERR_INVALID_ARG;
   if (fmt->has_zero && !zeros) return HQ_ERR_INVALID_ARG;
   if (fmt->has_global_scale && !global_scale) return HQ_ERR_INVALID_ARG;
-  if (!aligned16(packed)) return HQ_ERR_ALIGNMENT;
+  if (!aligned16(packed) || !aligned_scales(fmt, scales, global_scale)) return HQ_ERR_ALIGNMENT;
   return cuda_status(launch_pack(0, pack_kind(fmt), fmt->N, fmt->K, fmt->num_experts, codes, scales, zeros,
                                  global_scale, packed, (cudaStream_t)stream));
 }
@@ -491,7 +497,7 @@ hq_status_t hq_unpack_weights(const hq_format_t* fmt, const void* packed, uint8_
   if (st != HQ_OK) return st;
   if (!codes || !scales || !packed) return HQ_ERR_INVALID_ARG;
   if (fmt->has_zero && !zeros) return HQ_ERR_INVALID_ARG;
-  if (!aligned16(packed)) return HQ_ERR_ALIGNMENT;
+  if (!aligned16(packed) || !aligned_scales(fmt, scales, global_scale)) return HQ_ERR_ALIGNMENT;
   return cuda_status(launch_pack(1, pack_kind(fmt), fmt->N, fmt->K, fmt->num_experts, codes, scales, zeros,
                                  global_scale, const_cast<void*>(packed), (cudaStream_t)stream));
 }
