@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -768,7 +769,7 @@ hq_status_t hq_add_rms_norm(const hq_norm_t* n, hq_stream_t stream) {
     case HQ_A_E4M3_BLOCK: out = ROW_BLOCK, unit = 128; break;
     default: return HQ_ERR_UNSUPPORTED;
   }
-  if (n->T < 0 || n->T > kMaxRows || n->K < unit || n->K > kMaxRows || !(n->eps >= 0.0f) || n->eps > 3.4e38f)
+  if (n->T < 0 || n->T > kMaxRows || n->K < unit || n->K > kMaxRows || !(n->eps >= 0.0f) || n->eps > FLT_MAX)
     return HQ_ERR_INVALID_ARG;
   if (n->K % unit) return HQ_ERR_ALIGNMENT;
   if (n->K > ROW_MAX) return HQ_ERR_UNSUPPORTED;

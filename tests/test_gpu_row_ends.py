@@ -68,3 +68,17 @@ def test_swiglu_gates_far_below_zero(lib, afmt, copies, I):
     x[::2, 9], x[::2, I + 9] = 4, 3
     x[3::5, 7] = 1.5  # rows without such a gate between the others
     B.check_act(lib.swiglu_quantize(afmt, x.cuda()), B.swiglu(B.f64(x)), afmt == "e4m3_block")
+
+
+@pytest.mark.parametrize("afmt", FORMATS)
+def test_norm_with_the_largest_eps(lib, afmt):
+    """fp32's largest eps, with means that change the sum, that take it past fp32, that do not count, and of zero."""
+    eps = float(np.finfo(np.float32).max)
+    x = torch.tensor([[1e19], [6e18], [1e12], [1.0], [0.0]]) * torch.tensor([1.0, -2.0] * 64)
+    x, w = x.to(torch.bfloat16), torch.linspace(0.5, 1.5, 128).to(torch.bfloat16)
+    act, _ = lib.add_rms_norm(afmt, x.cuda(), w.cuda(), eps=eps)
+    want = B.norm(B.f64(x), B.f64(w)[None], eps)
+    if afmt == "bf16":
+        B.check_bf16(act["data"], want)
+    else:
+        B.check_act(act, want, afmt == "e4m3_block", rows_of_zeros=(4,))
