@@ -183,8 +183,10 @@ HQ_API int32_t hq_kernels_per_call(const hq_format_t* fmt, int64_t M_or_T, int32
 
 /* The launch plan of such a call on the current device (built-in rule, tuned table, HQ_TUNE): writes
  * plan_out[0] = GEMM kernel (0 tcgen05, 1 register-decode), plan_out[1] = its variant (tcgen05: 0 INT4, 1 NVFP4,
- * 2 MXFP4 x FP8, 3 MXFP4 x MXFP8, 4 MXFP4 x MXFP4; register-decode: the decode kind, 0 INT4 ... 6 UINT3),
- * plan_out[2] = token tile, plan_out[3] = 1 if K is split over CTAs (Stream-K), plan_out[4] = CTAs launched,
+ * 2 MXFP4 x FP8, 3 MXFP4 x MXFP8, 4 MXFP4 x MXFP4, E4M3 with block scales: 5 tiles of up to 128 tokens by 128
+ * features, 6 CTA pairs with 256 tokens by 128 features, 7 by 256; register-decode: the decode kind, 0 INT4 ... 6
+ * UINT3), plan_out[2] = token tile, plan_out[3] = 1 if K is split over CTAs (Stream-K; block scales: over a cluster's),
+ * plan_out[4] = CTAs launched,
  * plan_out[5] = 1 if MoE rows are copied expert-contiguous first.  moe: 0 hq_gemm, 1 hq_moe_gemm, 2
  * hq_moe_gemm_combine (each kind has its own rows in the tuned table).  Returns HQ_ERR_INVALID_ARG for an invalid
  * format, size, kind or null plan_out.  Host-only ("Tuning and JIT compilation per workload": the per-size choice). */

@@ -529,7 +529,7 @@ hq_status_t hq_launch_plan(const hq_format_t* fmt, int64_t M_or_T, int32_t topk,
   if (block_scaled(fmt) && moe) return HQ_ERR_UNSUPPORTED;
   const Plan p = make_plan(fmt, M_or_T, topk, moe, num_sms());
   plan_out[0] = p.small;
-  plan_out[1] = p.small ? p.dec : p.path;
+  plan_out[1] = p.small ? p.dec : (p.pair ? (p.pair == 256 ? 7 : 6) : p.path);
   plan_out[2] = p.bt;
   plan_out[3] = p.path == PATH_E4M3B ? p.sk > 1 : p.sk;
   plan_out[4] = p.grid;
