@@ -82,3 +82,16 @@ def test_norm_with_the_largest_eps(lib, afmt):
         B.check_bf16(act["data"], want)
     else:
         B.check_act(act, want, afmt == "e4m3_block", rows_of_zeros=(4,))
+
+
+@pytest.mark.parametrize("T,K", [(3, 4096), (500, 1024), (3000, 512), (700, 7168), (3, 32768)])
+def test_two_calls_give_the_same_bits(lib, T, K):
+    g = torch.Generator().manual_seed(T)
+    x, r = (torch.randn(T, K, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w = torch.randn(K, generator=g).to(torch.bfloat16).cuda()
+    for afmt in FORMATS:
+        a, b = (lib.add_rms_norm(afmt, x, w, residual=r) for _ in range(2))
+        assert torch.equal(a[1], b[1]) and all(torch.equal(a[0][k], b[0][k]) for k in a[0])
+    for afmt in ("e4m3_tok", "e4m3_block"):
+        a, b = (lib.swiglu_quantize(afmt, x) for _ in range(2))
+        assert all(torch.equal(a[k], b[k]) for k in a)
