@@ -208,8 +208,9 @@ HQ_API hq_status_t hq_workspace_init(void* workspace, size_t bytes, hq_stream_t 
  * fp32; C is rounded to nearest-even bf16.
  * E4M3 weights with F32 scales: C[m, n] = bias[n] + sum_b s(A)[m, b] * s(W)[n / 128, b] * sum_{k in block b} A[m, k] *
  * W[n, k]; every 128-K block is summed by itself and added, times its scale s(A) * s(W) (rounded to fp32, so that it
- * should lie in fp32's normal range), in fp32, in an order that does not depend on timing.  The
- * workspace holds the status header alone; A's scales and C are 16-byte aligned. */
+ * should lie in fp32's normal range), in fp32, in an order that does not depend on timing: two calls give the same bits.
+ * It goes by M, N and K, which decide how K is split, so that a row's last bits may differ between calls of other M.
+ * The workspace holds the status header alone; A's scales and C are 16-byte aligned. */
 HQ_API hq_status_t hq_gemm(const hq_format_t* fmt, const hq_act_t* A, const void* packedW, const void* bias, void* C,
                     int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes, hq_stream_t stream);
 
@@ -262,7 +263,7 @@ HQ_API hq_status_t hq_swiglu(const void* x, int64_t R, int64_t I, void* out, hq_
  * [R]) or of each 128 of its elements (HQ_A_E4M3_BLOCK: out_scale fp32 [R, I/128]) and out_data = e4m3(y / scale),
  * nearest even, [R, I].  A scale of zero has zero codes; a NaN or an infinity makes its scale NaN or infinite.
  * I is a multiple of 16 and at most 32768 (TOKEN; HQ_ERR_UNSUPPORTED above) or a multiple of 128 (BLOCK); pointers
- * 16-byte aligned.  R = 0 does nothing.  One kernel. */
+ * 16-byte aligned, outputs must not overlap x.  R = 0 does nothing.  One kernel. */
 HQ_API hq_status_t hq_swiglu_quantize(int32_t act_type, const void* x, int64_t R, int64_t I, void* out_data,
                                       void* out_scale, hq_stream_t stream);
 

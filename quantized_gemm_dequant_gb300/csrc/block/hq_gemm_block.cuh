@@ -76,8 +76,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 
 // ------------------------------------------------------------------ clusters
 // The lanes of a warp leave a wait, or a branch of one lane, one by one; barriers and tensor-memory instructions are the
-// whole warp's.  A __syncwarp() therefore stands between every such wait or branch and the next of those: a warp that
-// comes to them in parts is undefined behaviour.
+// whole warp's.  Between every such wait or branch and the next of those stands a __syncwarp(), or the wait is one that
+// the lanes leave together (mbar_wait_warp's votes): a warp that comes to them in parts is undefined behaviour.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(BLK_THREADS, BlkCfg<BT>::PER_SM)
 //
 // A K block of a 256 x 256 tile keeps the tensor pipe busy for 650 cycles, and the promotion of its 128 x 256 sums per
 // CTA by eight warps takes 256 cycles of the FMA pipes and as many of tensor-memory reads, under the next block's MMAs.
-// Measured: 8192 tokens, 14336 x 4096, 370 us = 2.6 PFLOP/s (355 to 400 from run to run: a long call draws the card's
+// Measured: 8192 tokens, 14336 x 4096, 385 us = 2.5 PFLOP/s (355 to 400 from run to run: a long call draws the card's
 // full power); one wave of tiles, 2048 x 2048 x 16384, 55 us = 820 cycles a K block.  With the additions left out that
 // takes 45 us, at the MMA's pace; with a quarter of the MMAs and neither reads nor additions 41, which is what copies,
 // barriers and hand-overs between the CTAs cost by themselves.  What is left over the MMA is the circle of a slot: filled,
@@ -434,8 +434,8 @@ struct PairCfg {
 };
 // warps 0-7 promote, 8 loads, 9 and 10 issue the MMAs (of the cluster's first CTA), 11 multiplies the scales
 constexpr int PAIR_THREADS = 384;
-// registers: 168 x 384 at launch; the promoting warps raise theirs to 216, the others go down to 72, and 2 x 216 + 72 =
-// 3 x 168
+// registers: 168 x 384 at launch (the 256-feature kernel spills 24 bytes of them); the promoting warps raise theirs to 216,
+// the others go down to 72, and 2 x 216 + 72 = 3 x 168
 constexpr int PAIR_TOKENS = 256;
 constexpr int PAIR_GROUP = 8;  // token tiles per round of feature tiles: the tiles in flight share operands in L2
 
@@ -505,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PAIR_THREADS, 1)
   static_assert(sizeof(PairSmem<BN>) <= 512, "shared state");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);  // [SGROUPS][4][TILES][128]
+  float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);  // [SGROUPS][SK][TILES][128]
   PairSmem<BN>& sh = *reinterpret_cast<PairSmem<BN>*>(smem + C::STAGES * C::STAGE + C::SCALES + C::OUT);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler sees it

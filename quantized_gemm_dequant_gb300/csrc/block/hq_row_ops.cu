@@ -6,10 +6,10 @@
 // y is never rounded on the way: fp32 until its code.
 //
 // All of them are bound by memory: a row is read once and stays in registers between its statistics and its codes.
-// Measured, inputs past L2: norm of 8192 x 7168 with a residual 62.8 us with a scale per row (6550 GB/s, 97% of copy
-// bandwidth), 66.9 us with one per 128 (6150 GB/s), 75.0 us to bf16 (6270 GB/s); rows as they are 28.7 us (6140 GB/s).
-// SwiGLU of 8192 x 7168 53.5 us (5480 GB/s) and of 32768 x 768 24.9 us (5050 GB/s): issue slots are two thirds full
-// there (190 instructions for 8 outputs a lane, 18 of them powers and reciprocals).
+// Measured, inputs past L2: norm of 8192 x 7168 with a residual 62.2 us with a scale per row (6610 GB/s, 97% of copy
+// bandwidth), 66.2 us with one per 128 (6240 GB/s), 74.8 us to bf16 (6280 GB/s); rows as they are 28.0 us (6360 GB/s).
+// SwiGLU of 8192 x 7168 with a scale per 128 50.4 us (5860 GB/s) and of 32768 x 768 with one per row 24.6 us (5120 GB/s):
+// issue slots are two thirds full there (190 instructions for 8 outputs a lane, 18 of them powers and reciprocals).
 #include <cuda_runtime.h>
 #include <float.h>
 #include <stdint.h>
@@ -148,7 +148,9 @@ __device__ __noinline__ void swiglu_rows_again(const uint16_t* rows_in, int64_t 
 
 // One row per CTA, or per warp (WARP, four rows a CTA), CH chunks of 8 elements per thread; the next row of the same
 // threads is loaded while the current one is reduced and written.  LONG: rows past 2048 chunks on 1024 threads, whose
-// registers leave no room for that, nor for the norm's weights.
+// registers leave no room for that, nor for the norm's weights, which every row reads again (from L2): 2048 x 32768 with a
+// residual 81.4 us with a scale per row (5770 GB/s), 85.9 with one per 128, 86.1 to bf16 (6240 GB/s); SwiGLU 67.8 us
+// (4950 GB/s).  Four of the seven instances spill 4 to 36 bytes.
 template <int SRC, int OUT, int CH, bool WARP, bool LONG>
 __global__ void __launch_bounds__(WARP || (SRC == SRC_SWIGLU && CH == 2) ? 128 : (CH == 1 || LONG ? 1024 : 512),
                                   SRC == SRC_SWIGLU && CH == 2 ? 9 : 0) row_kernel(const RowArgs a) {
@@ -437,7 +439,8 @@ cudaError_t launch_block_quant(bool swiglu, const void* x, int64_t rows, int64_t
                                cudaStream_t stream) {
   const int64_t n8 = rows * (width >> 3);
   // One chunk a thread where that leaves no SM more than two CTAs (16 x 7168 SwiGLU: 2.4 -> 2.05 us), else two of the
-  // SwiGLU (four: 53.5 -> 55 us at 8192 x 7168) and four of plain rows (two: 28.7 -> 30.4 us at 8192 x 7168).
+  // SwiGLU (four: 5.6 -> 6.4 us at 512 x 7168, though 50.5 -> 48.1 at 8192 x 7168) and four of plain rows (two: 28.0 ->
+  // 29.5 us at 8192 x 7168).
   const int unroll = n8 <= (int64_t)2 * sms() * BQ_THREADS ? 1 : (swiglu ? 2 : 4);
   const int64_t grid = (n8 + BQ_THREADS * unroll - 1) / (BQ_THREADS * unroll);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
